@@ -3,6 +3,7 @@
  *
  * The library implements the data-parallel hot path of paged KV caching:
  *   pa_reshape_and_cache  write new tokens' K/V into pool slots,
+ *   pa_gather_cache       read cached rows back as values,
  *   pa_copy_blocks        copy-on-write of shared blocks (one layer, or
  *                         all layers: pa_copy_blocks_layers),
  *   pa_swap_blocks        block copies between a device and a host pool,
@@ -40,6 +41,17 @@
  * num_q_heads a multiple of num_kv_heads; num_kv_heads <= 256.
  * Element types: f32 caches need f32 q; f16/bf16 caches need q of the same
  * type; fp8 caches (e4m3 or e5m2) take f16 or bf16 q (head_dim 128 only).
+ *
+ * 4-bit caches (PA_INT4): a row -- one token's head_dim values of one KV head
+ * -- is held as 4-bit codes c in 0..15 and two f16 numbers (step, low), with
+ *   low = f16(min x),  step = f16((max x - low) / 15),
+ *   c = (x - low) / step rounded to nearest even and limited to 0..15,
+ *   and read as low + step * c;
+ * x is limited to +-65504 first, a row of equal values has step 0, and a row
+ * that holds a NaN reads as NaN throughout.  A block of a K (or V) pool is
+ * block_size * num_kv_heads * (head_dim / 2 + 4) bytes: codes [num_kv_heads,
+ * block_size, head_dim / 2], dimension 2b in the low nibble of byte b, then
+ * (step, low) [num_kv_heads, block_size, 2].  k_scale and v_scale are ignored.
  */
 #ifndef PA_H
 #define PA_H
@@ -65,7 +77,8 @@ typedef enum {
     PA_F16 = 1,
     PA_BF16 = 2,
     PA_FP8_E4M3 = 3,          /* OCP E4M3 (finite-only, max 448), one byte */
-    PA_FP8_E5M2 = 4           /* OCP E5M2 (IEEE-like inf/NaN, max 57344), one byte */
+    PA_FP8_E5M2 = 4,          /* OCP E5M2 (IEEE-like inf/NaN, max 57344), one byte */
+    PA_INT4 = 5               /* 4-bit codes with a (step, low) pair per row; a cache type only */
 } pa_dtype;
 
 /* Bits OR-ed into *err_flag by device code. */
@@ -198,6 +211,8 @@ pa_status pa_decode_noalloc(void* out, const void* q, pa_dtype q_dtype,
  * with x the source value widened to float, IEEE float division, round to
  * nearest even, saturation to +-448; NaN becomes the NaN code.  Sources for
  * an fp8 cache may be f32, f16 or bf16; other caches need src == kv dtype.
+ * A 4-bit cache quantises each row on write (head of this file) from f32, f16
+ * or bf16; it needs head_dim 64 or 128 and a block_size of a multiple of 8.
  * Duplicate slots within one call leave one of the writes (unspecified which).
  */
 pa_status pa_reshape_and_cache(void* k_cache, void* v_cache, pa_dtype kv_dtype,
@@ -206,6 +221,27 @@ pa_status pa_reshape_and_cache(void* k_cache, void* v_cache, pa_dtype kv_dtype,
                                int num_kv_heads, int head_dim, int block_size,
                                int num_blocks, float k_scale, float v_scale,
                                int32_t* err_flag, cudaStream_t stream);
+
+/*
+ * pa_gather_cache -- the inverse of pa_reshape_and_cache: row t of key and
+ * value ([num_kv_heads, head_dim] each) becomes the K and V row of pool slot
+ * slot_mapping[t], as values of dst_dtype (a cached prefix handed to a kernel
+ * that wants contiguous K and V).
+ *   slot < 0                          the row is left as it was, no error.
+ *   slot >= num_blocks*block_size     the same, and PA_ERRBIT_BAD_SLOT.
+ * f32, f16 and bf16 caches need dst_dtype == kv_dtype and move bits; fp8
+ * caches (code times k_scale or v_scale) and 4-bit caches (low + step * c)
+ * give f32, f16 or bf16, computed in f32 and rounded to nearest even.  The
+ * same slot may appear more than once.  head_dim 64 or 128.
+ */
+pa_status pa_gather_cache(void* key, void* value, pa_dtype dst_dtype,
+                          const void* k_cache, const void* v_cache, pa_dtype kv_dtype,
+                          const int64_t* slot_mapping, int num_tokens, int num_kv_heads,
+                          int head_dim, int block_size, int num_blocks, float k_scale,
+                          float v_scale, int32_t* err_flag, cudaStream_t stream);
+
+/* Bytes of one K (or V) block of a pool, 0 for invalid arguments. */
+size_t pa_block_bytes(pa_dtype kv_dtype, int num_kv_heads, int head_dim, int block_size);
 
 /*
  * pa_copy_blocks -- copy-on-write block copies ("vLLM intro part 2",

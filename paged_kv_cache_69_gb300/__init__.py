@@ -18,7 +18,7 @@ import torch
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libpa.so")
 
-PA_F32, PA_F16, PA_BF16, PA_FP8_E4M3, PA_FP8_E5M2 = 0, 1, 2, 3, 4
+PA_F32, PA_F16, PA_BF16, PA_FP8_E4M3, PA_FP8_E5M2, PA_INT4 = 0, 1, 2, 3, 4, 5
 PA_OK = 0
 ERRBIT_BAD_BLOCK, ERRBIT_BAD_SLOT, ERRBIT_BAD_PAIR, ERRBIT_SEQ_TOO_LONG, ERRBIT_WAIT_TIMEOUT = 1, 2, 4, 8, 16
 ERRBIT_BAD_QUERY = 32
@@ -26,12 +26,13 @@ ERRBIT_BAD_QUERY = 32
 # entry points declared in include/pa.h
 EXPORTED = ("pa_status_string", "pa_last_error_detail", "pa_decode_workspace_size", "pa_decode",
             "pa_decode_simt", "pa_decode_noalloc", "pa_reshape_and_cache", "pa_copy_blocks",
-            "pa_copy_blocks_layers", "pa_swap_blocks", "pa_attention", "pa_attention_workspace_size")
+            "pa_copy_blocks_layers", "pa_swap_blocks", "pa_attention", "pa_attention_workspace_size",
+            "pa_gather_cache", "pa_block_bytes")
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
 _DTYPE_CODE = {torch.float32: PA_F32, torch.float16: PA_F16, torch.bfloat16: PA_BF16,
                torch.uint8: PA_FP8_E4M3, torch.float8_e4m3fn: PA_FP8_E4M3, torch.float8_e5m2: PA_FP8_E5M2}
-_NAME_CODE = {"f32": PA_F32, "f16": PA_F16, "bf16": PA_BF16, "fp8_e4m3": PA_FP8_E4M3, "fp8_e5m2": PA_FP8_E5M2}
+_NAME_CODE = {"f32": PA_F32, "f16": PA_F16, "bf16": PA_BF16, "fp8_e4m3": PA_FP8_E4M3, "fp8_e5m2": PA_FP8_E5M2, "int4": PA_INT4}
 
 
 class PaError(RuntimeError):
@@ -67,6 +68,11 @@ def _configure(L):
     L.pa_reshape_and_cache.restype = c_int
     L.pa_reshape_and_cache.argtypes = [vp, vp, c_int, vp, vp, c_int, vp, c_int, c_int, c_int, c_int,
                                        c_int, c_float, c_float, vp, vp]
+    L.pa_gather_cache.restype = c_int
+    L.pa_gather_cache.argtypes = [vp, vp, c_int, vp, vp, c_int, vp, c_int, c_int, c_int, c_int, c_int, c_float,
+                                  c_float, vp, vp]
+    L.pa_block_bytes.restype = sz
+    L.pa_block_bytes.argtypes = [c_int, c_int, c_int, c_int]
     L.pa_copy_blocks.restype = c_int
     L.pa_copy_blocks.argtypes = [vp, vp, c_int, vp, c_int, c_int, c_int, c_int, c_int, vp, vp]
     L.pa_copy_blocks_layers.restype = c_int
@@ -117,6 +123,10 @@ def _code(t: torch.Tensor, override=None) -> int:
     return _DTYPE_CODE[t.dtype]
 
 
+def _is_int4(kv_dtype) -> bool:
+    return kv_dtype == "int4" or (isinstance(kv_dtype, int) and kv_dtype == PA_INT4)
+
+
 def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
         stream = torch.cuda.current_stream()
@@ -131,11 +141,16 @@ def _dev(*ts):
             raise ValueError("libpa expects contiguous tensors")
 
 
-def _pools(k: torch.Tensor, v: torch.Tensor):
-    """K and V pools of one shape and element type; returns (NB, bs, Hkv, D)."""
+def _pools(k: torch.Tensor, v: torch.Tensor, kv_dtype=None):
+    """K and V pools of one shape and element type; returns (NB, bs, Hkv, D).
+    A 4-bit pool is uint8 with head_dim / 2 + 4 bytes per row."""
     if k.dim() != 4 or tuple(v.shape) != tuple(k.shape) or v.dtype != k.dtype:
         raise ValueError("k_cache and v_cache must be [num_blocks, block_size, num_kv_heads, head_dim] "
                          "of one shape and dtype")
+    if _is_int4(kv_dtype):
+        if k.dtype != torch.uint8 or k.shape[3] <= 4:
+            raise ValueError("4-bit pools must be uint8 [num_blocks, block_size, num_kv_heads, head_dim / 2 + 4]")
+        return tuple(k.shape[:3]) + (2 * (k.shape[3] - 4),)
     return tuple(k.shape)
 
 
@@ -164,6 +179,16 @@ def alloc_workspace(num_seqs: int, num_q_heads: int, max_seq_len: int, head_dim:
     if n == 0:
         raise PaError(1, "invalid workspace bounds")
     return torch.empty(n, dtype=torch.uint8, device=device or "cuda")   # torch allocations are 256-B aligned
+
+
+def alloc_int4_cache(num_blocks: int, block_size: int, num_kv_heads: int, head_dim: int, device=None) -> torch.Tensor:
+    """A zeroed 4-bit K (or V) pool, uint8 [num_blocks, block_size,
+    num_kv_heads, head_dim / 2 + 4]; kv_dtype="int4" in the calls.  Inside a
+    block the codes of all rows come first, then their (step, low) pairs."""
+    if head_dim not in (64, 128) or block_size % 8 or min(num_blocks, block_size, num_kv_heads) <= 0:
+        raise ValueError("a 4-bit pool needs head_dim 64 or 128 and a block_size of a multiple of 8")
+    return torch.zeros(num_blocks, block_size, num_kv_heads, head_dim // 2 + 4, dtype=torch.uint8,
+                       device=device or "cuda")
 
 
 def pa_decode(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -222,7 +247,7 @@ def pa_reshape_and_cache(k_cache: torch.Tensor, v_cache: torch.Tensor, key: torc
                          err_flag: Optional[torch.Tensor] = None, stream=None) -> None:
     """Write key/value [T, Hkv, D] into pool slots slot_mapping (int64 [T])."""
     _dev(k_cache, v_cache, key, value, slot_mapping, err_flag)
-    NB, bs, Hkv, D = _pools(k_cache, v_cache)
+    NB, bs, Hkv, D = _pools(k_cache, v_cache, kv_dtype)
     T = key.shape[0]
     if tuple(key.shape) != (T, Hkv, D) or tuple(value.shape) != (T, Hkv, D) or value.dtype != key.dtype:
         raise ValueError("key/value must be [num_tokens, num_kv_heads, head_dim] of one dtype")
@@ -234,11 +259,29 @@ def pa_reshape_and_cache(k_cache: torch.Tensor, v_cache: torch.Tensor, key: torc
                                       float(k_scale), float(v_scale), _ptr(err_flag), _stream(stream)))
 
 
+def pa_gather_cache(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    slot_mapping: torch.Tensor, kv_dtype=None, *, k_scale: float = 1.0, v_scale: float = 1.0,
+                    err_flag: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Read pool slots slot_mapping (int64 [T]) back into key/value
+    [T, Hkv, D]: bits of f32/f16/bf16 pools, values of fp8 and 4-bit pools."""
+    _dev(key, value, k_cache, v_cache, slot_mapping, err_flag)
+    NB, bs, Hkv, D = _pools(k_cache, v_cache, kv_dtype)
+    T = key.shape[0]
+    if tuple(key.shape) != (T, Hkv, D) or tuple(value.shape) != (T, Hkv, D) or value.dtype != key.dtype:
+        raise ValueError("key/value must be [num_tokens, num_kv_heads, head_dim] of one dtype")
+    _flag(err_flag)
+    if slot_mapping.dtype != torch.int64 or slot_mapping.numel() != T:
+        raise ValueError("slot_mapping must be int64 [num_tokens]")
+    _check(lib().pa_gather_cache(_ptr(key), _ptr(value), _code(key), _ptr(k_cache), _ptr(v_cache),
+                                 _code(k_cache, kv_dtype), _ptr(slot_mapping), T, Hkv, D, bs, NB, float(k_scale),
+                                 float(v_scale), _ptr(err_flag), _stream(stream)))
+
+
 def pa_copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor, block_mapping: torch.Tensor,
                    kv_dtype=None, *, err_flag: Optional[torch.Tensor] = None, stream=None) -> None:
     """Copy whole blocks src -> dst for each row (src, dst) of block_mapping (int64 [P, 2])."""
     _dev(k_cache, v_cache, block_mapping, err_flag)
-    NB, bs, Hkv, D = _pools(k_cache, v_cache)
+    NB, bs, Hkv, D = _pools(k_cache, v_cache, kv_dtype)
     _flag(err_flag)
     if block_mapping.dtype != torch.int64 or (block_mapping.numel() and block_mapping.shape[-1] != 2):
         raise ValueError("block_mapping must be int64 [num_pairs, 2]")
@@ -253,10 +296,10 @@ def pa_copy_blocks_layers(k_caches, v_caches, block_mapping: torch.Tensor, kv_dt
     if len(k_caches) != len(v_caches) or not k_caches:
         raise ValueError("k_caches and v_caches must be equal-length non-empty lists")
     _dev(*k_caches, *v_caches, block_mapping, err_flag)
-    NB, bs, Hkv, D = _pools(k_caches[0], v_caches[0])
+    NB, bs, Hkv, D = _pools(k_caches[0], v_caches[0], kv_dtype)
     _flag(err_flag)
     for t in list(k_caches) + list(v_caches):
-        if tuple(t.shape) != (NB, bs, Hkv, D) or t.dtype != k_caches[0].dtype:
+        if t.shape != k_caches[0].shape or t.dtype != k_caches[0].dtype:
             raise ValueError("all pools must have one shape and dtype")
     if block_mapping.dtype != torch.int64 or (block_mapping.numel() and block_mapping.shape[-1] != 2):
         raise ValueError("block_mapping must be int64 [num_pairs, 2]")
@@ -280,9 +323,9 @@ def pa_swap_blocks(dst_k: torch.Tensor, dst_v: torch.Tensor, src_k: torch.Tensor
             raise ValueError("pools must be device memory or pinned host memory")
     _dev(block_mapping, err_flag)
     _flag(err_flag)
-    NBd, bs, Hkv, D = _pools(dst_k, dst_v)
-    NBs = _pools(src_k, src_v)[0]
-    if tuple(src_k.shape[1:]) != (bs, Hkv, D) or src_k.dtype != dst_k.dtype:
+    NBd, bs, Hkv, D = _pools(dst_k, dst_v, kv_dtype)
+    NBs = _pools(src_k, src_v, kv_dtype)[0]
+    if src_k.shape[1:] != dst_k.shape[1:] or src_k.dtype != dst_k.dtype:
         raise ValueError("pools must share the block shape and dtype")
     if block_mapping.dtype != torch.int64 or (block_mapping.numel() and block_mapping.shape[-1] != 2):
         raise ValueError("block_mapping must be int64 [num_pairs, 2]")

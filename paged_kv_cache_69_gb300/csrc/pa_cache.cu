@@ -7,7 +7,8 @@
 // pool, so one warp moves one token with 16-byte vector accesses.  fp8 pools
 // quantise on write ("kv-cache-memory-core", section 4.4): the source value
 // widened to float, divided by the per-tensor scale (IEEE division), then
-// CUDA's saturating round-to-nearest-even E4M3 conversion.
+// CUDA's saturating round-to-nearest-even E4M3 conversion.  4-bit pools are
+// written by pa_cache4.cu.
 //
 // copy_blocks: copy-on-write copies of whole blocks ("vLLM intro part 2",
 // section 5), for one layer's pools or for all layers in one launch; swap:
@@ -17,6 +18,7 @@
 #include <cstdint>
 #include <cstdio>
 
+#include "pa_cache4.h"
 #include "pa_common.h"
 #include "pa_device.cuh"
 
@@ -170,10 +172,10 @@ static pa_status launch_block_copy(const char* who, void* const* dst_k, void* co
         src_blocks <= 0 || dst_blocks <= 0)
         return bad(PA_ERR_INVALID_ARG, "sizes must be positive (num_pairs >= 0)");
     if (num_layers > MAX_LAYERS) return bad(PA_ERR_UNSUPPORTED, "more than 256 layers");
-    if (!valid_dtype(kv_dtype)) return bad(PA_ERR_INVALID_ARG, "unknown dtype");
+    if (!valid_cache_dtype(kv_dtype)) return bad(PA_ERR_INVALID_ARG, "unknown dtype");
     if (num_pairs == 0) return PA_OK;
     if (!pairs || !dst_k || !dst_v || !src_k || !src_v) return bad(PA_ERR_INVALID_ARG, "null pointer");
-    const int64_t block_bytes = static_cast<int64_t>(block_size) * num_kv_heads * head_dim * dtype_bytes(kv_dtype);
+    const int64_t block_bytes = static_cast<int64_t>(block_size) * num_kv_heads * row_bytes(kv_dtype, head_dim);
     if (block_bytes % 16 != 0) return bad(PA_ERR_UNSUPPORTED, "block bytes must be a multiple of 16");
     BlockCopyArgs a{};
     for (int l = 0; l < num_layers; ++l) {
@@ -228,13 +230,16 @@ extern "C" pa_status pa_reshape_and_cache(void* k_cache, void* v_cache, pa_dtype
     if (num_tokens == 0) return PA_OK;
     if (!k_cache || !v_cache || !key || !value || !slot_mapping)
         return fail(PA_ERR_INVALID_ARG, "reshape_and_cache: null pointer");
-    if (!valid_dtype(kv_dtype) || !valid_dtype(src_dtype))
+    if (!valid_cache_dtype(kv_dtype) || !valid_dtype(src_dtype))
         return fail(PA_ERR_INVALID_ARG, "reshape_and_cache: unknown dtype");
     const int64_t row_elems = static_cast<int64_t>(num_kv_heads) * head_dim;
     if (row_elems % VEC != 0 || row_elems > (1 << 30))
         return fail(PA_ERR_UNSUPPORTED, "reshape_and_cache: num_kv_heads*head_dim must be a multiple of 8");
     if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(key) || !aligned16(value))
         return fail(PA_ERR_INVALID_ARG, "reshape_and_cache: caches and sources must be 16-byte aligned");
+    if (is_int4(kv_dtype))
+        return write_int4(k_cache, v_cache, key, value, src_dtype, slot_mapping, num_tokens, num_kv_heads, head_dim,
+                          block_size, num_blocks, err_flag, stream);
     const int64_t nslots = static_cast<int64_t>(num_blocks) * block_size;
     cudaError_t e;
     const int re = static_cast<int>(row_elems);

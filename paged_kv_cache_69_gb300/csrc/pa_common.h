@@ -15,8 +15,14 @@ pa_status fail(pa_status s, const char* what);
 pa_status fail_cuda(const char* what, cudaError_t e);
 
 inline bool is_fp8(pa_dtype d) { return d == PA_FP8_E4M3 || d == PA_FP8_E5M2; }
+inline bool is_int4(pa_dtype d) { return d == PA_INT4; }
+// element types of tensors; PA_INT4 is a cache type only
 inline bool valid_dtype(pa_dtype d) { return d == PA_F32 || d == PA_F16 || d == PA_BF16 || is_fp8(d); }
+inline bool valid_cache_dtype(pa_dtype d) { return valid_dtype(d) || is_int4(d); }
 inline int dtype_bytes(pa_dtype d) { return d == PA_F32 ? 4 : (is_fp8(d) ? 1 : 2); }
+// bytes of one token's K (or V) row of one head in a pool: 4-bit codes and
+// their (step, low) pair, or the elements
+inline int row_bytes(pa_dtype d, int head_dim) { return is_int4(d) ? head_dim / 2 + 4 : head_dim * dtype_bytes(d); }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool isfinite_host(float x) { return std::isfinite(x); }
 

@@ -1,0 +1,78 @@
+// pa_int4.cuh -- the 4-bit cache format: quantising a row and reading codes.
+//
+// A row is one token's head_dim values of one KV head.  It is held as 4-bit
+// codes c in 0..15 and two f16 numbers, step and low:
+//     low  = f16(min x)             step = f16((max x - low) / 15)
+//     c    = (x - low) / step rounded to nearest even, limited to 0..15
+//     x'   = low + step * c
+// with x limited to +-65504 first (the largest f16, as fp8 caches limit to
+// their largest value), every rounding from the exact value, and c = 0 where
+// step is 0 (a row of equal values).  A row that holds a NaN has step = low =
+// NaN and reads as NaN throughout.
+//
+// Layout of one K (or V) block of a pool: codes [num_kv_heads][block_size]
+// [head_dim / 2] (dimension 2b in the low nibble of byte b), then (step, low)
+// [num_kv_heads][block_size][2] f16.  Heads lie outside the tokens, so the 16
+// tokens of a chunk of one head are contiguous (1 KB at head_dim 128), and a
+// block is one contiguous span that the block copies and swaps move as bytes.
+#pragma once
+
+#include <cstdint>
+#include <cuda_fp16.h>
+
+#include "pa_device.cuh"
+
+namespace pa {
+
+constexpr int INT4_PARAM_BYTES = 4;           // (step, low) of a row
+
+// Byte offsets of a row's codes and parameters inside its block.
+__device__ __forceinline__ uint32_t int4_code_off(int h, int off, int bs, int D) {
+    return static_cast<uint32_t>(h * bs + off) * static_cast<uint32_t>(D / 2);
+}
+__device__ __forceinline__ uint32_t int4_param_off(int h, int off, int bs, int D, int Hkv) {
+    return static_cast<uint32_t>(Hkv * bs) * static_cast<uint32_t>(D / 2) +
+           static_cast<uint32_t>(h * bs + off) * INT4_PARAM_BYTES;
+}
+
+// s = a + b rounded, and the part that the rounding lost (exact).
+__device__ __forceinline__ float two_sum(float a, float b, float& lost) {
+    const float s = __fadd_rn(a, b);
+    const float t = __fsub_rn(s, a);
+    lost = __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t));
+    return s;
+}
+
+// (step, low) of a row with the given extremes.  The quotient is rounded to
+// odd in f32 before its rounding to f16, so that the two roundings give what
+// one from the exact value would.
+__device__ __forceinline__ void int4_params(float mn, float mx, __half& step, __half& low) {
+    low = __float2half_rn(mn);
+    float lost;
+    const float a = two_sum(mx, -__half2float(low), lost);
+    float s = a > 0.f ? __fdiv_rn(a, 15.f) : 0.f;
+    const float r = __fadd_rn(__fmaf_rn(-s, 15.f, a), lost);       // sign of the exact quotient minus s
+    uint32_t b = __float_as_uint(s);
+    if (s > 0.f && r != 0.f && !(b & 1u)) b += r > 0.f ? 1u : 0xffffffffu;
+    step = __float2half_rn(__uint_as_float(b));
+}
+
+// The code of x: the nearest of the 16 values, by comparing x with the
+// middle between two neighbours.  (c + 1/2) * step has at most 16 bits, so
+// the comparison is exact; an estimate of c that is one too low or high next
+// to a whole quotient still leads to the right side of it.
+__device__ __forceinline__ uint32_t int4_code(float x, float low, float step, float rstep) {
+    float lost;
+    const float a = two_sum(x, -low, lost);
+    const float c = fminf(fmaxf(floorf(a * rstep), 0.f), 15.f);
+    const float t = __fadd_rn(__fmaf_rn(-(c + 0.5f), step, a), lost);
+    const uint32_t ci = static_cast<uint32_t>(c);
+    return min(ci + ((t > 0.f || (t == 0.f && (ci & 1u))) ? 1u : 0u), 15u);
+}
+
+// The value of a code: step * c is exact in f32, the sum is rounded once.
+__device__ __forceinline__ float int4_value(uint32_t c, float low, float step) {
+    return __fmaf_rn(step, static_cast<float>(c), low);
+}
+
+}  // namespace pa
