@@ -120,7 +120,8 @@ size_t pa_decode_workspace_size(int num_seqs, int num_q_heads, int max_seq_len,
  * block_tables[i][t / block_size].  fp8 caches are read as
  * K_t = e4m3(k) * k_scale, V_t = e4m3(v) * v_scale (scales ignored otherwise);
  * the scales are applied to the scores and the output, never per element.
- * L == 0 writes zeros.
+ * 4-bit caches (f16 or bf16 q) are read as low + step * code.  L == 0 writes
+ * zeros.
  *
  * The work is split into chunks of 16 tokens (32 for fp8 caches with
  * head_dim 128 and at most 8 query heads per KV head), balanced over
@@ -160,7 +161,7 @@ pa_status pa_decode(void* out, const void* q, pa_dtype q_dtype,
 /*
  * pa_decode_simt -- the same operation, arguments and results as pa_decode,
  * computed with CUDA-core FMAs instead of tensor-core MMAs, for every cache
- * type.  pa_decode runs this kernel for f32 caches; for the other types it
+ * type but 4-bit.  pa_decode runs this kernel for f32 caches; for the other types it
  * is a measured comparison point.
  */
 pa_status pa_decode_simt(void* out, const void* q, pa_dtype q_dtype,
@@ -272,7 +273,7 @@ pa_status pa_copy_blocks(void* k_cache, void* v_cache, pa_dtype kv_dtype,
  * group share the MMA tile.  q_start is a device int32 array of num_seqs + 1
  * entries, non-decreasing, q_start[0] = 0, q_start[num_seqs] = total_q; every
  * n_i <= max_q_len, and max_q_len * (num_q_heads / num_kv_heads) <= 128.
- * Tensor cores only (f16, bf16 and fp8 caches); other arguments as for
+ * Tensor cores only (f16, bf16, fp8 and 4-bit caches); other arguments as for
  * pa_decode.  With every n_i = 1 the result equals pa_decode's.
  * Kernels: with at least 48 rows per KV head (max_q_len * G), a 16-bit cache
  * and partition_tokens a multiple of 32, the rows of up to four KV heads

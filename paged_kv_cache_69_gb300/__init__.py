@@ -199,10 +199,10 @@ def pa_decode(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache
     """out[i, h] = softmax(scale * q[i, h] K_i^T) V_i over the paged pool.
     q/out [B, Hq, D]; k_cache/v_cache [NB, bs, Hkv, D]; block_tables int32
     [B, MB]; seq_lens int32 [B].  ``kv_dtype`` defaults to the cache tensor's
-    dtype (uint8 storage means fp8-e4m3)."""
+    dtype (uint8 storage means fp8-e4m3; "int4" names a 4-bit pool)."""
     _dev(out, q, k_cache, v_cache, block_tables, seq_lens, workspace, err_flag)
     B, Hq, D = q.shape
-    NB, bs, Hkv, D2 = _pools(k_cache, v_cache)
+    NB, bs, Hkv, D2 = _pools(k_cache, v_cache, kv_dtype)
     if D2 != D or tuple(out.shape) != (B, Hq, D) or out.dtype != q.dtype:
         raise ValueError("q and out must be [num_seqs, num_q_heads, head_dim] of one dtype, head_dim "
                          "that of the pools")
@@ -228,7 +228,7 @@ def pa_decode_noalloc(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
     (NOALLOC_SCRATCH_BYTES per GPU, shared by all calls on that GPU)."""
     _dev(out, q, k_cache, v_cache, block_tables, seq_lens, err_flag)
     B, Hq, D = q.shape
-    NB, bs, Hkv, D2 = _pools(k_cache, v_cache)
+    NB, bs, Hkv, D2 = _pools(k_cache, v_cache, kv_dtype)
     if D2 != D or tuple(out.shape) != (B, Hq, D) or out.dtype != q.dtype:
         raise ValueError("q and out must be [num_seqs, num_q_heads, head_dim] of one dtype, head_dim "
                          "that of the pools")
@@ -351,7 +351,7 @@ def pa_attention(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_ca
     seq_lens[i]; max_q_len bounds every sequence's query count."""
     _dev(out, q, k_cache, v_cache, block_tables, seq_lens, q_start, workspace, err_flag)
     T, Hq, D = q.shape
-    NB, bs, Hkv, D2 = _pools(k_cache, v_cache)
+    NB, bs, Hkv, D2 = _pools(k_cache, v_cache, kv_dtype)
     B = seq_lens.numel()
     if D2 != D or tuple(out.shape) != (T, Hq, D) or out.dtype != q.dtype:
         raise ValueError("q and out must be [total_q, num_q_heads, head_dim] of one dtype, head_dim "

@@ -11,6 +11,7 @@
 #include <mutex>
 
 #include "pa_common.h"
+#include "pa_decode_int4.h"
 #include "pa_decode_kernel.cuh"
 #include "pa_kernels.h"
 
@@ -157,7 +158,7 @@ static pa_status decode_impl(bool tc, void* out, const void* q, pa_dtype q_dtype
     if (B == 0) return PA_OK;
     if (!out || !q || !k_cache || !v_cache || !block_tables || !seq_lens)
         return fail(PA_ERR_INVALID_ARG, "decode: null pointer");
-    if (!valid_dtype(q_dtype) || !valid_dtype(kv_dtype)) return fail(PA_ERR_INVALID_ARG, "decode: unknown dtype");
+    if (!valid_dtype(q_dtype) || !valid_cache_dtype(kv_dtype)) return fail(PA_ERR_INVALID_ARG, "decode: unknown dtype");
     if (Hq % Hkv != 0) return fail(PA_ERR_INVALID_ARG, "decode: num_q_heads must be a multiple of num_kv_heads");
     if (D != 64 && D != 128) return fail(PA_ERR_UNSUPPORTED, "decode: head_dim must be 64 or 128");
     if (bs != 8 && bs != 16 && bs != 32 && bs != 64 && bs != 128)
@@ -174,6 +175,10 @@ static pa_status decode_impl(bool tc, void* out, const void* q, pa_dtype q_dtype
             return fail(PA_ERR_UNSUPPORTED, "decode: an fp8 cache needs f16 or bf16 queries");
         if (!(k_scale > 0.f) || !(v_scale > 0.f) || !isfinite_host(k_scale) || !isfinite_host(v_scale))
             return fail(PA_ERR_INVALID_ARG, "decode: fp8 scales must be finite and > 0");
+    } else if (is_int4(kv_dtype)) {
+        if (q_dtype != PA_F16 && q_dtype != PA_BF16)
+            return fail(PA_ERR_UNSUPPORTED, "decode: a 4-bit cache needs f16 or bf16 queries");
+        if (!tc) return fail(PA_ERR_UNSUPPORTED, "decode: 4-bit caches run on tensor cores only");
     } else if (q_dtype != kv_dtype) {
         return fail(PA_ERR_UNSUPPORTED, "decode: q dtype must equal the cache dtype (fp8 caches excepted)");
     }
@@ -186,6 +191,9 @@ static pa_status decode_impl(bool tc, void* out, const void* q, pa_dtype q_dtype
     if (mq && (!tc || QL < 1 || total_q < 0 || static_cast<long long>(QL) * (Hq / Hkv) > 128))
         return fail(PA_ERR_UNSUPPORTED,
                     "attention: several query tokens need the tensor-core path and max_q_len * G <= 128");
+    if (is_int4(kv_dtype))
+        return decode_int4(out, q, q_dtype, k_cache, v_cache, block_tables, MB, seq_lens, B, Hq, Hkv, D, bs, NB, scale,
+                           err_flag, stream, q_start, QL, total_q);
     // fp8 caches on the tensor-core path run the native-e4m3 kernel (32-token
     // chunks, GQA groups of up to 8 heads, partitions a multiple of 32
     // tokens); other fp8 shapes convert e4m3 to f16 in registers.

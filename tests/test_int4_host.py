@@ -164,3 +164,44 @@ def test_gather_refuses_bad_fp8_scales_and_takes_no_tokens(lib):
     assert lib.pa_gather_cache(*args, 0.0, 1.0, None, None) == 1
     args[7] = 0
     assert lib.pa_gather_cache(*args, 1.0, 1.0, None, None) == 0
+
+
+def test_attention_binding_reads_4bit_shapes(rec):  # noqa: F811
+    k, v = _pool4(D=128)
+    q = torch.zeros(3, 4, 128, dtype=torch.bfloat16)
+    bt, sl = torch.zeros(3, 5, dtype=torch.int32), torch.ones(3, dtype=torch.int32)
+    pa.pa_decode(torch.empty_like(q), q, k, v, bt, sl, 0.1, "int4")
+    a = rec.calls[-1][1]
+    assert (a[2], a[5], a[7], a[9], a[10], a[11], a[12], a[13], a[14]) == \
+        (pa.PA_BF16, pa.PA_INT4, 5, 3, 4, 2, 128, 16, 10)
+    pa.pa_decode_noalloc(torch.empty_like(q), q, k, v, bt, sl, 0.1, "int4")
+    assert rec.calls[-1][1][5] == pa.PA_INT4 and rec.calls[-1][1][12] == 128
+    qs = torch.tensor([0, 1, 2, 3], dtype=torch.int32)
+    pa.pa_attention(torch.empty_like(q), q, k, v, bt, sl, qs, 0.1, 2, "int4")
+    assert rec.calls[-1][1][5] == pa.PA_INT4 and rec.calls[-1][1][15] == 128
+    n = len(rec.calls)
+    with pytest.raises(ValueError):
+        pa.pa_decode(q[..., :64].contiguous(), q[..., :64].contiguous(), k, v, bt, sl, 0.1, "int4")
+    assert len(rec.calls) == n
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(qd=pa.PA_F32), 2),                   # 16-bit queries
+    (dict(qd=pa.PA_INT4), 1),
+    (dict(D=96), 2),
+    (dict(bs=24), 2),
+    (dict(k=8), 1),
+    (dict(P=24), 1),
+])
+def test_int4_decode_host_validation(lib, over, status):
+    from test_abi_host import _attention_args, _decode_args
+    assert lib.pa_decode(*_decode_args(kvd=pa.PA_INT4, **over)) == status
+    assert lib.pa_last_error_detail().decode() != ""
+    assert lib.pa_attention(*_attention_args(kvd=pa.PA_INT4, **over)) == status
+
+
+def test_int4_needs_the_tensor_core_kernel(lib):
+    from test_abi_host import _attention_args, _decode_args
+    assert lib.pa_decode_simt(*_decode_args(kvd=pa.PA_INT4)) == 2
+    assert lib.pa_attention(*_attention_args(kvd=pa.PA_INT4, MQ=65)) == 2      # 130 rows of a KV head
+    assert lib.pa_decode(*_decode_args(kvd=pa.PA_INT4, B=0)) == 0
