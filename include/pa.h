@@ -8,7 +8,10 @@
  *                         all layers: pa_copy_blocks_layers),
  *   pa_swap_blocks        block copies between a device and a host pool,
  *   pa_decode             one decode step of attention over a paged pool,
- *   pa_attention          several causal query tokens per sequence.
+ *   pa_decode_weights     the same, and the keys' weights added up,
+ *   pa_attention          several causal query tokens per sequence,
+ *   pa_evict              bring sequences down to a budget of tokens by their
+ *                         accumulated attention weight.
  *
  * Layouts (row-major, innermost last):
  *   k_cache, v_cache   [num_blocks, block_size, num_kv_heads, head_dim]
@@ -174,6 +177,36 @@ pa_status pa_decode_simt(void* out, const void* q, pa_dtype q_dtype,
                          int32_t* err_flag, cudaStream_t stream);
 
 /*
+ * pa_decode_weights -- pa_decode that also adds up the attention that every
+ * cached token receives, for pa_evict.  With p the softmax weights of
+ * pa_decode, the entry of token t of sequence i and KV head g (pool slot
+ * block * block_size + off) becomes
+ *   weights[block][g][off] += sum over the heads h of group g of p[i, h, t]
+ * except for the sequence's last fresh[i] tokens (null: 1, the token that this
+ * step wrote), whose entries start from 0: slots carry what their former
+ * owner left.  After a prompt of n tokens pass n once, then null.  weights is
+ * f32 [num_blocks, num_kv_heads, block_size]; entries of other slots are left
+ * as they were.  Sequences must not share blocks in one call (every holder
+ * would add to the same entries); the sums are f32, one addition per call.
+ * Any cache type of pa_decode; fp8 caches run a kernel that converts K and V
+ * to f16, so that the scores keep the query's full precision; the others give
+ * pa_decode's output.
+ *   fresh             int32 [num_seqs] on the device, or null
+ *   workspace         at least pa_decode_weights_workspace_size(...) bytes
+ * Other arguments as for pa_decode.
+ */
+size_t pa_decode_weights_workspace_size(int num_seqs, int num_q_heads, int max_seq_len,
+                                        int head_dim);
+pa_status pa_decode_weights(void* out, float* weights, const void* q, pa_dtype q_dtype,
+                            const void* k_cache, const void* v_cache, pa_dtype kv_dtype,
+                            const int32_t* block_tables, int max_blocks_per_seq,
+                            const int32_t* seq_lens, const int32_t* fresh, int num_seqs,
+                            int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                            int num_blocks, float scale, float k_scale, float v_scale,
+                            void* workspace, size_t workspace_bytes,
+                            int32_t* err_flag, cudaStream_t stream);
+
+/*
  * pa_decode_noalloc -- pa_decode for callers that cannot supply a workspace.
  * The pages have no counterpart: this exists for callers that must not
  * allocate device memory on the call path, such as a serving loop whose
@@ -291,6 +324,50 @@ pa_status pa_attention(void* out, const void* q, pa_dtype q_dtype,
                        int head_dim, int block_size, int num_blocks, float scale,
                        float k_scale, float v_scale, int partition_tokens, void* workspace,
                        size_t workspace_bytes, int32_t* err_flag, cudaStream_t stream);
+
+/*
+ * pa_evict -- bring every sequence longer than `budget` down to it, per KV
+ * head: of its L = seq_lens[i] tokens the first num_sink, the last num_recent
+ * and, of those between, the budget - num_sink - num_recent of largest
+ * accumulated weight stay (equal weights: the lower position; NaN counts as
+ * the lowest).  weights is f32 [num_blocks, num_kv_heads, block_size], one
+ * entry per pool slot and KV head, addressed through the same block tables as
+ * the pools.
+ * The kept rows of K, V and weights move to positions 0 .. budget-1: with
+ * heavy = budget - num_recent, a kept row below heavy stays where it is; the
+ * i-th position below heavy that is not kept takes the i-th kept row of
+ * [heavy, L - num_recent); the recent rows take [heavy, budget) in their order.
+ * (Attention does not depend on the order of the rows; keys carry their
+ * position already.)  Different heads may keep different tokens, so all heads
+ * of a sequence still share one table.
+ *   new_block_tables  null: in place, the blocks of the tables must then be
+ *                     this sequence's alone; rows from budget on are left as
+ *                     they were and their blocks may be released.  Otherwise
+ *                     int32 [num_seqs, new_max_blocks_per_seq]: all kept rows
+ *                     (all L when L <= budget) are copied into these blocks,
+ *                     which must be apart from the old ones; the old ones are
+ *                     left as they were, and may be shared.
+ *   new_seq_lens      int32 [num_seqs] out: min(L, budget).  May be seq_lens.
+ *   kept              int32 [num_seqs, num_kv_heads, budget] out, may be null:
+ *                     the former position of each position's row, -1 from the
+ *                     new length on.
+ * A sequence with L < 0 or longer than its table (PA_ERRBIT_SEQ_TOO_LONG), or
+ * with a block outside the pool among the blocks it uses
+ * (PA_ERRBIT_BAD_BLOCK), is skipped: kept is -1 throughout, its new length is
+ * L in place and 0 otherwise.
+ * Any cache type; a head's row must be a multiple of 16 bytes.
+ *   workspace         at least pa_evict_workspace_size(...) bytes, 256-byte
+ *                     aligned, no initialisation; calls sharing one must not
+ *                     overlap on the GPU.
+ */
+size_t pa_evict_workspace_size(int num_seqs, int num_kv_heads, int max_seq_len, int budget);
+pa_status pa_evict(void* k_cache, void* v_cache, pa_dtype kv_dtype, float* weights,
+                   const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+                   const int32_t* new_block_tables, int new_max_blocks_per_seq,
+                   int32_t* new_seq_lens, int32_t* kept, int num_seqs, int num_kv_heads,
+                   int head_dim, int block_size, int num_blocks, int budget, int num_sink,
+                   int num_recent, void* workspace, size_t workspace_bytes,
+                   int32_t* err_flag, cudaStream_t stream);
 
 /*
  * pa_copy_blocks_layers -- pa_copy_blocks for every layer of a model in one

@@ -27,7 +27,8 @@ ERRBIT_BAD_QUERY = 32
 EXPORTED = ("pa_status_string", "pa_last_error_detail", "pa_decode_workspace_size", "pa_decode",
             "pa_decode_simt", "pa_decode_noalloc", "pa_reshape_and_cache", "pa_copy_blocks",
             "pa_copy_blocks_layers", "pa_swap_blocks", "pa_attention", "pa_attention_workspace_size",
-            "pa_gather_cache", "pa_block_bytes")
+            "pa_gather_cache", "pa_block_bytes", "pa_evict", "pa_evict_workspace_size",
+            "pa_decode_weights", "pa_decode_weights_workspace_size")
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
 _DTYPE_CODE = {torch.float32: PA_F32, torch.float16: PA_F16, torch.bfloat16: PA_BF16,
@@ -84,6 +85,16 @@ def _configure(L):
     L.pa_attention.restype = c_int
     L.pa_attention.argtypes = [vp, vp, c_int, vp, vp, c_int, vp, c_int, vp, vp, c_int, c_int, c_int, c_int, c_int,
                                c_int, c_int, c_int, c_float, c_float, c_float, c_int, vp, sz, vp, vp]
+    L.pa_decode_weights_workspace_size.restype = sz
+    L.pa_decode_weights_workspace_size.argtypes = [c_int, c_int, c_int, c_int]
+    L.pa_decode_weights.restype = c_int
+    L.pa_decode_weights.argtypes = [vp, vp, vp, c_int, vp, vp, c_int, vp, c_int, vp, vp, c_int, c_int, c_int, c_int,
+                                    c_int, c_int, c_float, c_float, c_float, vp, sz, vp, vp]
+    L.pa_evict_workspace_size.restype = sz
+    L.pa_evict_workspace_size.argtypes = [c_int, c_int, c_int, c_int]
+    L.pa_evict.restype = c_int
+    L.pa_evict.argtypes = [vp, vp, c_int, vp, vp, c_int, vp, vp, c_int, vp, vp, c_int, c_int, c_int, c_int, c_int,
+                           c_int, c_int, c_int, vp, sz, vp, vp]
     return L
 
 
@@ -372,3 +383,86 @@ def pa_attention(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_ca
                               _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(err_flag),
                               _stream(stream)))
     return out
+
+
+def _weights(weights: torch.Tensor, NB: int, Hkv: int, bs: int):
+    if weights.dtype != torch.float32 or tuple(weights.shape) != (NB, Hkv, bs):
+        raise ValueError("weights must be float32 [num_blocks, num_kv_heads, block_size]")
+
+
+def pa_decode_weights_workspace_size(num_seqs: int, num_q_heads: int, max_seq_len: int, head_dim: int) -> int:
+    return int(lib().pa_decode_weights_workspace_size(num_seqs, num_q_heads, max_seq_len, head_dim))
+
+
+def pa_decode_weights(out: torch.Tensor, weights: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
+                      v_cache: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor, scale: float,
+                      kv_dtype=None, *, fresh: Optional[torch.Tensor] = None, k_scale: float = 1.0,
+                      v_scale: float = 1.0, workspace: Optional[torch.Tensor] = None,
+                      err_flag: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """pa_decode that also adds every key's softmax weight, summed over the
+    heads of its group, to ``weights`` (float32 [NB, Hkv, bs]).  The entries of
+    a sequence's last ``fresh`` tokens (int32 [B]; None: 1) start from 0."""
+    _dev(out, weights, q, k_cache, v_cache, block_tables, seq_lens, fresh, workspace, err_flag)
+    B, Hq, D = q.shape
+    NB, bs, Hkv, D2 = _pools(k_cache, v_cache, kv_dtype)
+    if D2 != D or tuple(out.shape) != (B, Hq, D) or out.dtype != q.dtype:
+        raise ValueError("q and out must be [num_seqs, num_q_heads, head_dim] of one dtype, head_dim "
+                         "that of the pools")
+    _tables(block_tables, seq_lens, B)
+    _weights(weights, NB, Hkv, bs)
+    _flag(err_flag)
+    if fresh is not None and (fresh.dtype != torch.int32 or fresh.numel() != B):
+        raise ValueError("fresh must be int32 [num_seqs]")
+    MB = block_tables.shape[1]
+    if workspace is None:
+        n = pa_decode_weights_workspace_size(B, Hq, MB * bs, D)
+        if n == 0:
+            raise PaError(1, "invalid workspace bounds")
+        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    _check(lib().pa_decode_weights(_ptr(out), _ptr(weights), _ptr(q), _code(q), _ptr(k_cache), _ptr(v_cache),
+                                   _code(k_cache, kv_dtype), _ptr(block_tables), MB, _ptr(seq_lens), _ptr(fresh), B, Hq,
+                                   Hkv, D, bs, NB, float(scale), float(k_scale), float(v_scale), _ptr(workspace),
+                                   workspace.numel() * workspace.element_size(), _ptr(err_flag), _stream(stream)))
+    return out
+
+
+def pa_evict_workspace_size(num_seqs: int, num_kv_heads: int, max_seq_len: int, budget: int) -> int:
+    return int(lib().pa_evict_workspace_size(num_seqs, num_kv_heads, max_seq_len, budget))
+
+
+def pa_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, weights: torch.Tensor, block_tables: torch.Tensor,
+             seq_lens: torch.Tensor, new_seq_lens: torch.Tensor, budget: int, kv_dtype=None, *, num_sink: int = 0,
+             num_recent: int = 0, new_block_tables: Optional[torch.Tensor] = None,
+             kept: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+             err_flag: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Bring every sequence down to ``budget`` tokens per KV head: the first
+    ``num_sink``, the last ``num_recent`` and the most heavily weighted between
+    them.  weights float32 [NB, Hkv, bs] moves with the rows; new_seq_lens
+    int32 [B] receives the lengths (it may be seq_lens); kept int32
+    [B, Hkv, budget] the former positions.  In place, or into the blocks of
+    ``new_block_tables`` (int32 [B, MB'], another tensor than block_tables)."""
+    _dev(k_cache, v_cache, weights, block_tables, seq_lens, new_seq_lens, new_block_tables, kept, workspace, err_flag)
+    NB, bs, Hkv, D = _pools(k_cache, v_cache, kv_dtype)
+    B = seq_lens.numel()
+    _tables(block_tables, seq_lens, B)
+    _weights(weights, NB, Hkv, bs)
+    _flag(err_flag)
+    if new_seq_lens.dtype != torch.int32 or new_seq_lens.numel() != B:
+        raise ValueError("new_seq_lens must be int32 [num_seqs]")
+    if kept is not None and (kept.dtype != torch.int32 or tuple(kept.shape) != (B, Hkv, budget)):
+        raise ValueError("kept must be int32 [num_seqs, num_kv_heads, budget]")
+    if new_block_tables is not None and new_block_tables.data_ptr() == block_tables.data_ptr():
+        new_block_tables = None
+    if new_block_tables is not None:
+        _tables(new_block_tables, seq_lens, B)
+    MB = block_tables.shape[1]
+    if workspace is None:
+        n = pa_evict_workspace_size(B, Hkv, MB * bs, int(budget))
+        if n == 0:
+            raise PaError(1, "invalid workspace bounds")
+        workspace = torch.empty(n, dtype=torch.uint8, device=k_cache.device)
+    _check(lib().pa_evict(_ptr(k_cache), _ptr(v_cache), _code(k_cache, kv_dtype), _ptr(weights), _ptr(block_tables), MB,
+                          _ptr(seq_lens), _ptr(new_block_tables),
+                          0 if new_block_tables is None else new_block_tables.shape[1], _ptr(new_seq_lens), _ptr(kept),
+                          B, Hkv, D, bs, NB, int(budget), int(num_sink), int(num_recent), _ptr(workspace),
+                          workspace.numel() * workspace.element_size(), _ptr(err_flag), _stream(stream)))

@@ -145,12 +145,13 @@ static int max_slots_for(int B, int max_seq_len, int partition_tokens, int sms) 
 
 // q_start == nullptr: one query per sequence (decode); otherwise sequence i
 // has q_start[i+1] - q_start[i] <= QL query rows starting at row q_start[i].
+// weights: the output of pa_decode_weights.
 static pa_status decode_impl(bool tc, void* out, const void* q, pa_dtype q_dtype, const void* k_cache,
                              const void* v_cache, pa_dtype kv_dtype, const int32_t* block_tables, int MB,
                              const int32_t* seq_lens, int B, int Hq, int Hkv, int D, int bs, int NB,
                              float scale, float k_scale, float v_scale, int partition_tokens,
                              void* workspace, size_t workspace_bytes, int32_t* err_flag, cudaStream_t stream,
-                             const int32_t* q_start = nullptr, int QL = 1, int total_q = 0) {
+                             const int32_t* q_start = nullptr, int QL = 1, int total_q = 0, bool weights = false) {
     const bool mq = q_start != nullptr;
     clear_error();
     if (B < 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || bs <= 0 || NB <= 0 || MB <= 0)
@@ -196,8 +197,10 @@ static pa_status decode_impl(bool tc, void* out, const void* q, pa_dtype q_dtype
                            err_flag, stream, q_start, QL, total_q);
     // fp8 caches on the tensor-core path run the native-e4m3 kernel (32-token
     // chunks, GQA groups of up to 8 heads, partitions a multiple of 32
-    // tokens); other fp8 shapes convert e4m3 to f16 in registers.
-    const bool native8 = !mq && tc && is_fp8(kv_dtype) && D == 128 && Hq / Hkv <= 8 &&
+    // tokens); other fp8 shapes convert e4m3 to f16 in registers, and so does
+    // pa_decode_weights, whose sums need the scores at the query's precision
+    // (the native kernels carry an f16 query in 8 bits).
+    const bool native8 = !mq && !weights && tc && is_fp8(kv_dtype) && D == 128 && Hq / Hkv <= 8 &&
                          partition_tokens % 32 == 0;
     const bool fp8t = native8 && Hq / Hkv <= 4;      // keys as the MMA rows: half the MMAs
     // Several query tokens with 48-128 (token, head) rows per KV head on a
@@ -448,6 +451,15 @@ static pa_status decode_impl(bool tc, void* out, const void* q, pa_dtype q_dtype
     ce = cudaLaunchKernelExC(&rcfg, rkern, rargs);
     if (ce != cudaSuccess) return fail_cuda("decode: reduce kernel launch", ce);
     return PA_OK;
+}
+
+pa_status decode_weights_out(void* out, const void* q, pa_dtype q_dtype, const void* k_cache, const void* v_cache,
+                             pa_dtype kv_dtype, const int32_t* block_tables, int MB, const int32_t* seq_lens, int B,
+                             int Hq, int Hkv, int D, int bs, int NB, float scale, float k_scale, float v_scale,
+                             void* workspace, size_t workspace_bytes, int32_t* err_flag, cudaStream_t stream) {
+    return decode_impl(true, out, q, q_dtype, k_cache, v_cache, kv_dtype, block_tables, MB, seq_lens, B, Hq, Hkv, D,
+                       bs, NB, scale, k_scale, v_scale, 0, workspace, workspace_bytes, err_flag, stream, nullptr, 1, 0,
+                       true);
 }
 
 }  // namespace pa

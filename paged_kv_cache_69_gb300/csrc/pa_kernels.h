@@ -20,4 +20,9 @@ const void* decode_kernel_mq_um(pa_dtype kv, pa_dtype q, int D, int CT);
 // Log-sum-exp merge; split_heads: several warps per (sequence, head), for
 // partitioned sequences with many partials.
 const void* reduce_kernel(pa_dtype out, int D, bool split_heads);
+// the output of pa_decode_weights
+pa_status decode_weights_out(void* out, const void* q, pa_dtype q_dtype, const void* k_cache, const void* v_cache,
+                             pa_dtype kv_dtype, const int32_t* block_tables, int MB, const int32_t* seq_lens, int B,
+                             int Hq, int Hkv, int D, int bs, int NB, float scale, float k_scale, float v_scale,
+                             void* workspace, size_t workspace_bytes, int32_t* err_flag, cudaStream_t stream);
 }  // namespace pa
