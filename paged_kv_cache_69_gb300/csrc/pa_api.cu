@@ -143,6 +143,52 @@ static int max_slots_for(int B, int max_seq_len, int partition_tokens, int sms) 
     return static_cast<int>(std::min<long long>(2LL * sms + units, 0x7fffffffLL));
 }
 
+// The parts of a workspace for prow partial rows per slot, or a failure.
+static pa_status carve_workspace(void* workspace, size_t bytes, int B, int prow, int D, int max_seq_len,
+                                 int partition_tokens, int sms, Workspace& w) {
+    const size_t need = workspace_bytes_for(B, prow, D, max_seq_len, partition_tokens, sms);
+    if (!workspace) return fail(PA_ERR_WORKSPACE, "decode: workspace pointer is null");
+    if (bytes < need) return fail(PA_ERR_WORKSPACE, "decode: workspace smaller than pa_decode_workspace_size()");
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return fail(PA_ERR_WORKSPACE, "decode: workspace must be 256-byte aligned");
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    w.split_list = reinterpret_cast<int4*>(ws); ws += align256(sizeof(int4) * static_cast<size_t>(B));
+    w.totals = reinterpret_cast<int*>(ws); ws += 256;
+    w.max_slots = max_slots_for(B, max_seq_len, partition_tokens, sms);
+    w.part_ml = reinterpret_cast<float2*>(ws); ws += align256(sizeof(float2) * static_cast<size_t>(w.max_slots) * prow);
+    w.part_acc = reinterpret_cast<float*>(ws);
+    return PA_OK;
+}
+
+pa_status launch_merge(const DecodeParams& p, pa_dtype out, bool split_heads, int sms, cudaStream_t stream) {
+    const void* rkern = reduce_kernel(out, p.D, split_heads);
+    if (!rkern) return fail(PA_ERR_UNSUPPORTED, "decode: no reduce kernel for this output dtype");
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t rcfg{};
+    const int red_block = red_threads(split_heads ? RED_SPLIT_WARPS : 1);
+    // persistent reduce grid: one wave of CTAs striding over the
+    // (split sequence, head group) items
+    int red_per_sm = 0;
+    cudaError_t ce = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&red_per_sm, rkern, red_block, 0);
+    if (ce != cudaSuccess) return fail_cuda("decode: reduce occupancy query", ce);
+    const long long items = static_cast<long long>(p.QL) *
+                            (split_heads ? static_cast<long long>(p.B) * p.Hq
+                                         : static_cast<long long>(p.B) * ((p.Hq + RED_THREADS / 32 - 1) / (RED_THREADS / 32)));
+    const long long g = std::max(1LL, std::min(items, static_cast<long long>(std::max(1, red_per_sm)) * sms));
+    rcfg.gridDim = dim3(static_cast<unsigned>(g));
+    rcfg.blockDim = dim3(static_cast<unsigned>(red_block));
+    rcfg.dynamicSmemBytes = 0;
+    rcfg.stream = stream;
+    rcfg.attrs = attr;
+    rcfg.numAttrs = 1;
+    DecodeParams arg = p;
+    void* rargs[] = {&arg};
+    ce = cudaLaunchKernelExC(&rcfg, rkern, rargs);
+    if (ce != cudaSuccess) return fail_cuda("decode: reduce kernel launch", ce);
+    return PA_OK;
+}
+
 // q_start == nullptr: one query per sequence (decode); otherwise sequence i
 // has q_start[i+1] - q_start[i] <= QL query rows starting at row q_start[i].
 // weights: the output of pa_decode_weights.
@@ -192,9 +238,14 @@ static pa_status decode_impl(bool tc, void* out, const void* q, pa_dtype q_dtype
     if (mq && (!tc || QL < 1 || total_q < 0 || static_cast<long long>(QL) * (Hq / Hkv) > 128))
         return fail(PA_ERR_UNSUPPORTED,
                     "attention: several query tokens need the tensor-core path and max_q_len * G <= 128");
-    if (is_int4(kv_dtype))
-        return decode_int4(out, q, q_dtype, k_cache, v_cache, block_tables, MB, seq_lens, B, Hq, Hkv, D, bs, NB, scale,
-                           err_flag, stream, q_start, QL, total_q);
+    if (is_int4(kv_dtype)) {
+        DeviceInfo di;
+        if (!device_info(di)) return fail(PA_ERR_CUDA, "decode: cannot query the current device");
+        Int4Call c{out, q, q_dtype, k_cache, v_cache, block_tables, MB, seq_lens, B, Hq, Hkv, D, bs, NB, scale,
+                   partition_tokens, Workspace{}, err_flag, stream, q_start, QL, total_q, di.sms, di.max_smem};
+        const pa_status st = carve_workspace(workspace, workspace_bytes, B, QL * Hq, D, MB * bs, partition_tokens, di.sms, c.ws);
+        return st == PA_OK ? decode_int4(c) : st;
+    }
     // fp8 caches on the tensor-core path run the native-e4m3 kernel (32-token
     // chunks, GQA groups of up to 8 heads, partitions a multiple of 32
     // tokens); other fp8 shapes convert e4m3 to f16 in registers, and so does
@@ -226,8 +277,6 @@ static pa_status decode_impl(bool tc, void* out, const void* q, pa_dtype q_dtype
                                : decode_kernel_simt(kv_dtype, q_dtype, D);
     if (!kern) return fail(PA_ERR_UNSUPPORTED, "decode: no kernel for this dtype / head_dim combination");
     const bool split_heads = partition_tokens > 0;
-    const void* rkern = reduce_kernel(q_dtype, D, split_heads);
-    if (!rkern) return fail(PA_ERR_UNSUPPORTED, "decode: no reduce kernel for this output dtype");
     DeviceInfo dev;
     if (!device_info(dev)) return fail(PA_ERR_CUDA, "decode: cannot query the current device");
 
@@ -332,18 +381,11 @@ static pa_status decode_impl(bool tc, void* out, const void* q, pa_dtype q_dtype
     p.qk_scale = scale * log2e * (is_fp8(kv_dtype) ? k_scale : 1.f);
     p.v_scale = is_fp8(kv_dtype) ? v_scale : 1.f;
 
-    // workspace
-    const int prow = QL * Hq;                         // partial rows per slot
-    const size_t need = workspace_bytes_for(B, prow, D, MB * bs, partition_tokens, dev.sms);
-    if (!workspace) return fail(PA_ERR_WORKSPACE, "decode: workspace pointer is null");
-    if (workspace_bytes < need) return fail(PA_ERR_WORKSPACE, "decode: workspace smaller than pa_decode_workspace_size()");
-    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return fail(PA_ERR_WORKSPACE, "decode: workspace must be 256-byte aligned");
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
-    p.split_list = reinterpret_cast<int4*>(ws); ws += align256(sizeof(int4) * static_cast<size_t>(B));
-    p.totals = reinterpret_cast<int*>(ws); ws += 256;
-    p.max_slots = max_slots_for(B, MB * bs, partition_tokens, dev.sms);
-    p.part_ml = reinterpret_cast<float2*>(ws); ws += align256(sizeof(float2) * static_cast<size_t>(p.max_slots) * prow);
-    p.part_acc = reinterpret_cast<float*>(ws);
+    Workspace w{};
+    const pa_status wst = carve_workspace(workspace, workspace_bytes, B, QL * Hq, D, MB * bs, partition_tokens, dev.sms, w);
+    if (wst != PA_OK) return wst;
+    p.split_list = w.split_list; p.totals = w.totals; p.max_slots = w.max_slots;
+    p.part_ml = w.part_ml; p.part_acc = w.part_acc;
 
     // tensor maps
     alignas(64) CUtensorMap tk, tv;
@@ -428,29 +470,7 @@ static pa_status decode_impl(bool tc, void* out, const void* q, pa_dtype q_dtype
     ce = cudaLaunchKernelExC(&cfg, kern, args);
     if (ce != cudaSuccess) return fail_cuda("decode: main kernel launch", ce);
 
-    cudaLaunchConfig_t rcfg{};
-    const int red_block = red_threads(split_heads ? RED_SPLIT_WARPS : 1);
-    {
-        // persistent reduce grid: one wave of CTAs striding over the
-        // (split sequence, head group) items
-        int red_per_sm = 0;
-        ce = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&red_per_sm, rkern, red_block, 0);
-        if (ce != cudaSuccess) return fail_cuda("decode: reduce occupancy query", ce);
-        const long long items = static_cast<long long>(QL) *
-                                (split_heads ? static_cast<long long>(B) * Hq
-                                             : static_cast<long long>(B) * ((Hq + RED_THREADS / 32 - 1) / (RED_THREADS / 32)));
-        const long long g = std::max(1LL, std::min(items, static_cast<long long>(std::max(1, red_per_sm)) * dev.sms));
-        rcfg.gridDim = dim3(static_cast<unsigned>(g));
-    }
-    rcfg.blockDim = dim3(static_cast<unsigned>(red_block));
-    rcfg.dynamicSmemBytes = 0;
-    rcfg.stream = stream;
-    rcfg.attrs = attr;
-    rcfg.numAttrs = 1;
-    void* rargs[] = {&p};
-    ce = cudaLaunchKernelExC(&rcfg, rkern, rargs);
-    if (ce != cudaSuccess) return fail_cuda("decode: reduce kernel launch", ce);
-    return PA_OK;
+    return launch_merge(p, q_dtype, split_heads, dev.sms, stream);
 }
 
 pa_status decode_weights_out(void* out, const void* q, pa_dtype q_dtype, const void* k_cache, const void* v_cache,

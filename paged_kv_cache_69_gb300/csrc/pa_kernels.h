@@ -4,6 +4,17 @@
 #include "../../include/pa.h"
 
 namespace pa {
+struct DecodeParams;
+// The parts of a decode workspace (pa_api.cu lays them out).
+struct Workspace {
+    int4* split_list;
+    int* totals;
+    float2* part_ml;
+    float* part_acc;
+    int max_slots;
+};
+// Launch of the log-sum-exp merge behind a main kernel's.
+pa_status launch_merge(const DecodeParams& p, pa_dtype out, bool split_heads, int sms, cudaStream_t stream);
 // Kernel entry for the given cache dtype, query dtype and head_dim, or null.
 const void* decode_kernel_tc(pa_dtype kv, pa_dtype q, int D);
 const void* decode_kernel_simt(pa_dtype kv, pa_dtype q, int D);
