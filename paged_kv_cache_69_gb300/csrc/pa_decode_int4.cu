@@ -19,11 +19,12 @@
 // operand layout of the second product by an 8 x 8 transpose (movmatrix).
 //
 // Work split, partials and the merge are the paged decode kernel's: the chunks
-// (64 tokens here) of all sequences form one stream, cut into ranges of equal
-// cost for persistent CTAs; one warp fills a ring of stages with contiguous
-// bulk copies (a block's codes of the CTA's heads are one span, its
-// parameters another), the other warps each own 8 or 16 query rows of one KV
-// head.
+// of all sequences form one stream, cut into ranges of equal cost for
+// persistent CTAs; one warp fills a ring of stages with contiguous bulk copies
+// (a block's codes of the CTA's heads are one span, its parameters another),
+// the other warps each own 8 or 16 query rows of one KV head.  TS such warps
+// share a chunk of 32 TS tokens, 32 each, and join their results in shared
+// memory at the end of a segment.
 #include <algorithm>
 #include <cmath>
 #include <cuda.h>
@@ -36,16 +37,22 @@
 
 namespace pa {
 
-constexpr int I4_CT = 64;                   // tokens of a chunk
-constexpr int I4_MT = I4_CT / 16;           // 16-token tiles of a chunk
+constexpr int I4_WT = 32;                   // tokens of a chunk that one warp takes
+constexpr int I4_WARPS = 4;                 // consumer warps of a CTA, where the rows allow
+// 16-token tiles that a warp carries through the two products at once, and
+// CTAs per SM: as many as the registers hold.
+constexpr int i4_tiles(int nqt) { return nqt == 1 ? 2 : 1; }
+constexpr int i4_ctas(int nqt) { return nqt == 1 ? 3 : 2; }
 constexpr int I4_MAX_STAGES = 8;
 constexpr int I4_NQ = 2;                    // query ring slots
 
-struct I4Desc {
-    int seq, tok0, slot, qrow0, qpos0, qn;
+struct I4Head {
+    int tok0, slot, qrow0, qpos0, qn, qslot;
     uint32_t flags;                         // SEG_* bits, QLOAD, DIRECT, GAP
-    int qslot;
-    uint64_t vmask;                         // tokens of the chunk that exist
+};
+struct I4Desc {
+    I4Head h;
+    uint32_t vmask[I4_WARPS];               // tokens of the chunk that exist, 32 per warp
 };
 
 struct Int4Params {
@@ -54,9 +61,27 @@ struct Int4Params {
     const uint8_t* v;
     size_t block_bytes;
     uint32_t code_bytes, param_bytes;       // of one stage's K (or V)
-    int RT;                                 // row tiles (warps) per KV head
+    int RT;                                 // row tiles per KV head
+    int TS;                                 // warps that share a chunk's tokens
     int nbox;                               // blocks of a chunk
+    int bshift, rshift;                     // log2 of the block size, and of the rows that a block has in a chunk
+    uint32_t join_off, frag_off;            // offsets of the join buffers and of the warps' query operands
 };
+
+// Bulk copy by 32-bit shared addresses.
+__device__ __forceinline__ void bulk_load32(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 :: "r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
+}
+
+// 16-byte copy by the thread's own address, and this thread's arrival on `bar`
+// once its copies so far have landed (counted in the barrier's 33 arrivals).
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" :: "r"(bar) : "memory");
+}
 
 // ---------------------------------------------------------------------------
 // producer: one warp; lane b copies block b of a chunk (or head b of a block
@@ -67,7 +92,7 @@ __device__ __forceinline__ void int4_producer(const Int4Params& a, const Plan& p
                                               uint64_t* full, uint64_t* empty, uint64_t* qempty, I4Desc* descs) {
     const DecodeParams& p = a.d;
     const int lane = threadIdx.x & 31;
-    const int S = p.stages, maxL = p.MB * p.bs;
+    const int S = p.stages, maxL = p.MB * p.bs, CT = p.ct;
     int lbase = pl.seq, lval = 0;
     auto load_lens = [&](int first) {
         lbase = first;
@@ -87,7 +112,7 @@ __device__ __forceinline__ void int4_producer(const Int4Params& a, const Plan& p
     int i = pl.seq, Si = pl.S, Ui = pl.U;
     int j = pl.cs - Si;
     const int nb = a.nbox;
-    int wbase = (j * I4_CT) / p.bs;                 // 32 table entries from here on, the next 32 in flight
+    int wbase = (j * CT) >> a.bshift;                 // 32 table entries from here on, the next 32 in flight
     int wval = load_win(i, wbase, p.MB);
     int L = len_of(i);
     int qrow = i, qn = 1;
@@ -99,7 +124,7 @@ __device__ __forceinline__ void int4_producer(const Int4Params& a, const Plan& p
         }
     };
     load_q_rows();
-    int nch = cdiv_i(L, I4_CT), nbl = cdiv_i(L, p.bs);
+    int nch = cdiv_i(L, CT), nbl = cdiv_i(L, p.bs);
     int nseq = 0, nbase = 0, nval = -1;
     auto prefetch_next = [&]() {
         if (wbase + 32 < nbl) {
@@ -111,27 +136,46 @@ __device__ __forceinline__ void int4_producer(const Int4Params& a, const Plan& p
     prefetch_next();
     const int range = blockIdx.x / p.NHG;
     const uint32_t head_codes = static_cast<uint32_t>(p.bs) * (D / 2);       // a block's codes of one head
-    const uint32_t params_at = static_cast<uint32_t>(p.Hkv) * head_codes;    // its parameters
-    const int rows = min(p.bs, I4_CT);                                       // rows of a block in a chunk
-    const bool whole = p.bs <= I4_CT;
-    const uint32_t box_codes = static_cast<uint32_t>(p.HPC * rows) * (D / 2), box_params = static_cast<uint32_t>(p.HPC * rows) * 4u;
+    const int rows = 1 << a.rshift;                                          // rows of a block in a chunk
+    const bool whole = p.bs <= CT;
+    const uint32_t box_codes = static_cast<uint32_t>(p.HPC * rows) * (D / 2);
+    const uint32_t qrow_bytes = static_cast<uint32_t>(p.HPC * p.G) * D * 2u;
+    // The copies of a chunk are on the path from a stage coming free to its
+    // refill, and one warp issues those of four: what a chunk needs beyond its
+    // block ids is worked out per sequence or per CTA.
+    const uint8_t* kcs = a.k + static_cast<size_t>(hg * p.HPC) * head_codes;
+    const uint8_t* vcs = a.v + static_cast<size_t>(hg * p.HPC) * head_codes;
+    const uint32_t base32 = smem_u32(base), full32 = smem_u32(full);
+    const uint32_t my_codes = lane * box_codes;
+    const uint32_t v_at = a.code_bytes + a.param_bytes;
+    // Parameters are small next to what a bulk copy costs to issue: each lane
+    // copies those of four tokens of a head, 16 bytes, for K and for V.
+    const int prow = lane * 4, pbox = prow / (p.HPC * rows), phead = (prow >> a.rshift) % p.HPC;
+    const bool pmine = prow < p.HPC * CT;
+    const uint32_t my_params = a.code_bytes + prow * 4u;
+    const size_t to_params = static_cast<size_t>(p.Hkv - hg * p.HPC) * head_codes +
+                             static_cast<size_t>((hg * p.HPC + phead) * p.bs + (prow & (rows - 1))) * 4u;
     int issued = 0, qcount = 0, slot = 0, qs = 0;
     uint32_t round = 0, qround = 0;
     int jp = j, ju = 0;
     if (p.PC > 0) { ju = j / p.PC; jp = j - ju * p.PC; }
     bool ok = true;
+    bool direct = (p.PC == 0 || nch <= p.PC) && Si >= pl.cs && Si + nch <= pl.ce;
     for (int k = pl.cs; k < pl.ce; ++k) {
-        while (j >= nch) {
-            Si += nch; Ui += n_units(L, p.PC, p.ct); ++i;
-            L = len_of(i);
-            load_q_rows();
-            nch = cdiv_i(L, I4_CT); nbl = cdiv_i(L, p.bs);
-            j = 0; jp = 0; ju = 0;
-            wbase = 0;
-            wval = (nseq == i && nbase == 0) ? nval : load_win(i, 0, nbl);
-            prefetch_next();
+        if (j >= nch) {
+            do {
+                Si += nch; Ui += n_units(L, p.PC, p.ct); ++i;
+                L = len_of(i);
+                load_q_rows();
+                nch = cdiv_i(L, CT); nbl = cdiv_i(L, p.bs);
+                j = 0; jp = 0; ju = 0;
+                wbase = 0;
+                wval = (nseq == i && nbase == 0) ? nval : load_win(i, 0, nbl);
+                prefetch_next();
+            } while (j >= nch);
+            direct = (p.PC == 0 || nch <= p.PC) && Si >= pl.cs && Si + nch <= pl.ce;
         }
-        const int tok0 = j * I4_CT, b0 = tok0 / p.bs;
+        const int tok0 = j * CT, b0 = tok0 >> a.bshift;
         if (b0 + nb - 1 >= wbase + 32) {
             if (nseq == i && nbase <= b0 && b0 + nb - 1 < nbase + 32) {
                 wbase = nbase; wval = nval;
@@ -140,36 +184,21 @@ __device__ __forceinline__ void int4_producer(const Int4Params& a, const Plan& p
             }
             prefetch_next();
         }
-        const int ntok = min(I4_CT, L - tok0);
+        const int ntok = min(CT, L - tok0);
         // lane b < nb: block b of the chunk
         const int id = __shfl_sync(0xffffffffu, wval, min(b0 + lane - wbase, 31));
-        const bool mine = lane < nb && lane * rows < ntok;
-        const bool good = mine && id >= 0 && id < p.NB;
-        if (mine && !good) raise_flag(p.err_flag, PA_ERRBIT_BAD_BLOCK);
+        const uint32_t used = (1u << ((ntok + rows - 1) >> a.rshift)) - 1u;       // blocks with a token (at most 16)
+        const bool good = ((used >> lane) & 1u) && static_cast<unsigned>(id) < static_cast<unsigned>(p.NB);
         const uint32_t goods = __ballot_sync(0xffffffffu, good);
-        uint64_t vmask = ntok >= 64 ? ~0ull : ((1ull << ntok) - 1ull);
-        if (goods != __ballot_sync(0xffffffffu, mine)) {
-            for (int b = 0; b < nb; ++b)
-                if (!((goods >> b) & 1u)) {
-                    const uint64_t r = rows >= 64 ? ~0ull : ((1ull << rows) - 1ull);
-                    vmask &= ~(r << (b * rows));
-                }
-        }
+        if (goods != used && lane == 0) raise_flag(p.err_flag, PA_ERRBIT_BAD_BLOCK);
         const bool seg_start = (k == pl.cs) || (jp == 0);
         const bool qload = seg_start && (k == pl.cs || j == 0);
-        if (lane == 0) {
-            if (issued >= S && !mbar_wait_bounded(&empty[slot], (round - 1) & 1u)) {
-                raise_flag(p.err_flag, PA_ERRBIT_WAIT_TIMEOUT);
-                ok = false;
-            }
-            if (ok && qload && qcount >= I4_NQ && !mbar_wait_bounded(&qempty[qs], (qround - 1) & 1u)) {
-                raise_flag(p.err_flag, PA_ERRBIT_WAIT_TIMEOUT);
-                ok = false;
-            }
+        ok = issued < S || mbar_wait_bounded(&empty[slot], (round - 1) & 1u);
+        if (qload && qcount >= I4_NQ) ok = mbar_wait_bounded(&qempty[qs], (qround - 1) & 1u) && ok;
+        if (!__all_sync(0xffffffffu, ok)) {
+            if (lane == 0) raise_flag(p.err_flag, PA_ERRBIT_WAIT_TIMEOUT);
+            break;
         }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) break;
-        const uint32_t qrow_bytes = static_cast<uint32_t>(p.HPC * p.G) * D * 2u;
         if (lane == 0) {
             const bool part_end = p.PC > 0 && jp == p.PC - 1;
             uint32_t flags = 0;
@@ -177,45 +206,53 @@ __device__ __forceinline__ void int4_producer(const Int4Params& a, const Plan& p
             if (qload) flags |= QLOAD;
             if (k == pl.ce - 1 || j == nch - 1 || part_end) flags |= SEG_END;
             if (k == pl.ce - 1 && part_end && j + 1 < nch) flags |= GAP;
-            if (n_units(L, p.PC, p.ct) == 1 && Si >= pl.cs && Si + nch <= pl.ce) flags |= DIRECT;
-            I4Desc d;
-            d.seq = i; d.tok0 = tok0; d.vmask = vmask; d.flags = flags; d.qn = qn;
+            if (direct) flags |= DIRECT;
+            I4Head d;
+            d.tok0 = tok0; d.flags = flags; d.qn = qn;
             d.slot = range + Ui + ju;
             d.qslot = qload ? qs : (qs == 0 ? I4_NQ - 1 : qs - 1);
             d.qrow0 = qrow;
             d.qpos0 = L - qn;
-            descs[slot] = d;
-            const uint32_t boxes = __popc(goods);
-            mbar_arrive_expect_tx(&full[slot], boxes * 2u * (box_codes + box_params) +
+            descs[slot].h = d;
+            if (ntok == CT && goods == used) {
+                for (int w = 0; w < CT / 32; ++w) descs[slot].vmask[w] = 0xffffffffu;
+            } else {
+                // tokens that exist and whose block is in the pool
+                for (int w = 0; w < CT / 32; ++w) {
+                    const int n = ntok - 32 * w;
+                    uint32_t m = n >= 32 ? 0xffffffffu : n > 0 ? (1u << n) - 1u : 0u;
+                    for (int t = 0; t < 32; t += 8)
+                        if (!((goods >> ((32 * w + t) >> a.rshift)) & 1u)) m &= ~(0xffu << t);
+                    descs[slot].vmask[w] = m;
+                }
+            }
+            mbar_arrive_expect_tx(&full[slot], __popc(goods) * 2u * box_codes +
                                                    (qload ? static_cast<uint32_t>(qn) * qrow_bytes : 0u));
         }
         __syncwarp();
-        uint8_t* kc = base + slot * p.stage_bytes;
-        uint8_t* kp = kc + a.code_bytes;
-        uint8_t* vc = kp + a.param_bytes;
-        uint8_t* vp = vc + a.code_bytes;
+        const uint32_t stage = base32 + slot * p.stage_bytes, bar = full32 + slot * 8u;
+        const int pid = __shfl_sync(0xffffffffu, id, pbox);
+        if (pmine && ((goods >> pbox) & 1u)) {
+            const size_t at = static_cast<size_t>(static_cast<unsigned>(pid)) * a.block_bytes + to_params +
+                              (whole ? 0u : static_cast<uint32_t>(tok0 & (p.bs - 1)) * 4u);
+            cp_async16(stage + my_params, kcs + at);
+            cp_async16(stage + v_at + my_params, vcs + at);
+        }
+        cp_async_arrive(bar);
         if (whole) {
             if (good) {
-                const size_t blk = static_cast<size_t>(id) * a.block_bytes;
-                const size_t cs = blk + static_cast<size_t>(hg * p.HPC) * head_codes;
-                const size_t ps = blk + params_at + static_cast<size_t>(hg * p.HPC * p.bs) * 4u;
-                bulk_load(kc + lane * box_codes, a.k + cs, box_codes, &full[slot]);
-                bulk_load(kp + lane * box_params, a.k + ps, box_params, &full[slot]);
-                bulk_load(vc + lane * box_codes, a.v + cs, box_codes, &full[slot]);
-                bulk_load(vp + lane * box_params, a.v + ps, box_params, &full[slot]);
+                const size_t blk = static_cast<size_t>(static_cast<unsigned>(id)) * a.block_bytes;
+                bulk_load32(stage + my_codes, kcs + blk, box_codes, bar);
+                bulk_load32(stage + v_at + my_codes, vcs + blk, box_codes, bar);
             }
         } else if (goods & 1u) {
             // a chunk is part of one block: a span per head
-            const size_t blk = static_cast<size_t>(__shfl_sync(0xffffffffu, id, 0)) * a.block_bytes;
-            const int t0 = tok0 % p.bs;
-            const uint32_t cb = I4_CT * (D / 2), pb = I4_CT * 4;
+            const size_t blk = static_cast<size_t>(__shfl_sync(0xffffffffu, id, 0)) * a.block_bytes +
+                               static_cast<size_t>(tok0 & (p.bs - 1)) * (D / 2);
+            const uint32_t cb = CT * (D / 2);
             for (int h = lane; h < p.HPC; h += 32) {
-                const size_t cs = blk + static_cast<size_t>(hg * p.HPC + h) * head_codes + static_cast<size_t>(t0) * (D / 2);
-                const size_t ps = blk + params_at + static_cast<size_t>((hg * p.HPC + h) * p.bs + t0) * 4u;
-                bulk_load(kc + h * cb, a.k + cs, cb, &full[slot]);
-                bulk_load(kp + h * pb, a.k + ps, pb, &full[slot]);
-                bulk_load(vc + h * cb, a.v + cs, cb, &full[slot]);
-                bulk_load(vp + h * pb, a.v + ps, pb, &full[slot]);
+                bulk_load32(stage + h * cb, kcs + blk + static_cast<size_t>(h) * head_codes, cb, bar);
+                bulk_load32(stage + v_at + h * cb, vcs + blk + static_cast<size_t>(h) * head_codes, cb, bar);
             }
         }
         if (qload) {
@@ -242,6 +279,40 @@ __device__ __forceinline__ void int4_producer(const Int4Params& a, const Plan& p
             }
         }
     }
+}
+
+// Loads from shared memory by 32-bit address: the stage's address is computed
+// from a rounded-up base, behind which the compiler would not see the address
+// space and load through 64-bit generic addresses.
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t r;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 r;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 r;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" :: "r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ float2 lds_params(uint32_t a) {        // (step, low)
+    const uint32_t r = lds32(a);
+    return __half22float2(*reinterpret_cast<const __half2*>(&r));
+}
+// D = A B, f16 operands: mma_16816 with a zero accumulator.
+__device__ __forceinline__ void mma_16816_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
@@ -274,35 +345,58 @@ __device__ __forceinline__ uint32_t pack_out(float a, float b) {
 // ---------------------------------------------------------------------------
 template <class QT, int D, int NQT, bool HL>
 __device__ __forceinline__ void int4_consumer(const Int4Params& a, const Plan& pl, int hg, int w, uint8_t* base,
-                                              uint64_t* full, uint64_t* empty, uint64_t* qempty, const I4Desc* descs) {
+                                              uint64_t* full, uint64_t* empty, uint64_t* qempty, uint64_t* joined,
+                                              const I4Desc* descs) {
     using T = typename QT::T;
+    constexpr int MT = i4_tiles(NQT);             // 16-token tiles at once
+    constexpr int SUBS = I4_WT / (16 * MT);       // times that a chunk takes
     constexpr int KW = D / 32;                    // 32-bit code words of a key that a lane reads
     constexpr int OT = D / 16;                    // 16-dimension output tiles
     constexpr float UNIT = 16777216.f;            // 2^24: what an f16 with the bits of n is short of n
     const DecodeParams& p = a.d;
     const int lane = threadIdx.x & 31, g4 = lane >> 2, t4 = lane & 3;
-    const int hl = w / a.RT, rt = w - hl * a.RT;
+    const int tile = w / a.TS, ts = w - tile * a.TS;      // (KV head, row tile), and its share of the tokens
+    const int hl = tile / a.RT, rt = tile - hl * a.RT;
     const int S = p.stages;
     const int rows_total = p.QL * p.G;
-    const int rows = min(p.bs, I4_CT);            // rows of a block in a chunk
+    const uint32_t base32 = smem_u32(base);
     // Row r of a tile of 8 tokens is token tau(r) = r ^ (r / 2 % 2), on both
     // sides of P: the four tokens that a quarter of the V loads reads are then
     // two even and two odd 64-byte rows.
     const int tk = g4 ^ ((g4 >> 1) & 1);
     const int tv0 = (2 * t4) ^ (t4 & 1), tv1 = (2 * t4 + 1) ^ (t4 & 1);
-    // byte offset of a token's row of this head in the stage's codes / parameters
-    auto row_of = [&](int t) -> uint32_t {
-        const int b = t / rows;
-        return static_cast<uint32_t>((b * p.HPC + hl) * rows + (t - b * rows));
-    };
+    // A stage is K codes, K parameters, V codes, V parameters, each [block]
+    // [head][row]; a block has 8 rows or a multiple.  Bytes from its start to
+    // the codes of the first of each 8 tokens of this head, and to the
+    // parameters of the lane's token of them.  With 8 rows per warp HPC * TS is
+    // 4 and the distances inside a stage are constants of the code.
+    const uint32_t POFF = NQT == 1 ? I4_WARPS * I4_WT * (D / 2) : a.code_bytes;
+    const uint32_t VOFF = NQT == 1 ? I4_WARPS * I4_WT * (D / 2 + 4) : a.code_bytes + a.param_bytes;
+    uint32_t c8[I4_WT / 8], p8[I4_WT / 8];
+#pragma unroll
+    for (int x = 0; x < I4_WT / 8; ++x) {
+        const uint32_t t = I4_WT * ts + 8 * x, b = t >> a.rshift;
+        const uint32_t row = ((b * p.HPC + hl) << a.rshift) + (t - (b << a.rshift));
+        c8[x] = row * (D / 2);
+        p8[x] = (row + tk) * 4u;
+    }
+    const uint32_t ok = tk * (D / 2) + t4 * (D / 8);                   // the lane's part of a key row
+    const uint32_t ov0 = tv0 * (D / 2) + g4 * (D / 16), ov1 = tv1 * (D / 2) + g4 * (D / 16);   // and of two value rows
 
     float acc[OT][NQT][4];
-    uint32_t qf[NQT][KW][4];
-    float m[NQT][2], l[NQT][2], c0[NQT][2];       // rows 2 t4 and 2 t4 + 1 of each tile
-    float sq[NQT][2], qk[NQT][2];
+    // The warp's query operand, [tile][word][lane] 16 bytes, kept in shared
+    // memory: the registers it would take buy another CTA per SM.
+    const uint32_t qf = base32 + a.frag_off + static_cast<uint32_t>(w * NQT * KW * 512) + lane * 16u;
+    // rows 2 t4 and 2 t4 + 1 of each tile: reference of the exponent (a row's
+    // largest score within 2^8, 0 while it has none), sum of the weights, sum
+    // of weight * low; the last two over the lane's tokens
+    float m[NQT][2], l[NQT][2], c0[NQT][2];
+    float top[NQT][2], mu[NQT][2];                // m + 8, and m or 0 while it is -infinity
+    float sq[NQT][2];                             // sum of the query row, times the score scale
+    float unit_qk = 0.f;                          // score of one unit of the codes' dot product
     int jt[NQT][2], lim[NQT][2];
-    float inv = 0.f;                              // power of two on step in the weights; 0: not set yet
-    int in_rows = 0;
+    float inv = 0.f, step_top = 0.f;              // power of two on step in the weights (0: not set yet); 2^7 over it
+    int in_rows = 0, joins = 0;
 #pragma unroll
     for (int n = 0; n < NQT; ++n)
 #pragma unroll
@@ -311,7 +405,7 @@ __device__ __forceinline__ void int4_consumer(const Int4Params& a, const Plan& p
             jt[n][e] = R / p.G;
             if (R < rows_total) in_rows |= 1 << (2 * n + e);
             lim[n][e] = INT_MAX;
-            sq[n][e] = qk[n][e] = 0.f;
+            sq[n][e] = 0.f;
         }
 
     for (int st = 0, k = pl.cs; k < pl.ce; ++k, ++st) {
@@ -320,73 +414,74 @@ __device__ __forceinline__ void int4_consumer(const Int4Params& a, const Plan& p
             if (lane == 0) raise_flag(p.err_flag, PA_ERRBIT_WAIT_TIMEOUT);
             return;
         }
-        const I4Desc d = descs[slot];
-        const uint8_t* kc = base + slot * p.stage_bytes;
-        const uint8_t* kp = kc + a.code_bytes;
-        const uint8_t* vc = kp + a.param_bytes;
-        const uint8_t* vp = vc + a.code_bytes;
+        const I4Head d = descs[slot].h;
+        const uint32_t vmask = descs[slot].vmask[ts];
+        const uint32_t stage = base32 + slot * p.stage_bytes;
         if (d.flags & SEG_START) {
             if (d.flags & QLOAD) {
                 // The B operand of this lane: row g4 of each tile, dimensions
-                // [D/4 * t4, D/4 * (t4 + 1)) in the codes' order.  bf16 rows are
-                // scaled by a power of two into f16's range (their 8 bits fit).
+                // [D/4 * t4, D/4 * (t4 + 1)) in the codes' order.  For bf16 rows a
+                // power of two puts the warp's largest element into [2^13, 2^14):
+                // their 8 bits fit an f16, except in elements below 2^-28 of the
+                // largest, which are rounded to a multiple of 2^-38 of it.
                 const uint8_t* qb = base + p.q_off + d.qslot * p.q_slot_bytes;
+                uint32_t raw[NQT][KW][4];
 #pragma unroll
                 for (int n = 0; n < NQT; ++n) {
                     const int R = (rt * NQT + n) * 8 + g4, jj = R / p.G;
                     const bool on = R < rows_total && jj < d.qn;
                     const uint4* src = reinterpret_cast<const uint4*>(
                         qb + (static_cast<size_t>(jj * p.HPC + hl) * p.G + (R - jj * p.G)) * D * 2 + t4 * (D / 2));
-                    uint32_t raw[KW][4];
 #pragma unroll
                     for (int x = 0; x < KW; ++x) {
                         const uint4 r = on ? src[x] : make_uint4(0, 0, 0, 0);
-                        raw[x][0] = r.x; raw[x][1] = r.y; raw[x][2] = r.z; raw[x][3] = r.w;
+                        raw[n][x][0] = r.x; raw[n][x][1] = r.y; raw[n][x][2] = r.z; raw[n][x][3] = r.w;
                     }
-                    float f = 1.f;
-                    if constexpr (QT::code == PA_BF16) {
-                        float mx = 0.f;
+                }
+                auto pair = [&](uint32_t x) -> float2 {
+                    if constexpr (QT::code == PA_BF16) return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&x));
+                    else return __half22float2(*reinterpret_cast<const __half2*>(&x));
+                };
+                float f = 1.f;
+                if constexpr (QT::code == PA_BF16) {
+                    float mx = 0.f;
+#pragma unroll
+                    for (int n = 0; n < NQT; ++n)
 #pragma unroll
                         for (int x = 0; x < KW; ++x)
 #pragma unroll
                             for (int y = 0; y < 4; ++y) {
-                                const float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw[x][y]));
+                                const float2 v = pair(raw[n][x][y]);
                                 mx = fmaxf(mx, fmaxf(fabsf(v.x), fabsf(v.y)));
                             }
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                        // 2^(13 - exponent of the largest), from its exponent bits
-                        const int ex = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
-                        if (mx > 0.f && ex < 128) f = __uint_as_float(static_cast<uint32_t>(min(13 - ex, 126) + 127) << 23);
 #pragma unroll
-                        for (int x = 0; x < KW; ++x)
+                    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                    // 2^(13 - exponent of the largest), from its exponent bits
+                    const int ex = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
+                    if (mx > 0.f && ex < 128) f = __uint_as_float(static_cast<uint32_t>(min(13 - ex, 126) + 127) << 23);
+                }
+                const float qk = p.qk_scale / f;
+                unit_qk = qk * UNIT;
 #pragma unroll
-                            for (int y = 0; y < 4; ++y) {
-                                const float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw[x][y]));
-                                raw[x][y] = f32x2_to_f16x2(v.x * f, v.y * f);
-                            }
-                    }
+                for (int n = 0; n < NQT; ++n) {
                     float s = 0.f;
 #pragma unroll
                     for (int x = 0; x < KW; ++x) {
                         // words hold dims (0,1) (2,3) (4,5) (6,7): pairs (0,4) (2,6) (1,5) (3,7)
-                        qf[n][x][0] = __byte_perm(raw[x][0], raw[x][2], 0x5410);
-                        qf[n][x][1] = __byte_perm(raw[x][1], raw[x][3], 0x5410);
-                        qf[n][x][2] = __byte_perm(raw[x][0], raw[x][2], 0x7632);
-                        qf[n][x][3] = __byte_perm(raw[x][1], raw[x][3], 0x7632);
+                        float2 v[4];
 #pragma unroll
                         for (int y = 0; y < 4; ++y) {
-                            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&raw[x][y]));
-                            s += v.x + v.y;
+                            v[y] = pair(raw[n][x][y]);
+                            s += v[y].x + v[y].y;
                         }
+                        sts128(qf + (n * KW + x) * 512u,
+                               make_uint4(f32x2_to_f16x2(v[0].x * f, v[2].x * f), f32x2_to_f16x2(v[1].x * f, v[3].x * f),
+                                          f32x2_to_f16x2(v[0].y * f, v[2].y * f), f32x2_to_f16x2(v[1].y * f, v[3].y * f)));
                     }
                     s += __shfl_xor_sync(0xffffffffu, s, 1);
                     s += __shfl_xor_sync(0xffffffffu, s, 2);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        sq[n][e] = __shfl_sync(0xffffffffu, s, (2 * t4 + e) * 4);
-                        qk[n][e] = p.qk_scale / __shfl_sync(0xffffffffu, f, (2 * t4 + e) * 4);
-                    }
+                    for (int e = 0; e < 2; ++e) sq[n][e] = __shfl_sync(0xffffffffu, s, (2 * t4 + e) * 4) * p.qk_scale;
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&qempty[d.qslot]);
@@ -397,188 +492,227 @@ __device__ __forceinline__ void int4_consumer(const Int4Params& a, const Plan& p
                 for (int o = 0; o < OT; ++o) acc[o][n][0] = acc[o][n][1] = acc[o][n][2] = acc[o][n][3] = 0.f;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    m[n][e] = -INFINITY; l[n][e] = 0.f; c0[n][e] = 0.f;
+                    m[n][e] = top[n][e] = -INFINITY; mu[n][e] = l[n][e] = c0[n][e] = 0.f;
                     if (p.q_start) lim[n][e] = ((in_rows >> (2 * n + e)) & 1) && jt[n][e] < d.qn ? d.qpos0 + jt[n][e] : -1;
                 }
             }
-            inv = 0.f;
+            inv = step_top = 0.f;
         }
-        // ---- S^T = K Q^T over the chunk's tokens ----
-        float s[I4_MT][NQT][4];
+#pragma unroll 1
+        for (int sub = 0; sub < SUBS; ++sub) {
+            uint32_t c[2 * MT], pr[2 * MT];
 #pragma unroll
-        for (int mt = 0; mt < I4_MT; ++mt) {
-            const uint32_t r0 = row_of(16 * mt + tk), r1 = row_of(16 * mt + 8 + tk);
-            uint32_t ka[KW], kb[KW];
-            if constexpr (KW == 4) {
-                const uint4 x = *reinterpret_cast<const uint4*>(kc + r0 * (D / 2) + t4 * 16);
-                const uint4 y = *reinterpret_cast<const uint4*>(kc + r1 * (D / 2) + t4 * 16);
-                ka[0] = x.x; ka[1] = x.y; ka[2] = x.z; ka[3] = x.w;
-                kb[0] = y.x; kb[1] = y.y; kb[2] = y.z; kb[3] = y.w;
-            } else {
-                const uint2 x = *reinterpret_cast<const uint2*>(kc + r0 * (D / 2) + t4 * 8);
-                const uint2 y = *reinterpret_cast<const uint2*>(kc + r1 * (D / 2) + t4 * 8);
-                ka[0] = x.x; ka[1] = x.y; kb[0] = y.x; kb[1] = y.y;
+            for (int x = 0; x < 2 * MT; ++x) {
+                c[x] = stage + (SUBS > 1 && sub ? c8[(2 * MT + x) % (I4_WT / 8)] : c8[x]);
+                pr[x] = stage + (SUBS > 1 && sub ? p8[(2 * MT + x) % (I4_WT / 8)] : p8[x]);
             }
-            float lo[NQT][4], hi[NQT][4];
+            const int tok0 = d.tok0 + I4_WT * ts + 16 * MT * sub;
+            const uint32_t vm = vmask >> (16 * MT * sub);
+            constexpr uint32_t ALL = MT == 2 ? 0xffffffffu : 0xffffu;
+            const bool all = (vm & ALL) == ALL;
+            // ---- S^T = K Q^T ----
+            // The steps along head_dim run outside the tiles: each product then
+            // has 2 MT accumulators (the low and the high nibbles' of each
+            // tile), whose dependent MMAs are that far apart.
+            float s[MT][NQT][4];
+            {
+                uint32_t ka[MT][KW], kb[MT][KW];
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    const uint32_t at = c[2 * mt] + ok, bt = c[2 * mt + 1] + ok;
+                    if constexpr (KW == 4) {
+                        const uint4 x = lds128(at), y = lds128(bt);
+                        ka[mt][0] = x.x; ka[mt][1] = x.y; ka[mt][2] = x.z; ka[mt][3] = x.w;
+                        kb[mt][0] = y.x; kb[mt][1] = y.y; kb[mt][2] = y.z; kb[mt][3] = y.w;
+                    } else {
+                        const uint2 x = lds64(at), y = lds64(bt);
+                        ka[mt][0] = x.x; ka[mt][1] = x.y; kb[mt][0] = y.x; kb[mt][1] = y.y;
+                    }
+                }
+                float hi[MT][NQT][4];
+#pragma unroll
+                for (int x = 0; x < KW; ++x) {
+                    uint4 f[NQT];
+#pragma unroll
+                    for (int n = 0; n < NQT; ++n) f[n] = lds128(qf + (n * KW + x) * 512u);
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        const uint32_t a8 = ka[mt][x] >> 8, b8 = kb[mt][x] >> 8;
+                        const uint32_t A1[4] = {ka[mt][x] & 0x000f000fu, kb[mt][x] & 0x000f000fu, a8 & 0x000f000fu, b8 & 0x000f000fu};
+                        const uint32_t A2[4] = {ka[mt][x] & 0x00f000f0u, kb[mt][x] & 0x00f000f0u, a8 & 0x00f000f0u, b8 & 0x00f000f0u};
+#pragma unroll
+                        for (int n = 0; n < NQT; ++n) {
+                            if (x == 0) {
+                                mma_16816_zero(s[mt][n], A1, f[n].x, f[n].y);
+                                mma_16816_zero(hi[mt][n], A2, f[n].z, f[n].w);
+                            } else {
+                                mma_16816<false>(s[mt][n], A1, f[n].x, f[n].y);
+                                mma_16816<false>(hi[mt][n], A2, f[n].z, f[n].w);
+                            }
+                        }
+                    }
+                }
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    const float2 p0 = lds_params(pr[2 * mt] + POFF), p1 = lds_params(pr[2 * mt + 1] + POFF);
+                    const float s0 = p0.x * unit_qk, s1 = p1.x * unit_qk;
+#pragma unroll
+                    for (int n = 0; n < NQT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            s[mt][n][e] = fmaf(fmaf(hi[mt][n][e], 0.0625f, s[mt][n][e]), e < 2 ? s0 : s1, (e < 2 ? p0.y : p1.y) * sq[n][e & 1]);
+                }
+            }
+            // tokens that do not exist, or lie behind a row's position
+            if (!all || (p.q_start && tok0 + 16 * MT - 1 > d.qpos0)) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int n = 0; n < NQT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int t = 16 * mt + 8 * (e >> 1) + tk;
+                            if (!((vm >> t) & 1u) || tok0 + t > lim[n][e & 1]) s[mt][n][e] = -INFINITY;
+                        }
+            }
+            // ---- V parameters: (step, low) of the lane's two tokens of each tile ----
+            float vs[MT][2], vl[MT][2];
+            float smax = 0.f;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float2 v = lds_params(pr[2 * mt + e] + VOFF + POFF);
+                    vs[mt][e] = v.x; vl[mt][e] = v.y;
+                }
+            if (!all) {                               // the pool may hold NaN where no token is
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        if (!((vm >> (16 * mt + 8 * e + tk)) & 1u)) vs[mt][e] = vl[mt][e] = 0.f;
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) smax = fmaxf(smax, fmaxf(fabsf(vs[mt][0]), fabsf(vs[mt][1])));
+            // ---- online softmax (log2 domain) ----
+            // The reference of a row moves only when a score passes it by more than
+            // 2^8, and the power of two on the steps only when a step passes 2^7
+            // with it: weights then stay below 2^15, within f16, and a chunk mostly
+            // needs no exchange between lanes but one vote.
+            float mx[NQT][2];
+            bool far = smax > step_top;
 #pragma unroll
             for (int n = 0; n < NQT; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) lo[n][e] = hi[n][e] = 0.f;
+                for (int e = 0; e < 2; ++e) {
+                    mx[n][e] = -INFINITY;
 #pragma unroll
-            for (int x = 0; x < KW; ++x) {
-                const uint32_t a8 = ka[x] >> 8, b8 = kb[x] >> 8;
-                const uint32_t A1[4] = {ka[x] & 0x000f000fu, kb[x] & 0x000f000fu, a8 & 0x000f000fu, b8 & 0x000f000fu};
-                const uint32_t A2[4] = {ka[x] & 0x00f000f0u, kb[x] & 0x00f000f0u, a8 & 0x00f000f0u, b8 & 0x00f000f0u};
+                    for (int mt = 0; mt < MT; ++mt) mx[n][e] = fmaxf(mx[n][e], fmaxf(s[mt][n][e], s[mt][n][e + 2]));
+                    far = far || mx[n][e] > top[n][e];
+                }
+            if (__any_sync(0xffffffffu, far)) {
+                smax = max_g4(smax);
+                float grow = 1.f;
+                if (smax > step_top) {
+                    const int ex = static_cast<int>(__float_as_uint(smax) >> 23) - 127;
+                    const float ni = __uint_as_float(static_cast<uint32_t>(1 - ex + 127) << 23);   // steps into [2, 4)
+                    if (inv != 0.f) grow = ni / inv;
+                    inv = ni;
+                    step_top = 128.f / ni;
+                }
 #pragma unroll
                 for (int n = 0; n < NQT; ++n) {
-                    mma_16816<false>(lo[n], A1, qf[n][x][0], qf[n][x][1]);
-                    mma_16816<false>(hi[n], A2, qf[n][x][2], qf[n][x][3]);
+                    float f[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float mn = fmaxf(m[n][e], max_g4(mx[n][e]));
+                        const float al = m[n][e] == mn ? 1.f : ex2_approx(m[n][e] - mn);
+                        m[n][e] = mn;
+                        top[n][e] = mn + 8.f;
+                        mu[n][e] = mn == -INFINITY ? 0.f : mn;
+                        l[n][e] *= al;
+                        c0[n][e] *= al;
+                        f[e] = al * grow;
+                    }
+#pragma unroll
+                    for (int o = 0; o < OT; ++o) {
+                        acc[o][n][0] *= f[0]; acc[o][n][1] *= f[1]; acc[o][n][2] *= f[0]; acc[o][n][3] *= f[1];
+                    }
                 }
             }
-            const float2 p0 = __half22float2(*reinterpret_cast<const __half2*>(kp + r0 * 4));
-            const float2 p1 = __half22float2(*reinterpret_cast<const __half2*>(kp + r1 * 4));
-            const float s0 = p0.x * UNIT, s1 = p1.x * UNIT;
+            uint32_t pf[MT][NQT][2], pl_[HL ? MT : 1][NQT][2];
 #pragma unroll
             for (int n = 0; n < NQT; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float dot = fmaf(hi[n][e], 0.0625f, lo[n][e]);
-                    s[mt][n][e] = fmaf(dot, e < 2 ? s0 : s1, (e < 2 ? p0.y : p1.y) * sq[n][e & 1]) * qk[n][e & 1];
-                }
-        }
-        // tokens that do not exist, or lie behind a row's position
-        const bool all = d.vmask == ~0ull;
-        if (!all || (p.q_start && d.tok0 + I4_CT - 1 > d.qpos0)) {
+                for (int e = 0; e < 2; ++e) {
 #pragma unroll
-            for (int mt = 0; mt < I4_MT; ++mt)
-#pragma unroll
-                for (int n = 0; n < NQT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int t = 16 * mt + 8 * (e >> 1) + tk;
-                        if (!((d.vmask >> t) & 1ull) || d.tok0 + t > lim[n][e & 1]) s[mt][n][e] = -INFINITY;
+                    for (int mt = 0; mt < MT; ++mt) {
+                        s[mt][n][e] = ex2_approx(s[mt][n][e] - mu[n][e]);
+                        s[mt][n][e + 2] = ex2_approx(s[mt][n][e + 2] - mu[n][e]);
+                        l[n][e] += s[mt][n][e] + s[mt][n][e + 2];
+                        c0[n][e] = fmaf(s[mt][n][e], vl[mt][0], fmaf(s[mt][n][e + 2], vl[mt][1], c0[n][e]));
                     }
-        }
-        // ---- V parameters: (step, low) of the lane's two tokens of each tile ----
-        float vs[I4_MT][2], vl[I4_MT][2];
-        float smax = 0.f;
-#pragma unroll
-        for (int mt = 0; mt < I4_MT; ++mt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int t = 16 * mt + 8 * e + tk;
-                float2 v = __half22float2(*reinterpret_cast<const __half2*>(vp + row_of(t) * 4));
-                if (!all && !((d.vmask >> t) & 1ull)) v = make_float2(0.f, 0.f);   // the pool may hold NaN there
-                vs[mt][e] = v.x; vl[mt][e] = v.y;
-                smax = fmaxf(smax, fabsf(v.x));
-            }
-        // Weights p * step enter an f16 operand: a power of two, common to the
-        // segment, keeps the largest step's in [2^9, 2^15].
-        smax = max_g4(smax);
-        float grow = 1.f;
-        if ((inv == 0.f && smax > 0.f) || smax * inv > 32768.f) {
-            const int ex = static_cast<int>(__float_as_uint(smax) >> 23) - 127;
-            const float ni = __uint_as_float(static_cast<uint32_t>(9 - ex + 127) << 23);
-            if (inv != 0.f) grow = ni / inv;
-            inv = ni;
-        }
-        // ---- online softmax (log2 domain) of the rows ----
-        uint32_t pf[I4_MT][NQT][2], pl_[HL ? I4_MT : 1][NQT][2];
-        float al[NQT][2];
-        bool same = grow == 1.f;
-#pragma unroll
-        for (int n = 0; n < NQT; ++n) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float mx = -INFINITY;
-#pragma unroll
-                for (int mt = 0; mt < I4_MT; ++mt) mx = fmaxf(mx, fmaxf(s[mt][n][e], s[mt][n][e + 2]));
-                const float mn = fmaxf(m[n][e], max_g4(mx));
-                const float mu = mn == -INFINITY ? 0.f : mn;
-                al[n][e] = ex2_approx(m[n][e] - mu);
-                m[n][e] = mn;
-                same = same && al[n][e] == 1.f;
-                float ps = 0.f, cs = 0.f;
-#pragma unroll
-                for (int mt = 0; mt < I4_MT; ++mt) {
-                    s[mt][n][e] = ex2_approx(s[mt][n][e] - mu);
-                    s[mt][n][e + 2] = ex2_approx(s[mt][n][e + 2] - mu);
-                    ps += s[mt][n][e] + s[mt][n][e + 2];
-                    cs = fmaf(s[mt][n][e], vl[mt][0], fmaf(s[mt][n][e + 2], vl[mt][1], cs));
                 }
-                l[n][e] = fmaf(l[n][e], al[n][e], ps);
-                c0[n][e] = fmaf(c0[n][e], al[n][e], cs);
-            }
-        }
 #pragma unroll
-        for (int mt = 0; mt < I4_MT; ++mt) {
-            const float w0 = vs[mt][0] * inv, w1 = vs[mt][1] * inv;
+            for (int mt = 0; mt < MT; ++mt) {
+                const float w0 = vs[mt][0] * inv, w1 = vs[mt][1] * inv;
 #pragma unroll
-            for (int n = 0; n < NQT; ++n) {
-                const float x0 = s[mt][n][0] * w0, x1 = s[mt][n][1] * w0, x2 = s[mt][n][2] * w1, x3 = s[mt][n][3] * w1;
-                const uint32_t h0 = f32x2_to_f16x2(x0, x1), h1 = f32x2_to_f16x2(x2, x3);
-                pf[mt][n][0] = movmatrix(h0);
-                pf[mt][n][1] = movmatrix(h1);
-                if constexpr (HL) {
-                    const float2 y0 = __half22float2(*reinterpret_cast<const __half2*>(&h0));
-                    const float2 y1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
-                    pl_[mt][n][0] = movmatrix(f32x2_to_f16x2(x0 - y0.x, x1 - y0.y));
-                    pl_[mt][n][1] = movmatrix(f32x2_to_f16x2(x2 - y1.x, x3 - y1.y));
+                for (int n = 0; n < NQT; ++n) {
+                    const float x0 = s[mt][n][0] * w0, x1 = s[mt][n][1] * w0, x2 = s[mt][n][2] * w1, x3 = s[mt][n][3] * w1;
+                    const uint32_t h0 = f32x2_to_f16x2(x0, x1), h1 = f32x2_to_f16x2(x2, x3);
+                    pf[mt][n][0] = movmatrix(h0);
+                    pf[mt][n][1] = movmatrix(h1);
+                    if constexpr (HL) {
+                        const float2 y0 = __half22float2(*reinterpret_cast<const __half2*>(&h0));
+                        const float2 y1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
+                        pl_[mt][n][0] = movmatrix(f32x2_to_f16x2(x0 - y0.x, x1 - y0.y));
+                        pl_[mt][n][1] = movmatrix(f32x2_to_f16x2(x2 - y1.x, x3 - y1.y));
+                    }
                 }
             }
-        }
-        if (!__all_sync(0xffffffffu, same)) {
+            // ---- O^T += V^T P^T ----
 #pragma unroll
-            for (int n = 0; n < NQT; ++n) {
-                const float f0 = al[n][0] * grow, f1 = al[n][1] * grow;
+            for (int mt = 0; mt < MT; ++mt) {
+                // k columns 2 t4, 2 t4 + 1 and 8 on: four tokens of D / 8 dimensions
+                const uint32_t r[4] = {c[2 * mt] + ov0 + VOFF, c[2 * mt] + ov1 + VOFF, c[2 * mt + 1] + ov0 + VOFF,
+                                       c[2 * mt + 1] + ov1 + VOFF};
+                constexpr int VW = D / 64;            // code words of a value that a lane reads
+                uint32_t v[4][VW];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    if constexpr (VW == 2) {
+                        const uint2 y = lds64(r[x]);
+                        v[x][0] = y.x; v[x][1] = y.y;
+                    } else {
+                        v[x][0] = lds32(r[x]);
+                    }
+                }
+                // pairs of tokens: q[half][word * 2 + upper] holds 4 dimensions of two tokens
+                uint32_t q[2][2 * VW], q8[2][2 * VW];
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int y = 0; y < VW; ++y) {
+                        q[x][2 * y] = __byte_perm(v[2 * x][y], v[2 * x + 1][y], 0x5410);
+                        q[x][2 * y + 1] = __byte_perm(v[2 * x][y], v[2 * x + 1][y], 0x7632);
+                        q8[x][2 * y] = q[x][2 * y] >> 8;
+                        q8[x][2 * y + 1] = q[x][2 * y + 1] >> 8;
+                    }
 #pragma unroll
                 for (int o = 0; o < OT; ++o) {
-                    acc[o][n][0] *= f0; acc[o][n][1] *= f1; acc[o][n][2] *= f0; acc[o][n][3] *= f1;
-                }
-            }
-        }
-        // ---- O^T += V^T P^T ----
+                    // head_dim 128: tile o has dimensions 16 g4 + o and 16 g4 + 8 + o (nibble o of both words);
+                    // 64: 8 g4 + o and 8 g4 + 4 + o (nibbles o and o + 4 of the one word)
+                    constexpr int step = VW == 2 ? 2 : 1;
+                    const int ia = VW == 2 ? o / 4 : 0, ib = ia + step;
+                    const int nib = VW == 2 ? o % 4 : o;
+                    const uint32_t mask = (nib & 1) ? 0x00f000f0u : 0x000f000fu;
+                    const uint32_t A[4] = {(nib < 2 ? q[0][ia] : q8[0][ia]) & mask, (nib < 2 ? q[0][ib] : q8[0][ib]) & mask,
+                                           (nib < 2 ? q[1][ia] : q8[1][ia]) & mask, (nib < 2 ? q[1][ib] : q8[1][ib]) & mask};
 #pragma unroll
-        for (int mt = 0; mt < I4_MT; ++mt) {
-            // k columns 2 t4, 2 t4 + 1 and 8 on: four tokens of D / 8 dimensions
-            const uint32_t r[4] = {row_of(16 * mt + tv0), row_of(16 * mt + tv1), row_of(16 * mt + 8 + tv0),
-                                   row_of(16 * mt + 8 + tv1)};
-            constexpr int VW = D / 64;            // code words of a value that a lane reads
-            uint32_t v[4][VW];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                if constexpr (VW == 2) {
-                    const uint2 y = *reinterpret_cast<const uint2*>(vc + r[x] * (D / 2) + g4 * 8);
-                    v[x][0] = y.x; v[x][1] = y.y;
-                } else {
-                    v[x][0] = *reinterpret_cast<const uint32_t*>(vc + r[x] * (D / 2) + g4 * 4);
-                }
-            }
-            // pairs of tokens: q[half][word * 2 + upper] holds 4 dimensions of two tokens
-            uint32_t q[2][2 * VW], q8[2][2 * VW];
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-#pragma unroll
-                for (int y = 0; y < VW; ++y) {
-                    q[x][2 * y] = __byte_perm(v[2 * x][y], v[2 * x + 1][y], 0x5410);
-                    q[x][2 * y + 1] = __byte_perm(v[2 * x][y], v[2 * x + 1][y], 0x7632);
-                    q8[x][2 * y] = q[x][2 * y] >> 8;
-                    q8[x][2 * y + 1] = q[x][2 * y + 1] >> 8;
-                }
-#pragma unroll
-            for (int o = 0; o < OT; ++o) {
-                // head_dim 128: tile o has dimensions 16 g4 + o and 16 g4 + 8 + o (nibble o of both words);
-                // 64: 8 g4 + o and 8 g4 + 4 + o (nibbles o and o + 4 of the one word)
-                constexpr int step = VW == 2 ? 2 : 1;
-                const int ia = VW == 2 ? o / 4 : 0, ib = ia + step;
-                const int nib = VW == 2 ? o % 4 : o;
-                const uint32_t mask = (nib & 1) ? 0x00f000f0u : 0x000f000fu;
-                const uint32_t A[4] = {(nib < 2 ? q[0][ia] : q8[0][ia]) & mask, (nib < 2 ? q[0][ib] : q8[0][ib]) & mask,
-                                       (nib < 2 ? q[1][ia] : q8[1][ia]) & mask, (nib < 2 ? q[1][ib] : q8[1][ib]) & mask};
-#pragma unroll
-                for (int n = 0; n < NQT; ++n) {
-                    mma_16816<false>(acc[o][n], A, pf[mt][n][0], pf[mt][n][1]);
-                    if constexpr (HL) mma_16816<false>(acc[o][n], A, pl_[mt][n][0], pl_[mt][n][1]);
+                    for (int n = 0; n < NQT; ++n) {
+                        mma_16816<false>(acc[o][n], A, pf[mt][n][0], pf[mt][n][1]);
+                        if constexpr (HL) mma_16816<false>(acc[o][n], A, pl_[mt][n][0], pl_[mt][n][1]);
+                    }
                 }
             }
         }
@@ -587,25 +721,64 @@ __device__ __forceinline__ void int4_consumer(const Int4Params& a, const Plan& p
         if (d.flags & SEG_END) {
             const bool direct = (d.flags & DIRECT) != 0;
             const float back = inv > 0.f ? UNIT / inv : 0.f;
+            // warps ts > 0 hand (m, l, values) of their tokens to warp ts = 0
+            constexpr int JF = D / 8 + 2;                 // floats per lane, tile and row of the pair
+            float* jb = reinterpret_cast<float*>(base + a.join_off) + static_cast<size_t>(tile * (a.TS - 1)) * NQT * 2 * JF * 32 + lane;
+            uint64_t* jfull = joined + 2 * tile;
+            uint64_t* jfree = jfull + 1;
+            if (a.TS > 1) {
+                if (ts > 0) {
+                    if (joins > 0 && !mbar_wait_bounded(jfree, (joins - 1) & 1u)) {
+                        if (lane == 0) raise_flag(p.err_flag, PA_ERRBIT_WAIT_TIMEOUT);
+                        return;
+                    }
+                } else if (!mbar_wait_bounded(jfull, joins & 1u)) {
+                    if (lane == 0) raise_flag(p.err_flag, PA_ERRBIT_WAIT_TIMEOUT);
+                    return;
+                }
+                ++joins;
+            }
 #pragma unroll
             for (int n = 0; n < NQT; ++n)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float lt = sum_g4(l[n][e]), ct = sum_g4(c0[n][e]);
-                    const bool on = ((in_rows >> (2 * n + e)) & 1) && jt[n][e] < d.qn && (direct || d.slot < p.max_slots);
-                    if (!on) continue;
-                    const int R = (rt * NQT + n) * 8 + 2 * t4 + e;
-                    const int head = (hg * p.HPC + hl) * p.G + (R - jt[n][e] * p.G);
-                    const float sc = direct ? (lt == 0.f ? 0.f : 1.f / lt) : 1.f;
+                    float lt = sum_g4(l[n][e]);
+                    const float ct = sum_g4(c0[n][e]);
                     // the lane's D / 8 dimensions from D / 8 * g4 on, in order
                     float v[D / 8];
 #pragma unroll
                     for (int o = 0; o < OT; ++o) {
                         const float u = (o & 1) ? back * 0.0625f : back;
-                        v[o] = fmaf(acc[o][n][e], u, ct) * sc;
-                        v[OT + o] = fmaf(acc[o][n][2 + e], u, ct) * sc;
+                        v[o] = fmaf(acc[o][n][e], u, ct);
+                        v[OT + o] = fmaf(acc[o][n][2 + e], u, ct);
                     }
+                    if (ts > 0) {
+                        float* b = jb + static_cast<size_t>(((ts - 1) * NQT + n) * 2 + e) * JF * 32;
+                        b[0] = m[n][e];
+                        b[32] = lt;
+#pragma unroll
+                        for (int x = 0; x < D / 8; ++x) b[(2 + x) * 32] = v[x];
+                        continue;
+                    }
+                    float mr = m[n][e];
+                    for (int x = 1; x < a.TS; ++x) {
+                        const float* b = jb + static_cast<size_t>(((x - 1) * NQT + n) * 2 + e) * JF * 32;
+                        const float m2 = b[0], mn = fmaxf(mr, m2);
+                        const float mu = mn == -INFINITY ? 0.f : mn;
+                        const float f1 = ex2_approx(mr - mu), f2 = ex2_approx(m2 - mu);
+                        mr = mn;
+                        lt = lt * f1 + b[32] * f2;
+#pragma unroll
+                        for (int y = 0; y < D / 8; ++y) v[y] = v[y] * f1 + b[(2 + y) * 32] * f2;
+                    }
+                    const bool on = ((in_rows >> (2 * n + e)) & 1) && jt[n][e] < d.qn && (direct || d.slot < p.max_slots);
+                    if (!on) continue;
+                    const int R = (rt * NQT + n) * 8 + 2 * t4 + e;
+                    const int head = (hg * p.HPC + hl) * p.G + (R - jt[n][e] * p.G);
                     if (direct) {
+                        const float sc = lt == 0.f ? 0.f : 1.f / lt;
+#pragma unroll
+                        for (int x = 0; x < D / 8; ++x) v[x] *= sc;
                         uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(p.out) +
                                                             (static_cast<size_t>(d.qrow0 + jt[n][e]) * p.Hq + head) * D + g4 * (D / 8));
 #pragma unroll
@@ -617,10 +790,14 @@ __device__ __forceinline__ void int4_consumer(const Int4Params& a, const Plan& p
                         float4* o = reinterpret_cast<float4*>(p.part_acc + prow * D + g4 * (D / 8));
 #pragma unroll
                         for (int x = 0; x < D / 32; ++x) o[x] = make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
-                        if (g4 == 0) p.part_ml[prow] = make_float2(m[n][e], lt);
+                        if (g4 == 0) p.part_ml[prow] = make_float2(mr, lt);
                     }
                 }
-            if ((d.flags & GAP) && !direct && d.slot + 1 < p.max_slots) {
+            if (a.TS > 1) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(ts > 0 ? jfull : jfree);
+            }
+            if (ts == 0 && (d.flags & GAP) && !direct && d.slot + 1 < p.max_slots) {
                 // the slot that a range end on a partition end skips: an empty partial
                 for (int r = 0; r < 8 * NQT; ++r) {
                     const int R = rt * NQT * 8 + r, jj = R / p.G;
@@ -635,9 +812,10 @@ __device__ __forceinline__ void int4_consumer(const Int4Params& a, const Plan& p
     }
 }
 
-// MAXW: consumer warps at most; 4 leaves the registers for two CTAs per SM.
-template <class QT, int D, int NQT, bool HL, int MAXW>
-__global__ void __launch_bounds__((MAXW + 1) * 32, MAXW <= 4 ? 2 : 1)
+// MAXW: consumer warps at most, CTAS: CTAs per SM that the registers are
+// limited for.
+template <class QT, int D, int NQT, bool HL, int MAXW, int CTAS>
+__global__ void __launch_bounds__((MAXW + 1) * 32, CTAS)
 int4_decode_kernel(const __grid_constant__ Int4Params a) {
     extern __shared__ uint8_t smem_raw[];
     const DecodeParams& p = a.d;
@@ -645,7 +823,8 @@ int4_decode_kernel(const __grid_constant__ Int4Params a) {
     uint64_t* full = reinterpret_cast<uint64_t*>(base + p.bar_off);
     uint64_t* empty = full + I4_MAX_STAGES;
     uint64_t* qempty = empty + I4_MAX_STAGES;
-    I4Desc* descs = reinterpret_cast<I4Desc*>(qempty + I4_NQ);
+    uint64_t* joined = qempty + I4_NQ;                     // (full, free) of each tile's join buffer
+    I4Desc* descs = reinterpret_cast<I4Desc*>(joined + 2 * I4_WARPS);
     int2* scratch = reinterpret_cast<int2*>(descs + I4_MAX_STAGES);
     int4* s_first = reinterpret_cast<int4*>(scratch + 32);
     int2* s_tot = reinterpret_cast<int2*>(s_first + 1);
@@ -661,22 +840,28 @@ int4_decode_kernel(const __grid_constant__ Int4Params a) {
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) {
-            mbar_init(&full[s], 1);
+            mbar_init(&full[s], 33);           // the bulk copies' bytes, and each lane's own copies
             mbar_init(&empty[s], p.NCW);
         }
         for (int s = 0; s < I4_NQ; ++s) mbar_init(&qempty[s], p.NCW);
+        for (int s = 0; s < I4_WARPS; ++s) {
+            mbar_init(&joined[2 * s], max(1, a.TS - 1));
+            mbar_init(&joined[2 * s + 1], 1);
+        }
         fence_barrier_init();
         fence_proxy_async_smem();
     }
     __syncthreads();
     if (warp == p.NCW) int4_producer<D>(a, pl, hg, base, full, empty, qempty, descs);
-    else if (warp < p.NCW) int4_consumer<QT, D, NQT, HL>(a, pl, hg, warp, base, full, empty, qempty, descs);
+    else if (warp < p.NCW) int4_consumer<QT, D, NQT, HL>(a, pl, hg, warp, base, full, empty, qempty, joined, descs);
 }
 
 template <class QT, int D, int NQT, bool HL>
 static const void* int4_fn_w(int ncw) {
-    if (ncw <= 4) return reinterpret_cast<const void*>(&int4_decode_kernel<QT, D, NQT, HL, 4>);
-    return reinterpret_cast<const void*>(&int4_decode_kernel<QT, D, NQT, HL, 8>);
+    // more than four row tiles of a head: 65 to 128 rows, 16 per warp
+    if constexpr (NQT == 2)
+        if (ncw > I4_WARPS) return reinterpret_cast<const void*>(&int4_decode_kernel<QT, D, NQT, HL, 8, 1>);
+    return reinterpret_cast<const void*>(&int4_decode_kernel<QT, D, NQT, HL, I4_WARPS, i4_ctas(NQT)>);
 }
 template <class QT, bool HL>
 static const void* int4_fn(int D, int nqt, int ncw) {
@@ -693,48 +878,55 @@ pa_status decode_int4(const Int4Call& c) {
     const int nqt = rows <= 8 ? 1 : 2;
     const int RT = cdiv_ll(rows, 8 * nqt);
     if (RT > 8) return fail(PA_ERR_UNSUPPORTED, "decode: more than 128 query rows per KV head");
-    // heads per CTA: up to 4 warps (two CTAs per SM), at least one head
+    // Four consumer warps per CTA: HPC heads x RT row tiles x TS warps along
+    // the tokens.  Two or more head groups keep three CTAs per SM within the
+    // 2 x SMs ranges that the workspace has partials for.
     int HPC = 1;
-    for (int h = c.Hkv; h >= 1; --h)
-        if (c.Hkv % h == 0 && h * RT <= std::max(4, RT)) { HPC = h; break; }
-    const int NCW = HPC * RT;
+    for (int h = 4; h > 1; h /= 2)
+        if (c.Hkv % h == 0 && c.Hkv >= 2 * h && h * RT <= I4_WARPS) { HPC = h; break; }
+    const int TS = std::max(1, I4_WARPS / (HPC * RT));
+    const int NCW = HPC * RT * TS, CT = I4_WT * TS;
     Int4Params a{};
     DecodeParams& p = a.d;
     p.out = c.out; p.q = c.q; p.block_tables = c.tables; p.seq_lens = c.lens; p.err_flag = c.err;
     p.B = c.B; p.Hq = c.Hq; p.Hkv = c.Hkv; p.G = G; p.D = D; p.bs = c.bs; p.NB = c.NB; p.MB = c.MB;
     p.out_bytes = 2;
     p.HPC = HPC; p.NHG = c.Hkv / HPC; p.MT = RT; p.NCW = NCW;
-    p.ct = I4_CT;
+    p.ct = CT;
     // partitions are whole chunks
-    p.PC = cdiv_ll(c.partition_tokens, I4_CT);
+    p.PC = cdiv_ll(c.partition_tokens, CT);
     p.q_start = c.q_start; p.QL = c.QL; p.total_q = c.q_start ? c.total_q : c.B;
     p.WQ = 4; p.WS = 3;
     p.qk_scale = c.scale * 1.4426950408889634f;
     p.v_scale = 1.f;
     a.k = static_cast<const uint8_t*>(c.k); a.v = static_cast<const uint8_t*>(c.v);
     a.block_bytes = static_cast<size_t>(c.bs) * c.Hkv * (D / 2 + INT4_PARAM_BYTES);
-    a.code_bytes = static_cast<uint32_t>(HPC * I4_CT * (D / 2));
-    a.param_bytes = static_cast<uint32_t>(HPC * I4_CT * INT4_PARAM_BYTES);
+    a.code_bytes = static_cast<uint32_t>(HPC * CT * (D / 2));
+    a.param_bytes = static_cast<uint32_t>(HPC * CT * INT4_PARAM_BYTES);
     a.RT = RT;
-    a.nbox = c.bs <= I4_CT ? I4_CT / c.bs : 1;
+    a.TS = TS;
+    a.nbox = c.bs <= CT ? CT / c.bs : 1;
+    for (a.bshift = 3; (1 << a.bshift) < c.bs; ++a.bshift) {}
+    for (a.rshift = 3; (1 << a.rshift) < std::min(c.bs, CT); ++a.rshift) {}
     p.stage_bytes = 2 * (a.code_bytes + a.param_bytes);
     p.q_bytes = static_cast<uint32_t>(c.QL * HPC * G * D * 2);
     p.q_slot_bytes = (p.q_bytes + 127u) & ~127u;
-    const uint32_t extras = 1024;
-    const long long fixed = static_cast<long long>(I4_NQ) * p.q_slot_bytes + extras + 128;
+    const uint32_t join = static_cast<uint32_t>(HPC * RT * (TS - 1) * nqt * 2 * (D / 8 + 2) * 32 * 4);
+    const uint32_t frags = static_cast<uint32_t>(NCW * nqt * (D / 32) * 512);
+    const uint32_t extras = 1152;
+    const long long fixed = static_cast<long long>(I4_NQ) * p.q_slot_bytes + join + frags + extras + 128;
     const long long sm = std::min(c.max_smem, 227 * 1024);
     const int threads = (NCW + 1) * 32;
+    const int ctas = NCW <= I4_WARPS ? i4_ctas(nqt) : 1;
     int stages = 0;
-    if (NCW <= 4) {
-        const long long per_cta = (sm + 1024) / 2 - 1024 - fixed;
-        const int s2 = static_cast<int>(std::min<long long>(I4_MAX_STAGES, per_cta / p.stage_bytes));
-        if (s2 >= 2) stages = s2;
-    }
-    if (stages == 0) stages = static_cast<int>(std::min<long long>(I4_MAX_STAGES, (sm - fixed) / p.stage_bytes));
+    for (int n = ctas; n >= 1 && stages < 2; --n)
+        stages = static_cast<int>(std::min<long long>(I4_MAX_STAGES, ((sm + 1024) / n - 1024 - fixed) / p.stage_bytes));
     if (stages < 2) return fail(PA_ERR_UNSUPPORTED, "decode: pipeline stages do not fit in shared memory");
     p.stages = stages;
     p.q_off = stages * p.stage_bytes;
-    p.bar_off = p.q_off + I4_NQ * p.q_slot_bytes;
+    a.join_off = p.q_off + I4_NQ * p.q_slot_bytes;
+    a.frag_off = a.join_off + join;
+    p.bar_off = a.frag_off + frags;
     const size_t smem = 128 + p.bar_off + extras;
     p.split_list = c.ws.split_list; p.totals = c.ws.totals; p.max_slots = c.ws.max_slots;
     p.part_ml = c.ws.part_ml; p.part_acc = c.ws.part_acc;
@@ -746,7 +938,7 @@ pa_status decode_int4(const Int4Call& c) {
     ce = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem);
     if (ce != cudaSuccess) return fail_cuda("decode: occupancy query", ce);
     per_sm = std::max(1, per_sm);
-    const long long chunk_bound = static_cast<long long>(c.B) * cdiv_ll(static_cast<long long>(c.MB) * c.bs, I4_CT);
+    const long long chunk_bound = static_cast<long long>(c.B) * cdiv_ll(static_cast<long long>(c.MB) * c.bs, CT);
     long long NR = std::max(1LL, static_cast<long long>(per_sm) * c.sms / p.NHG);
     NR = std::min(NR, 2LL * c.sms);            // the workspace holds 2 x SMs ranges
     NR = std::min(NR, chunk_bound);
