@@ -160,7 +160,7 @@ static pa_status carve_workspace(void* workspace, size_t bytes, int B, int prow,
 }
 
 pa_status launch_merge(const DecodeParams& p, pa_dtype out, bool split_heads, int sms, cudaStream_t stream) {
-    const void* rkern = reduce_kernel(out, p.D, split_heads);
+    const void* rkern = p.scores ? reduce_kernel_weights(out, p.D) : reduce_kernel(out, p.D, split_heads);
     if (!rkern) return fail(PA_ERR_UNSUPPORTED, "decode: no reduce kernel for this output dtype");
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -191,13 +191,13 @@ pa_status launch_merge(const DecodeParams& p, pa_dtype out, bool split_heads, in
 
 // q_start == nullptr: one query per sequence (decode); otherwise sequence i
 // has q_start[i+1] - q_start[i] <= QL query rows starting at row q_start[i].
-// weights: the output of pa_decode_weights.
+// weights: what pa_decode_weights adds, else null.
 static pa_status decode_impl(bool tc, void* out, const void* q, pa_dtype q_dtype, const void* k_cache,
                              const void* v_cache, pa_dtype kv_dtype, const int32_t* block_tables, int MB,
                              const int32_t* seq_lens, int B, int Hq, int Hkv, int D, int bs, int NB,
                              float scale, float k_scale, float v_scale, int partition_tokens,
                              void* workspace, size_t workspace_bytes, int32_t* err_flag, cudaStream_t stream,
-                             const int32_t* q_start = nullptr, int QL = 1, int total_q = 0, bool weights = false) {
+                             const int32_t* q_start = nullptr, int QL = 1, int total_q = 0, const WeightsOut* weights = nullptr) {
     const bool mq = q_start != nullptr;
     clear_error();
     if (B < 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || bs <= 0 || NB <= 0 || MB <= 0)
@@ -242,7 +242,7 @@ static pa_status decode_impl(bool tc, void* out, const void* q, pa_dtype q_dtype
         DeviceInfo di;
         if (!device_info(di)) return fail(PA_ERR_CUDA, "decode: cannot query the current device");
         Int4Call c{out, q, q_dtype, k_cache, v_cache, block_tables, MB, seq_lens, B, Hq, Hkv, D, bs, NB, scale,
-                   partition_tokens, Workspace{}, err_flag, stream, q_start, QL, total_q, di.sms, di.max_smem};
+                   partition_tokens, Workspace{}, err_flag, stream, q_start, QL, total_q, di.sms, di.max_smem, weights};
         const pa_status st = carve_workspace(workspace, workspace_bytes, B, QL * Hq, D, MB * bs, partition_tokens, di.sms, c.ws);
         return st == PA_OK ? decode_int4(c) : st;
     }
@@ -269,7 +269,8 @@ static pa_status decode_impl(bool tc, void* out, const void* q, pa_dtype q_dtype
     const bool um = mq && !is_fp8(kv_dtype) && QL * (Hq / Hkv) >= 48 && um_rows <= 128 && UH > 0 &&
                     partition_tokens % um_ct == 0;
     const int CT = um ? um_ct : native8 ? 32 : 16;
-    const void* kern = um      ? decode_kernel_mq_um(kv_dtype, q_dtype, D, CT)
+    const void* kern = weights ? decode_kernel_weights(kv_dtype, q_dtype, D)
+                       : um    ? decode_kernel_mq_um(kv_dtype, q_dtype, D, CT)
                        : mq    ? decode_kernel_mq(kv_dtype, q_dtype, D)
                        : fp8t  ? decode_kernel_fp8t(kv_dtype, q_dtype, D)
                        : native8 ? decode_kernel_e4m3(kv_dtype, q_dtype, D)
@@ -386,6 +387,7 @@ static pa_status decode_impl(bool tc, void* out, const void* q, pa_dtype q_dtype
     if (wst != PA_OK) return wst;
     p.split_list = w.split_list; p.totals = w.totals; p.max_slots = w.max_slots;
     p.part_ml = w.part_ml; p.part_acc = w.part_acc;
+    if (weights) { p.scores = weights->scores; p.lse = weights->lse; p.chunk0 = weights->chunk0; }
 
     // tensor maps
     alignas(64) CUtensorMap tk, tv;
@@ -470,16 +472,18 @@ static pa_status decode_impl(bool tc, void* out, const void* q, pa_dtype q_dtype
     ce = cudaLaunchKernelExC(&cfg, kern, args);
     if (ce != cudaSuccess) return fail_cuda("decode: main kernel launch", ce);
 
-    return launch_merge(p, q_dtype, split_heads, dev.sms, stream);
+    const pa_status mst = launch_merge(p, q_dtype, split_heads, dev.sms, stream);
+    return mst == PA_OK && weights ? launch_weights(p, *weights, stream) : mst;
 }
 
-pa_status decode_weights_out(void* out, const void* q, pa_dtype q_dtype, const void* k_cache, const void* v_cache,
-                             pa_dtype kv_dtype, const int32_t* block_tables, int MB, const int32_t* seq_lens, int B,
-                             int Hq, int Hkv, int D, int bs, int NB, float scale, float k_scale, float v_scale,
-                             void* workspace, size_t workspace_bytes, int32_t* err_flag, cudaStream_t stream) {
+pa_status decode_with_weights(const WeightsOut& w, void* out, const void* q, pa_dtype q_dtype, const void* k_cache,
+                              const void* v_cache, pa_dtype kv_dtype, const int32_t* block_tables, int MB,
+                              const int32_t* seq_lens, int B, int Hq, int Hkv, int D, int bs, int NB, float scale,
+                              float k_scale, float v_scale, void* workspace, size_t workspace_bytes,
+                              int32_t* err_flag, cudaStream_t stream) {
     return decode_impl(true, out, q, q_dtype, k_cache, v_cache, kv_dtype, block_tables, MB, seq_lens, B, Hq, Hkv, D,
                        bs, NB, scale, k_scale, v_scale, 0, workspace, workspace_bytes, err_flag, stream, nullptr, 1, 0,
-                       true);
+                       &w);
 }
 
 }  // namespace pa

@@ -341,9 +341,10 @@ __device__ __forceinline__ uint32_t pack_out(float a, float b) {
 // ---------------------------------------------------------------------------
 // consumer: warp w owns NQT tiles of 8 query rows of one KV head.
 // HL: each weight enters the second product as a pair of f16 numbers (the
-// rounded weight and what the rounding lost).
+// rounded weight and what the rounding lost).  WT: pa_decode_weights, the
+// scores and (m, l) are kept.
 // ---------------------------------------------------------------------------
-template <class QT, int D, int NQT, bool HL>
+template <class QT, int D, int NQT, bool HL, bool WT>
 __device__ __forceinline__ void int4_consumer(const Int4Params& a, const Plan& pl, int hg, int w, uint8_t* base,
                                               uint64_t* full, uint64_t* empty, uint64_t* qempty, uint64_t* joined,
                                               const I4Desc* descs) {
@@ -575,6 +576,22 @@ __device__ __forceinline__ void int4_consumer(const Int4Params& a, const Plan& p
                             if (!((vm >> t) & 1u) || tok0 + t > lim[n][e & 1]) s[mt][n][e] = -INFINITY;
                         }
             }
+            if constexpr (WT) {
+                // rows are heads here; 8 lanes store 8 tokens of a head, one sector
+#pragma unroll
+                for (int n = 0; n < NQT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        if ((in_rows >> (2 * n + e)) & 1) {
+                            float* dst = score_row(p, k, (hg * p.HPC + hl) * p.G + (rt * NQT + n) * 8 + 2 * t4 + e) +
+                                         I4_WT * ts + 16 * MT * sub + tk;
+#pragma unroll
+                            for (int mt = 0; mt < MT; ++mt) {
+                                dst[16 * mt] = s[mt][n][e];
+                                dst[16 * mt + 8] = s[mt][n][e + 2];
+                            }
+                        }
+            }
             // ---- V parameters: (step, low) of the lane's two tokens of each tile ----
             float vs[MT][2], vl[MT][2];
             float smax = 0.f;
@@ -775,6 +792,9 @@ __device__ __forceinline__ void int4_consumer(const Int4Params& a, const Plan& p
                     if (!on) continue;
                     const int R = (rt * NQT + n) * 8 + 2 * t4 + e;
                     const int head = (hg * p.HPC + hl) * p.G + (R - jt[n][e] * p.G);
+                    if constexpr (WT) {
+                        if (direct && g4 == 0) p.lse[static_cast<size_t>(d.qrow0) * p.Hq + head] = make_float2(mr, lt);
+                    }
                     if (direct) {
                         const float sc = lt == 0.f ? 0.f : 1.f / lt;
 #pragma unroll
@@ -814,7 +834,7 @@ __device__ __forceinline__ void int4_consumer(const Int4Params& a, const Plan& p
 
 // MAXW: consumer warps at most, CTAS: CTAs per SM that the registers are
 // limited for.
-template <class QT, int D, int NQT, bool HL, int MAXW, int CTAS>
+template <class QT, int D, int NQT, bool HL, bool WT, int MAXW, int CTAS>
 __global__ void __launch_bounds__((MAXW + 1) * 32, CTAS)
 int4_decode_kernel(const __grid_constant__ Int4Params a) {
     extern __shared__ uint8_t smem_raw[];
@@ -853,20 +873,20 @@ int4_decode_kernel(const __grid_constant__ Int4Params a) {
     }
     __syncthreads();
     if (warp == p.NCW) int4_producer<D>(a, pl, hg, base, full, empty, qempty, descs);
-    else if (warp < p.NCW) int4_consumer<QT, D, NQT, HL>(a, pl, hg, warp, base, full, empty, qempty, joined, descs);
+    else if (warp < p.NCW) int4_consumer<QT, D, NQT, HL, WT>(a, pl, hg, warp, base, full, empty, qempty, joined, descs);
 }
 
-template <class QT, int D, int NQT, bool HL>
+template <class QT, int D, int NQT, bool HL, bool WT>
 static const void* int4_fn_w(int ncw) {
     // more than four row tiles of a head: 65 to 128 rows, 16 per warp
     if constexpr (NQT == 2)
-        if (ncw > I4_WARPS) return reinterpret_cast<const void*>(&int4_decode_kernel<QT, D, NQT, HL, 8, 1>);
-    return reinterpret_cast<const void*>(&int4_decode_kernel<QT, D, NQT, HL, I4_WARPS, i4_ctas(NQT)>);
+        if (ncw > I4_WARPS) return reinterpret_cast<const void*>(&int4_decode_kernel<QT, D, NQT, HL, WT, 8, 1>);
+    return reinterpret_cast<const void*>(&int4_decode_kernel<QT, D, NQT, HL, WT, I4_WARPS, i4_ctas(NQT)>);
 }
-template <class QT, bool HL>
+template <class QT, bool HL, bool WT>
 static const void* int4_fn(int D, int nqt, int ncw) {
-    if (D == 128) return nqt == 1 ? int4_fn_w<QT, 128, 1, HL>(ncw) : int4_fn_w<QT, 128, 2, HL>(ncw);
-    return nqt == 1 ? int4_fn_w<QT, 64, 1, HL>(ncw) : int4_fn_w<QT, 64, 2, HL>(ncw);
+    if (D == 128) return nqt == 1 ? int4_fn_w<QT, 128, 1, HL, WT>(ncw) : int4_fn_w<QT, 128, 2, HL, WT>(ncw);
+    return nqt == 1 ? int4_fn_w<QT, 64, 1, HL, WT>(ncw) : int4_fn_w<QT, 64, 2, HL, WT>(ncw);
 }
 
 static int cdiv_ll(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
@@ -931,7 +951,10 @@ pa_status decode_int4(const Int4Call& c) {
     p.split_list = c.ws.split_list; p.totals = c.ws.totals; p.max_slots = c.ws.max_slots;
     p.part_ml = c.ws.part_ml; p.part_acc = c.ws.part_acc;
 
-    const void* kern = c.q_dtype == PA_F16 ? int4_fn<F16T, true>(D, nqt, NCW) : int4_fn<BF16T, false>(D, nqt, NCW);
+    const bool h = c.q_dtype == PA_F16;
+    const void* kern = c.weights ? (h ? int4_fn<F16T, true, true>(D, nqt, NCW) : int4_fn<BF16T, false, true>(D, nqt, NCW))
+                                 : (h ? int4_fn<F16T, true, false>(D, nqt, NCW) : int4_fn<BF16T, false, false>(D, nqt, NCW));
+    if (c.weights) { p.scores = c.weights->scores; p.lse = c.weights->lse; p.chunk0 = c.weights->chunk0; }
     cudaError_t ce = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (ce != cudaSuccess) return fail_cuda("decode: set shared memory size", ce);
     int per_sm = 0;
@@ -957,7 +980,8 @@ pa_status decode_int4(const Int4Call& c) {
     void* args[] = {&a};
     ce = cudaLaunchKernelExC(&cfg, kern, args);
     if (ce != cudaSuccess) return fail_cuda("decode: main kernel launch", ce);
-    return launch_merge(p, c.q_dtype, c.partition_tokens > 0, c.sms, c.stream);
+    const pa_status st = launch_merge(p, c.q_dtype, c.partition_tokens > 0, c.sms, c.stream);
+    return st == PA_OK && c.weights ? launch_weights(p, *c.weights, c.stream) : st;
 }
 
 }  // namespace pa

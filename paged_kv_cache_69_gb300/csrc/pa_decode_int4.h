@@ -25,6 +25,7 @@ struct Int4Call {
     const int32_t* q_start;       // null: one query token per sequence
     int QL, total_q;
     int sms, max_smem;
+    const WeightsOut* weights;    // null but for pa_decode_weights
 };
 pa_status decode_int4(const Int4Call& c);
 

@@ -107,7 +107,18 @@ struct DecodeParams {
     int q_tma;                // 1: query rows arrive by a 128-B-swizzled tensor copy
     uint32_t q_plane_bytes;   // tcgen05 path: distance between the query slot's 128-B column planes
     int um_rows;              // tcgen05 path: tile rows per KV head (its query rows padded to 32)
+    // pa_decode_weights (else null): the scores of every chunk of the stream,
+    // [chunk][Hq][ct] in log2 units; (m, l) of every sequence and head; each
+    // sequence's first chunk
+    float* scores;
+    float2* lse;              // [B][Hq]
+    int* chunk0;              // [B]
 };
+
+// Where the scores of chunk k and head h start.
+__device__ __forceinline__ float* score_row(const DecodeParams& p, int k, int h) {
+    return p.scores + (static_cast<size_t>(k) * p.Hq + h) * p.ct;
+}
 
 __device__ __forceinline__ int cdiv_i(int a, int b) { return (a + b - 1) / b; }
 
@@ -290,6 +301,7 @@ __device__ inline void make_plan(const DecodeParams& p, int range, int2* scratch
         for (int i = i0; i < i1; ++i) {
             const int L = clamp_len(p.seq_lens[i], maxL);
             const int nch = cdiv_i(L, p.ct), nu = n_units(L, p.PC, p.ct);
+            if (p.chunk0) p.chunk0[i] = S;
             if (L == 0) {
                 // no keys: zero outputs for every query row of the sequence
                 int qa, qn;
@@ -370,7 +382,9 @@ struct UmBars {
     uint32_t tmem;            // tensor-memory base address
 };
 
-template <class KV, class QT, int D, bool TC, int CT, bool MQ = false, bool T8 = false, bool UM = false>
+// WT: also keep the scores and the softmax statistics (pa_decode_weights).
+template <class KV, class QT, int D, bool TC, int CT, bool MQ = false, bool T8 = false, bool UM = false,
+          bool WT = false>
 struct DecodeKernel {
     using KT = typename KV::T;
     using QE = typename QT::T;
@@ -387,6 +401,7 @@ struct DecodeKernel {
     static constexpr int KS = D / 16;         // 16-deep k-steps over head_dim
     static constexpr int ROWB = D * KV::bytes;  // bytes of one K/V row
     static constexpr int CPR = ROWB / 16;     // 16-byte chunks per row
+    static_assert(!WT || (CT == 16 && !MQ && !T8 && !UM), "scores are kept by the 16-token decode kernels");
     static_assert(!UM || (MQ && TC && !FP8), "tcgen05 path: several query tokens, 16-bit caches");
     static constexpr int UM_M = 128;          // tcgen05 tile rows: (query token, head) rows of one KV head
     static constexpr int UM_TCOLS = 256;      // tensor-memory columns per CTA: two S buffers, then O
@@ -742,6 +757,10 @@ struct DecodeKernel {
                     else store4<float>(prow + col, v);
                 }
             }
+            if constexpr (WT) {
+                if (direct && ok && t4 == 0)
+                    p.lse[static_cast<size_t>(d.qrow0) * p.Hq + ri.head[hh]] = make_float2(hh ? m1 : m0, hh ? lt1 : lt0);
+            }
             if (!direct && ok && t4 == 0)
                 p.part_ml[(static_cast<size_t>(d.slot) * p.QL + ri.j[hh]) * p.Hq + ri.head[hh]] =
                     make_float2(hh ? m1 : m0, hh ? lt1 : lt0);
@@ -868,6 +887,16 @@ struct DecodeKernel {
                     if constexpr (MQ) keep = keep && d.tok0 + col <= (e < 2 ? lim0 : lim1);
                     s[nt][e] = keep ? s[nt][e] * p.qk_scale : -INFINITY;
                 }
+            if constexpr (WT) {
+                // rows g4 and g4 + 8: four lanes store 8 tokens, one sector
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                    if (!ri.in[hh]) continue;
+                    float* dst = score_row(p, k, ri.head[hh]) + 2 * t4;
+                    *reinterpret_cast<float2*>(dst) = make_float2(s[0][2 * hh], s[0][2 * hh + 1]);
+                    *reinterpret_cast<float2*>(dst + 8) = make_float2(s[1][2 * hh], s[1][2 * hh + 1]);
+                }
+            }
             float mx0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
             float mx1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
             mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
@@ -1870,6 +1899,9 @@ struct DecodeKernel {
                 if (r < nr) {
                     float x = s[r] + __shfl_xor_sync(0xffffffffu, s[r], 16);
                     x = valid ? x * p.qk_scale : -INFINITY;
+                    if constexpr (WT) {
+                        if (half == 0) score_row(p, k, out_h0 + r)[tq] = x;
+                    }
                     float cm = x;
                     cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, 1));
                     cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, 2));
@@ -1919,6 +1951,9 @@ struct DecodeKernel {
                             QE* row = o + static_cast<size_t>(out_h0 + r) * D + c0;
 #pragma unroll
                             for (int c = 0; c < DPL; ++c) row[c] = from_float<QE>(acc[r][c] * inv);
+                            if constexpr (WT) {
+                                if (lane == 0) p.lse[static_cast<size_t>(d.seq) * p.Hq + out_h0 + r] = make_float2(m[r], l[r]);
+                            }
                         }
                     }
                 } else if (d.slot < p.max_slots) {
@@ -1983,11 +2018,12 @@ struct DecodeKernel {
     }
 };
 
-template <class KV, class QT, int D, bool TC, int CT, bool MQ = false, bool T8 = false, bool UM = false>
+template <class KV, class QT, int D, bool TC, int CT, bool MQ = false, bool T8 = false, bool UM = false,
+          bool WT = false>
 __global__ void __launch_bounds__(MAX_WARPS * 32, 1)
 pa_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap tk,
                  const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tq) {
-    using K = DecodeKernel<KV, QT, D, TC, CT, MQ, T8, UM>;
+    using K = DecodeKernel<KV, QT, D, TC, CT, MQ, T8, UM, WT>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(base + p.bar_off);
@@ -2122,7 +2158,7 @@ __host__ __device__ constexpr int red_threads(int wpi) { return wpi == 1 ? RED_T
 // partitioned sequences have hundreds (the CTA's warps split one head's
 // partials, so that a long sequence's reads are spread over 16 warps, and
 // combine their results through shared memory).
-template <typename OutT, int D, int WPI>
+template <typename OutT, int D, int WPI, bool WT = false>
 __global__ void __launch_bounds__(red_threads(WPI))
 pa_reduce_kernel(const __grid_constant__ DecodeParams p) {
     constexpr int DPL = D / 32;
@@ -2263,6 +2299,9 @@ pa_reduce_kernel(const __grid_constant__ DecodeParams p) {
                 __syncthreads();              // the buffer is reused by the next stride / item
             }
             if (sub != 0) continue;
+        }
+        if constexpr (WT) {
+            if (lane == 0) p.lse[static_cast<size_t>(qrow) * p.Hq + h] = make_float2(M, den);
         }
         const float inv = den > 0.f ? 1.f / den : 0.f;
 #pragma unroll

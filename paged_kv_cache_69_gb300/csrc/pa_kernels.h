@@ -13,8 +13,19 @@ struct Workspace {
     float* part_acc;
     int max_slots;
 };
-// Launch of the log-sum-exp merge behind a main kernel's.
+// Launch of the log-sum-exp merge behind a main kernel's, and behind that, if
+// p.scores is set, of the kernel that adds the weights up.
 pa_status launch_merge(const DecodeParams& p, pa_dtype out, bool split_heads, int sms, cudaStream_t stream);
+// What pa_decode_weights adds to a decode call: the pool that is added to, the
+// new tokens' counts (or null) and where the scores, (m, l) and first chunks go.
+struct WeightsOut {
+    float* weights;
+    const int32_t* fresh;
+    float* scores;
+    float2* lse;
+    int* chunk0;
+};
+pa_status launch_weights(const DecodeParams& p, const WeightsOut& w, cudaStream_t stream);
 // Kernel entry for the given cache dtype, query dtype and head_dim, or null.
 const void* decode_kernel_tc(pa_dtype kv, pa_dtype q, int D);
 const void* decode_kernel_simt(pa_dtype kv, pa_dtype q, int D);
@@ -31,9 +42,14 @@ const void* decode_kernel_mq_um(pa_dtype kv, pa_dtype q, int D, int CT);
 // Log-sum-exp merge; split_heads: several warps per (sequence, head), for
 // partitioned sequences with many partials.
 const void* reduce_kernel(pa_dtype out, int D, bool split_heads);
-// the output of pa_decode_weights
-pa_status decode_weights_out(void* out, const void* q, pa_dtype q_dtype, const void* k_cache, const void* v_cache,
-                             pa_dtype kv_dtype, const int32_t* block_tables, int MB, const int32_t* seq_lens, int B,
-                             int Hq, int Hkv, int D, int bs, int NB, float scale, float k_scale, float v_scale,
-                             void* workspace, size_t workspace_bytes, int32_t* err_flag, cudaStream_t stream);
+// pa_decode with the weights added up.
+pa_status decode_with_weights(const WeightsOut& w, void* out, const void* q, pa_dtype q_dtype, const void* k_cache,
+                              const void* v_cache, pa_dtype kv_dtype, const int32_t* block_tables, int MB,
+                              const int32_t* seq_lens, int B, int Hq, int Hkv, int D, int bs, int NB, float scale,
+                              float k_scale, float v_scale, void* workspace, size_t workspace_bytes,
+                              int32_t* err_flag, cudaStream_t stream);
+// The 16-token kernels that keep the scores (f32 caches: CUDA cores), and the
+// merge that keeps (m, l).
+const void* decode_kernel_weights(pa_dtype kv, pa_dtype q, int D);
+const void* reduce_kernel_weights(pa_dtype out, int D);
 }  // namespace pa

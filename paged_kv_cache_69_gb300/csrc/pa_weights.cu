@@ -2,110 +2,113 @@
 // softmax weight, summed over the query heads of its group, to a pool of
 // accumulated weights.
 //
-// The output is pa_decode's.  The weights come from one CTA per (sequence, KV
-// head): for each head of the group a first pass over the keys finds the
-// maximum and the sum of the softmax, a second adds exp(s - max) / sum to the
-// keys' entries; scores in f32, one thread per key.
+// The decode kernels keep what they have in hand: the scores of each chunk
+// (f32, log2 units, [chunk][head][token]) and, per sequence and head, the
+// maximum m and the sum l of the softmax, from the segment that covers a whole
+// sequence or from the merge.  The kernel here then forms
+//   w[g][t] = sum over the heads h of group g of 2^(s[h][t] - m[h]) / l[h]
+// and adds it to the entry of each token.  Reading the scores back costs
+// 4 bytes per token and query head, where a second pass over the keys would
+// cost head_dim elements per KV head.  A thread takes four tokens of one KV
+// head: 16-byte loads of each head's scores and one 16-byte update.
+#include <cuda.h>
+
 #include "pa_common.h"
-#include "pa_int4.cuh"
+#include "pa_decode_kernel.cuh"
 #include "pa_kernels.h"
 
 namespace pa {
 
-struct WeightsArgs {
-    float* weights;               // [NB][Hkv][bs]
-    const void* q;
-    const uint8_t* k;
-    const int32_t* tables;
-    const int32_t* lens;
-    const int32_t* fresh;
-    int32_t* err;
-    int MB, Hq, Hkv, G, D, bs, NB;
-    float qk_scale;               // scale * log2(e) (* k_scale for fp8)
-};
-
-struct Int4T { static constexpr pa_dtype code = PA_INT4; static constexpr int bytes = 0; };
 constexpr int WT_THREADS = 256;
+constexpr int WT_TOKENS = 256;                // tokens of a sequence per CTA
 
-// <q, K_t> of one key row.
-template <class KV>
-__device__ __forceinline__ float key_dot(const WeightsArgs& a, const float* q, int block, int off, int g) {
-    float s = 0.f;
-    if constexpr (KV::code == PA_INT4) {
-        const uint8_t* b = a.k + static_cast<size_t>(block) * a.bs * a.Hkv * (a.D / 2 + INT4_PARAM_BYTES);
-        const float2 p = __half22float2(*reinterpret_cast<const __half2*>(b + int4_param_off(g, off, a.bs, a.D, a.Hkv)));
-        const uint8_t* c = b + int4_code_off(g, off, a.bs, a.D);
-        for (int d = 0; d < a.D; d += 2) {
-            const uint32_t x = c[d / 2];
-            s = fmaf(q[d], int4_value(x & 15u, p.y, p.x), s);
-            s = fmaf(q[d + 1], int4_value(x >> 4, p.y, p.x), s);
-        }
-    } else {
-        const typename KV::T* row = reinterpret_cast<const typename KV::T*>(a.k) +
-                                    ((static_cast<size_t>(block) * a.bs + off) * a.Hkv + g) * a.D;
-        for (int d = 0; d < a.D; ++d) {
-            float x;
-            if constexpr (KV::code == PA_FP8_E4M3) x = fp8_to_float(row[d]);
-            else if constexpr (KV::code == PA_FP8_E5M2) x = e5m2_to_float(row[d]);
-            else x = to_float(row[d]);
-            s = fmaf(q[d], x, s);
-        }
-    }
-    return s * a.qk_scale;
-}
-
-template <class KV, class QT>
 __global__ void __launch_bounds__(WT_THREADS)
-weights_kernel(const __grid_constant__ WeightsArgs a) {
-    __shared__ float q[128];
-    __shared__ float rm[WT_THREADS / 32], rs[WT_THREADS / 32];
+weights_kernel(const __grid_constant__ DecodeParams p, float* __restrict__ weights, const int32_t* __restrict__ fresh) {
     grid_dependency_wait();
-    const int i = blockIdx.x, g = blockIdx.y, tid = threadIdx.x;
-    const int L = min(max(a.lens[i], 0), a.MB * a.bs);
-    const int first_fresh = L - (a.fresh ? min(max(a.fresh[i], 0), L) : min(L, 1));
-    const int32_t* bt = a.tables + static_cast<size_t>(i) * a.MB;
-    for (int r = 0; r < a.G; ++r) {
-        __syncthreads();
-        const typename QT::T* qr = static_cast<const typename QT::T*>(a.q) +
-                                   (static_cast<size_t>(i) * a.Hq + g * a.G + r) * a.D;
-        for (int d = tid; d < a.D; d += WT_THREADS) q[d] = to_float(qr[d]);
-        __syncthreads();
-        float m = -INFINITY, l = 0.f;
-        for (int t = tid; t < L; t += WT_THREADS) {
-            const int b = bt[t / a.bs];
-            if (b < 0 || b >= a.NB) continue;
-            const float s = key_dot<KV>(a, q, b, t % a.bs, g);
-            const float mn = fmaxf(m, s);
-            l = l * exp2f(m - mn) + exp2f(s - mn);
-            m = mn;
+    const int i = blockIdx.y, t0 = blockIdx.x * WT_TOKENS;
+    const int L = clamp_len(p.seq_lens[i], p.MB * p.bs);
+    if (t0 >= L) return;
+    const int first_fresh = L - (fresh ? min(max(fresh[i], 0), L) : 1);
+    const int32_t* bt = p.block_tables + static_cast<size_t>(i) * p.MB;
+    const int chunk0 = p.chunk0[i];
+    const float2* lse = p.lse + static_cast<size_t>(i) * p.Hq;
+    const int quads = (min(WT_TOKENS, L - t0) + 3) / 4;
+    // consecutive threads: consecutive quads of tokens of one KV head
+    for (int x = threadIdx.x; x < quads * p.Hkv; x += WT_THREADS) {
+        const int g = x / quads, t = t0 + 4 * (x - g * quads);
+        const int b = bt[t / p.bs];
+        if (b < 0 || b >= p.NB) continue;     // left out of the softmax, too
+        const int c = t / p.ct, in = t - c * p.ct;
+        const float* sp = score_row(p, chunk0 + c, g * p.G) + in;
+        float w[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+        for (int r = 0; r < p.G; ++r) {
+            const float4 s = *reinterpret_cast<const float4*>(sp + static_cast<size_t>(r) * p.ct);
+            const float2 ml = lse[g * p.G + r];
+            const float inv = 1.f / ml.y;
+            w[0] = fmaf(exp2f(s.x - ml.x), inv, w[0]);
+            w[1] = fmaf(exp2f(s.y - ml.x), inv, w[1]);
+            w[2] = fmaf(exp2f(s.z - ml.x), inv, w[2]);
+            w[3] = fmaf(exp2f(s.w - ml.x), inv, w[3]);
         }
+        float* dst = weights + (static_cast<size_t>(b) * p.Hkv + g) * p.bs + t % p.bs;
+        float4 old = *reinterpret_cast<const float4*>(dst);
+        float o[4] = {old.x, old.y, old.z, old.w};
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const float m2 = __shfl_xor_sync(0xffffffffu, m, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
-            const float mn = fmaxf(fmaxf(m, m2), -1e38f);
-            l = l * exp2f(m - mn) + l2 * exp2f(m2 - mn);
-            m = mn;
-        }
-        if ((tid & 31) == 0) { rm[tid >> 5] = m; rs[tid >> 5] = l; }
-        __syncthreads();
-        float M = -1e38f, den = 0.f;
-        for (int w = 0; w < WT_THREADS / 32; ++w) M = fmaxf(M, rm[w]);
-        for (int w = 0; w < WT_THREADS / 32; ++w) den += rs[w] * exp2f(rm[w] - M);
-        for (int t = tid; t < L; t += WT_THREADS) {
-            const int b = bt[t / a.bs];
-            if (b < 0 || b >= a.NB) continue;
-            const float p = exp2f(key_dot<KV>(a, q, b, t % a.bs, g) - M) / den;
-            float* w = a.weights + (static_cast<size_t>(b) * a.Hkv + g) * a.bs + t % a.bs;
-            *w = (r == 0 && t >= first_fresh) ? p : *w + p;
-        }
+        for (int e = 0; e < 4; ++e)
+            if (t + e < L) o[e] = (t + e >= first_fresh ? 0.f : o[e]) + w[e];
+        *reinterpret_cast<float4*>(dst) = make_float4(o[0], o[1], o[2], o[3]);
     }
 }
 
-template <class KV>
-static const void* weights_fn(pa_dtype q) {
-    if (q == PA_F32) return reinterpret_cast<const void*>(&weights_kernel<KV, F32T>);
-    if (q == PA_F16) return reinterpret_cast<const void*>(&weights_kernel<KV, F16T>);
-    return reinterpret_cast<const void*>(&weights_kernel<KV, BF16T>);
+pa_status launch_weights(const DecodeParams& p, const WeightsOut& w, cudaStream_t stream) {
+    if (p.B > 65535) return fail(PA_ERR_UNSUPPORTED, "decode_weights: more than 65535 sequences");
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>((static_cast<long long>(p.MB) * p.bs + WT_TOKENS - 1) / WT_TOKENS),
+                       static_cast<unsigned>(p.B));
+    cfg.blockDim = dim3(WT_THREADS);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    DecodeParams arg = p;
+    float* weights = w.weights;
+    const int32_t* fresh = w.fresh;
+    void* args[] = {&arg, &weights, &fresh};
+    const cudaError_t e = cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(&weights_kernel), args);
+    return e == cudaSuccess ? PA_OK : fail_cuda("decode_weights launch", e);
+}
+
+const void* decode_kernel_weights(pa_dtype kv, pa_dtype q, int D) {
+#define PA_WT(KVT, QTT, DD, TC) reinterpret_cast<const void*>(&pa_decode_kernel<KVT, QTT, DD, TC, 16, false, false, false, true>)
+#define PA_WTD(KVT, TC) (D == 128 ? PA_WT(KVT, KVT, 128, TC) : D == 64 ? PA_WT(KVT, KVT, 64, TC) : nullptr)
+    if (kv == PA_F32 && q == PA_F32) return PA_WTD(F32T, false);
+    if (kv == PA_F16 && q == PA_F16) return PA_WTD(F16T, true);
+    if (kv == PA_BF16 && q == PA_BF16) return PA_WTD(BF16T, true);
+    if (D != 128) return nullptr;
+    if (kv == PA_FP8_E4M3) return q == PA_F16 ? PA_WT(FP8T, F16T, 128, true) : q == PA_BF16 ? PA_WT(FP8T, BF16T, 128, true) : nullptr;
+    if (kv == PA_FP8_E5M2) return q == PA_F16 ? PA_WT(E5M2T, F16T, 128, true) : q == PA_BF16 ? PA_WT(E5M2T, BF16T, 128, true) : nullptr;
+#undef PA_WTD
+#undef PA_WT
+    return nullptr;
+}
+
+const void* reduce_kernel_weights(pa_dtype out, int D) {
+#define PA_RED(T) (D == 128 ? reinterpret_cast<const void*>(&pa_reduce_kernel<T, 128, 1, true>) \
+                   : D == 64 ? reinterpret_cast<const void*>(&pa_reduce_kernel<T, 64, 1, true>) : nullptr)
+    if (out == PA_F32) return PA_RED(float);
+    if (out == PA_F16) return PA_RED(__half);
+    if (out == PA_BF16) return PA_RED(__nv_bfloat16);
+#undef PA_RED
+    return nullptr;
+}
+
+static size_t wt_align(size_t x) { return (x + 255) & ~size_t(255); }
+// A chunk has at most 128 tokens (4-bit caches).
+static size_t score_bytes(int B, int Hq, int max_len) {
+    return sizeof(float) * static_cast<size_t>(B) * ((static_cast<size_t>(max_len) + 127) / 128 * 128) * Hq;
 }
 
 }  // namespace pa
@@ -113,7 +116,11 @@ static const void* weights_fn(pa_dtype q) {
 using namespace pa;
 
 extern "C" size_t pa_decode_weights_workspace_size(int num_seqs, int num_q_heads, int max_seq_len, int head_dim) {
-    return pa_decode_workspace_size(num_seqs, num_q_heads, max_seq_len, head_dim, 0);
+    const size_t base = pa_decode_workspace_size(num_seqs, num_q_heads, max_seq_len, head_dim, 0);
+    if (base == 0) return 0;
+    return wt_align(base) + wt_align(sizeof(int) * static_cast<size_t>(num_seqs)) +
+           wt_align(sizeof(float2) * static_cast<size_t>(num_seqs) * num_q_heads) +
+           wt_align(score_bytes(num_seqs, num_q_heads, max_seq_len));
 }
 
 extern "C" pa_status pa_decode_weights(void* out, float* weights, const void* q, pa_dtype q_dtype,
@@ -126,20 +133,22 @@ extern "C" pa_status pa_decode_weights(void* out, float* weights, const void* q,
     clear_error();
     if (num_seqs > 0 && !weights) return fail(PA_ERR_INVALID_ARG, "decode_weights: null pointer");
     if (num_seqs > 0 && !aligned16(weights)) return fail(PA_ERR_INVALID_ARG, "decode_weights: weights must be 16-byte aligned");
-    const pa_status st = decode_weights_out(out, q, q_dtype, k_cache, v_cache, kv_dtype, block_tables,
-                                            max_blocks_per_seq, seq_lens, num_seqs, num_q_heads, num_kv_heads, head_dim,
-                                            block_size, num_blocks, scale, k_scale, v_scale, workspace,
-                                            workspace_bytes, err_flag, stream);
-    if (st != PA_OK || num_seqs == 0) return st;
-    WeightsArgs a{weights, q, static_cast<const uint8_t*>(k_cache), block_tables, seq_lens, fresh, err_flag,
-                  max_blocks_per_seq, num_q_heads, num_kv_heads, num_q_heads / num_kv_heads, head_dim, block_size,
-                  num_blocks, scale * 1.4426950408889634f * (is_fp8(kv_dtype) ? k_scale : 1.f)};
-    const void* fn = kv_dtype == PA_F32 ? weights_fn<F32T>(q_dtype) : kv_dtype == PA_F16 ? weights_fn<F16T>(q_dtype)
-                     : kv_dtype == PA_BF16 ? weights_fn<BF16T>(q_dtype)
-                     : kv_dtype == PA_FP8_E4M3 ? weights_fn<FP8T>(q_dtype)
-                     : kv_dtype == PA_FP8_E5M2 ? weights_fn<E5M2T>(q_dtype) : weights_fn<Int4T>(q_dtype);
-    void* args[] = {&a};
-    const cudaError_t e = cudaLaunchKernel(fn, dim3(static_cast<unsigned>(num_seqs), static_cast<unsigned>(num_kv_heads)),
-                                           dim3(WT_THREADS), args, 0, stream);
-    return e == cudaSuccess ? PA_OK : fail_cuda("decode_weights launch", e);
+    WeightsOut w{weights, fresh, nullptr, nullptr, nullptr};
+    if (num_seqs > 0 && num_q_heads > 0 && head_dim > 0 && max_blocks_per_seq > 0 && block_size > 0 &&
+        static_cast<long long>(max_blocks_per_seq) * block_size < (1LL << 30) && workspace) {
+        // the parts behind pa_decode's workspace; a missing device is reported below
+        const int max_len = max_blocks_per_seq * block_size;
+        const size_t base = pa_decode_workspace_size(num_seqs, num_q_heads, max_len, head_dim, 0);
+        if (base != 0) {
+            if (workspace_bytes < pa_decode_weights_workspace_size(num_seqs, num_q_heads, max_len, head_dim))
+                return fail(PA_ERR_WORKSPACE, "decode_weights: workspace smaller than pa_decode_weights_workspace_size()");
+            uint8_t* ws = static_cast<uint8_t*>(workspace) + wt_align(base);
+            w.chunk0 = reinterpret_cast<int*>(ws); ws += wt_align(sizeof(int) * static_cast<size_t>(num_seqs));
+            w.lse = reinterpret_cast<float2*>(ws); ws += wt_align(sizeof(float2) * static_cast<size_t>(num_seqs) * num_q_heads);
+            w.scores = reinterpret_cast<float*>(ws);
+        }
+    }
+    return decode_with_weights(w, out, q, q_dtype, k_cache, v_cache, kv_dtype, block_tables, max_blocks_per_seq,
+                               seq_lens, num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, scale,
+                               k_scale, v_scale, workspace, workspace_bytes, err_flag, stream);
 }
