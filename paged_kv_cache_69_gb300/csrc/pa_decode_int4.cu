@@ -74,6 +74,10 @@ __device__ __forceinline__ void bulk_load32(uint32_t dst, const void* src, uint3
                  :: "r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
 }
 
+__device__ __forceinline__ void bulk_load32_hint(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar, uint64_t policy) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;"
+                 :: "r"(dst), "l"(src), "r"(bytes), "r"(bar), "l"(policy) : "memory");
+}
 // 16-byte copy by the thread's own address, and this thread's arrival on `bar`
 // once its copies so far have landed (counted in the barrier's 33 arrivals).
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
@@ -87,12 +91,14 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
 // producer: one warp; lane b copies block b of a chunk (or head b of a block
 // that is longer than a chunk).
 // ---------------------------------------------------------------------------
-template <int D>
+template <int D, bool WT>
 __device__ __forceinline__ void int4_producer(const Int4Params& a, const Plan& pl, int hg, uint8_t* base,
                                               uint64_t* full, uint64_t* empty, uint64_t* qempty, I4Desc* descs) {
     const DecodeParams& p = a.d;
     const int lane = threadIdx.x & 31;
     const int S = p.stages, maxL = p.MB * p.bs, CT = p.ct;
+    uint64_t policy = 0;
+    if constexpr (WT) policy = l2_evict_first();
     int lbase = pl.seq, lval = 0;
     auto load_lens = [&](int first) {
         lbase = first;
@@ -242,8 +248,13 @@ __device__ __forceinline__ void int4_producer(const Int4Params& a, const Plan& p
         if (whole) {
             if (good) {
                 const size_t blk = static_cast<size_t>(static_cast<unsigned>(id)) * a.block_bytes;
-                bulk_load32(stage + my_codes, kcs + blk, box_codes, bar);
-                bulk_load32(stage + v_at + my_codes, vcs + blk, box_codes, bar);
+                if constexpr (WT) {            // K and V pass once; the scores are read again
+                    bulk_load32_hint(stage + my_codes, kcs + blk, box_codes, bar, policy);
+                    bulk_load32_hint(stage + v_at + my_codes, vcs + blk, box_codes, bar, policy);
+                } else {
+                    bulk_load32(stage + my_codes, kcs + blk, box_codes, bar);
+                    bulk_load32(stage + v_at + my_codes, vcs + blk, box_codes, bar);
+                }
             }
         } else if (goods & 1u) {
             // a chunk is part of one block: a span per head
@@ -396,6 +407,13 @@ __device__ __forceinline__ void int4_consumer(const Int4Params& a, const Plan& p
     float sq[NQT][2];                             // sum of the query row, times the score scale
     float unit_qk = 0.f;                          // score of one unit of the codes' dot product
     int jt[NQT][2], lim[NQT][2];
+    // the lane's scores of the next chunk, of its first row
+    float* sdst = nullptr;
+    int ct_log2 = 5;
+    if constexpr (WT) {
+        while ((1 << ct_log2) < p.ct) ++ct_log2;
+        sdst = score_row(p, pl.cs, (hg * p.HPC + hl) * p.G + rt * NQT * 8 + 2 * t4) + I4_WT * ts + tk;
+    }
     float inv = 0.f, step_top = 0.f;              // power of two on step in the weights (0: not set yet); 2^7 over it
     int in_rows = 0, joins = 0;
 #pragma unroll
@@ -583,8 +601,7 @@ __device__ __forceinline__ void int4_consumer(const Int4Params& a, const Plan& p
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
                         if ((in_rows >> (2 * n + e)) & 1) {
-                            float* dst = score_row(p, k, (hg * p.HPC + hl) * p.G + (rt * NQT + n) * 8 + 2 * t4 + e) +
-                                         I4_WT * ts + 16 * MT * sub + tk;
+                            float* dst = sdst + (static_cast<uint32_t>(n * 8 + e) << ct_log2) + 16 * MT * sub;
 #pragma unroll
                             for (int mt = 0; mt < MT; ++mt) {
                                 dst[16 * mt] = s[mt][n][e];
@@ -733,6 +750,7 @@ __device__ __forceinline__ void int4_consumer(const Int4Params& a, const Plan& p
                 }
             }
         }
+        if constexpr (WT) sdst += static_cast<size_t>(p.Hq) << ct_log2;
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[slot]);
         if (d.flags & SEG_END) {
@@ -872,7 +890,7 @@ int4_decode_kernel(const __grid_constant__ Int4Params a) {
         fence_proxy_async_smem();
     }
     __syncthreads();
-    if (warp == p.NCW) int4_producer<D>(a, pl, hg, base, full, empty, qempty, descs);
+    if (warp == p.NCW) int4_producer<D, WT>(a, pl, hg, base, full, empty, qempty, descs);
     else if (warp < p.NCW) int4_consumer<QT, D, NQT, HL, WT>(a, pl, hg, warp, base, full, empty, qempty, joined, descs);
 }
 

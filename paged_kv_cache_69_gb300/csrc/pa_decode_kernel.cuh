@@ -414,6 +414,8 @@ struct DecodeKernel {
         const int lane = threadIdx.x & 31;
         const int S = p.stages;
         const int maxL = p.MB * p.bs;
+        uint64_t policy = 0;
+        if constexpr (WT) policy = l2_evict_first();
         // Sequence lengths come 32 sequences per warp-wide load, and block
         // table entries in 32-entry windows with the window after the
         // current one always in flight, so neither a change of sequence nor
@@ -587,8 +589,14 @@ struct DecodeKernel {
                         uint8_t* kd = kbuf + b * p.box_bytes;
                         uint8_t* vd = vbuf + b * p.box_bytes;
                         if (!p.per_head_copies) {
-                            tma_load_4d(kd, tk, &full[slot], 0, row0, hg * p.HPC, 0);
-                            tma_load_4d(vd, tv, &full[slot], 0, row0, hg * p.HPC, 0);
+                            if constexpr (WT) {
+                                // K and V pass once; the scores are read again
+                                tma_load_4d_hint(kd, tk, &full[slot], 0, row0, hg * p.HPC, 0, policy);
+                                tma_load_4d_hint(vd, tv, &full[slot], 0, row0, hg * p.HPC, 0, policy);
+                            } else {
+                                tma_load_4d(kd, tk, &full[slot], 0, row0, hg * p.HPC, 0);
+                                tma_load_4d(vd, tv, &full[slot], 0, row0, hg * p.HPC, 0);
+                            }
                         } else {
                             const int DH = ROWB / 128;
                             const int E128 = 128 / KV::bytes;
@@ -801,7 +809,6 @@ struct DecodeKernel {
         const int tokV = (mi & 1) * 8 + r8;        // V (transposed) row
         const uint32_t rbK = lay.row_base(tokK, hl), rbV = lay.row_base(tokV, hl);
         const RowInfo ri = row_info(p, hg, hl, mt, lane);
-
         float acc[NT][4];
         uint32_t qa[KS][4];
         float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
@@ -888,13 +895,15 @@ struct DecodeKernel {
                     s[nt][e] = keep ? s[nt][e] * p.qk_scale : -INFINITY;
                 }
             if constexpr (WT) {
-                // rows g4 and g4 + 8: four lanes store 8 tokens, one sector
+                // rows g4 and g4 + 8 (heads 8 apart): four lanes store 8 tokens,
+                // one sector; a pointer kept across chunks would spill (102 us
+                // as against 106 on the 7B-like batch)
+                float* dst = score_row(p, k, ri.head[0]) + 2 * t4;
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh) {
                     if (!ri.in[hh]) continue;
-                    float* dst = score_row(p, k, ri.head[hh]) + 2 * t4;
-                    *reinterpret_cast<float2*>(dst) = make_float2(s[0][2 * hh], s[0][2 * hh + 1]);
-                    *reinterpret_cast<float2*>(dst + 8) = make_float2(s[1][2 * hh], s[1][2 * hh + 1]);
+                    *reinterpret_cast<float2*>(dst + 8 * CT * hh) = make_float2(s[0][2 * hh], s[0][2 * hh + 1]);
+                    *reinterpret_cast<float2*>(dst + 8 * CT * hh + 8) = make_float2(s[1][2 * hh], s[1][2 * hh + 1]);
                 }
             }
             float mx0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
@@ -2174,6 +2183,8 @@ pa_reduce_kernel(const __grid_constant__ DecodeParams p) {
     const int sub = warp % WPI;
     const int HG = cdiv_i(p.Hq, HPB);    // head groups of HPB heads
     const int per_seq = p.QL * HG;       // items of one split sequence: query tokens x head groups
+    // the kernel that adds the weights up may become resident now
+    if constexpr (WT) grid_dependents_launch();
     // The list and its length are final once every CTA of the main grid has
     // passed its trigger, which precedes this grid's start: the first item's
     // entry loads before the wait for the partials.

@@ -20,43 +20,61 @@
 namespace pa {
 
 constexpr int WT_THREADS = 256;
-constexpr int WT_TOKENS = 256;                // tokens of a sequence per CTA
+constexpr int WT_STEPS = 4;                   // token spans of a CTA, one after another
 
-__global__ void __launch_bounds__(WT_THREADS)
-weights_kernel(const __grid_constant__ DecodeParams p, float* __restrict__ weights, const int32_t* __restrict__ fresh) {
-    grid_dependency_wait();
-    const int i = blockIdx.y, t0 = blockIdx.x * WT_TOKENS;
-    const int L = clamp_len(p.seq_lens[i], p.MB * p.bs);
-    if (t0 >= L) return;
-    const int first_fresh = L - (fresh ? min(max(fresh[i], 0), L) : 1);
-    const int32_t* bt = p.block_tables + static_cast<size_t>(i) * p.MB;
-    const int chunk0 = p.chunk0[i];
-    const float2* lse = p.lse + static_cast<size_t>(i) * p.Hq;
-    const int quads = (min(WT_TOKENS, L - t0) + 3) / 4;
+// NH: heads of a group whose scores are loaded at once.
+// What the decode kernel and those before it wrote is final when this grid
+// starts (the merge, whose start it follows, starts behind the decode
+// kernel's prologue), so lengths, tables and first chunks are read before the
+// wait for the scores and (m, l).
+template <int NH>
+__global__ void __launch_bounds__(WT_THREADS, NH == 4 ? 4 : 3)
+weights_kernel(const __grid_constant__ DecodeParams p, float* __restrict__ weights, const int32_t* __restrict__ fresh,
+               int quads, int bs_log2, int ct_log2) {
     // consecutive threads: consecutive quads of tokens of one KV head
-    for (int x = threadIdx.x; x < quads * p.Hkv; x += WT_THREADS) {
-        const int g = x / quads, t = t0 + 4 * (x - g * quads);
-        const int b = bt[t / p.bs];
-        if (b < 0 || b >= p.NB) continue;     // left out of the softmax, too
-        const int c = t / p.ct, in = t - c * p.ct;
-        const float* sp = score_row(p, chunk0 + c, g * p.G) + in;
+    const int i = blockIdx.y, x = threadIdx.x, g = blockIdx.z * (WT_THREADS / quads) + x / quads;
+    const int span = 4 * quads, t0 = static_cast<int>(blockIdx.x) * WT_STEPS * span;
+    int t = t0 + 4 * (x & (quads - 1));
+    const int maxL = p.MB << bs_log2;
+    const int L = clamp_len(p.seq_lens[i], maxL);
+    const int32_t* bt = p.block_tables + static_cast<size_t>(i) * p.MB;
+    int next = t < maxL ? __ldg(bt + (t >> bs_log2)) : -1;
+    const int old_until = L - (fresh ? min(max(fresh[i], 0), L) : 1);
+    const float* scores = score_row(p, __ldcg(p.chunk0 + i), g * p.G);
+    grid_dependency_wait();
+    if (t0 >= L || g >= p.Hkv) return;
+    const float2* lse = p.lse + static_cast<size_t>(i) * p.Hq + g * p.G;
+    const size_t chunk = static_cast<size_t>(p.Hq) << ct_log2;
+#pragma unroll 1
+    for (int k = 0; k < WT_STEPS && t < L; ++k, t += span) {
+        const int b = next;
+        next = t + span < maxL ? __ldg(bt + ((t + span) >> bs_log2)) : -1;
+        if (b < 0 || b >= p.NB) continue;                     // a bad block is left out of the softmax, too
+        float* dst = weights + ((static_cast<size_t>(b) * p.Hkv + g) << bs_log2) + (t & (p.bs - 1));
+        const float4 old = *reinterpret_cast<const float4*>(dst);
+        const float* sp = scores + (t >> ct_log2) * chunk + (t & (p.ct - 1));
         float w[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-        for (int r = 0; r < p.G; ++r) {
-            const float4 s = *reinterpret_cast<const float4*>(sp + static_cast<size_t>(r) * p.ct);
-            const float2 ml = lse[g * p.G + r];
-            const float inv = 1.f / ml.y;
-            w[0] = fmaf(exp2f(s.x - ml.x), inv, w[0]);
-            w[1] = fmaf(exp2f(s.y - ml.x), inv, w[1]);
-            w[2] = fmaf(exp2f(s.z - ml.x), inv, w[2]);
-            w[3] = fmaf(exp2f(s.w - ml.x), inv, w[3]);
+#pragma unroll 1
+        for (int r0 = 0; r0 < p.G; r0 += NH) {
+            float4 s[NH];
+#pragma unroll
+            for (int r = 0; r < NH; ++r)
+                if (r0 + r < p.G) s[r] = __ldcs(reinterpret_cast<const float4*>(sp + (static_cast<size_t>(r0 + r) << ct_log2)));
+#pragma unroll
+            for (int r = 0; r < NH; ++r)
+                if (r0 + r < p.G) {
+                    const float2 ml = lse[r0 + r];
+                    const float inv = 1.f / ml.y;
+                    w[0] = fmaf(ex2_approx(s[r].x - ml.x), inv, w[0]);
+                    w[1] = fmaf(ex2_approx(s[r].y - ml.x), inv, w[1]);
+                    w[2] = fmaf(ex2_approx(s[r].z - ml.x), inv, w[2]);
+                    w[3] = fmaf(ex2_approx(s[r].w - ml.x), inv, w[3]);
+                }
         }
-        float* dst = weights + (static_cast<size_t>(b) * p.Hkv + g) * p.bs + t % p.bs;
-        float4 old = *reinterpret_cast<const float4*>(dst);
         float o[4] = {old.x, old.y, old.z, old.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            if (t + e < L) o[e] = (t + e >= first_fresh ? 0.f : o[e]) + w[e];
+            if (t + e < L) o[e] = (t + e < old_until ? o[e] : 0.f) + w[e];
         *reinterpret_cast<float4*>(dst) = make_float4(o[0], o[1], o[2], o[3]);
     }
 }
@@ -67,8 +85,12 @@ pa_status launch_weights(const DecodeParams& p, const WeightsOut& w, cudaStream_
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>((static_cast<long long>(p.MB) * p.bs + WT_TOKENS - 1) / WT_TOKENS),
-                       static_cast<unsigned>(p.B));
+    // a CTA: WT_STEPS spans of 4 * quads tokens, of 256 / quads KV heads
+    int quads = 8;
+    while (quads < WT_THREADS && WT_THREADS / (2 * quads) >= p.Hkv) quads *= 2;
+    const int heads = WT_THREADS / quads;
+    cfg.gridDim = dim3(static_cast<unsigned>((static_cast<long long>(p.MB) * p.bs + WT_STEPS * 4 * quads - 1) / (WT_STEPS * 4 * quads)),
+                       static_cast<unsigned>(p.B), static_cast<unsigned>((p.Hkv + heads - 1) / heads));
     cfg.blockDim = dim3(WT_THREADS);
     cfg.stream = stream;
     cfg.attrs = attr;
@@ -76,8 +98,12 @@ pa_status launch_weights(const DecodeParams& p, const WeightsOut& w, cudaStream_
     DecodeParams arg = p;
     float* weights = w.weights;
     const int32_t* fresh = w.fresh;
-    void* args[] = {&arg, &weights, &fresh};
-    const cudaError_t e = cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(&weights_kernel), args);
+    int bs_log2 = 3, ct_log2 = 4;             // block sizes and chunks are powers of two
+    while ((1 << bs_log2) < p.bs) ++bs_log2;
+    while ((1 << ct_log2) < p.ct) ++ct_log2;
+    void* args[] = {&arg, &weights, &fresh, &quads, &bs_log2, &ct_log2};
+    const cudaError_t e = cudaLaunchKernelExC(&cfg, p.G <= 4 ? reinterpret_cast<const void*>(&weights_kernel<4>)
+                                                          : reinterpret_cast<const void*>(&weights_kernel<8>), args);
     return e == cudaSuccess ? PA_OK : fail_cuda("decode_weights launch", e);
 }
 
