@@ -11,10 +11,15 @@
 // Attention does not depend on the order of the rows, so only the rows that
 // change places are moved, and the recent ones stay last for the next call.
 //
-// evict_select_kernel: one CTA per (sequence, KV head).  The k-th largest
-// weight is found by a radix select over order-preserving 32-bit keys (four
-// 8-bit digits, a histogram each); one more pass in position order ranks the
-// ties, lists the free places below `heavy` and the kept rows behind it.
+// evict_select_kernel: a cluster of 1 to 8 CTAs per (sequence, KV head), each
+// with a contiguous part of its tokens.  The weights are read once, turned
+// into order-preserving 32-bit keys and kept in shared memory; the k-th
+// largest is found by a radix select of three digits (11, 11, 10 bits), whose
+// histograms the CTAs read from one another (distributed shared memory).  The
+// last histogram also tells each CTA how many ties lie in the parts before
+// its own.  A thread then owns a run of consecutive tokens: it ranks its
+// ties, counts the free places below `heavy` and the kept rows behind it,
+// and writes both lists in position order.
 // evict_move_kernel: a CTA moves a slice of 64 bytes (or less) of a head's
 // rows of one plane (K, V, the 4-bit parameters, the weights).  Slices share
 // no bytes, so the order that an in-place move needs holds inside a CTA.
@@ -65,38 +70,70 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
     return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
+// Exclusive prefix sum over the block; `total` is the block's sum.
 __device__ __forceinline__ int block_scan_excl(int v, int* warp_sums, int& total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int NW = EV_SEL_THREADS / 32;
     int x = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
     }
+    __syncthreads();                            // the sums of the scan before are read
     if (lane == 31) warp_sums[warp] = x;
     __syncthreads();
-    if (warp == 0) {
-        int s = lane < nw ? warp_sums[lane] : 0;
+    int s = lane < NW ? warp_sums[lane] : 0;    // every warp scans the warps' sums
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, s, o);
-            if (lane >= o) s += y;
-        }
-        if (lane < nw) warp_sums[lane] = s;
+    for (int o = 1; o < NW; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += y;
     }
-    __syncthreads();
-    total = warp_sums[nw - 1];
-    const int r = x - v + (warp ? warp_sums[warp - 1] : 0);
-    __syncthreads();
-    return r;
+    total = __shfl_sync(0xffffffffu, s, NW - 1);
+    const int before = __shfl_sync(0xffffffffu, s, max(warp - 1, 0));
+    return x - v + (warp ? before : 0);
 }
 
+// Thread-block clusters (PTX ISA: barrier.cluster, mapa, ld.shared::cluster).
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %cluster_nctaid.x;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The int at the same shared address in CTA `rank` of the cluster.
+__device__ __forceinline__ int peer_int(const int* p, uint32_t rank) {
+    uint32_t a;
+    int v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+
+constexpr int EV_BINS = 2048;
+constexpr int EV_CACHE = 24576;            // keys that a CTA keeps at most (101 KB with padding)
+constexpr int EV_MAX_CLUSTER = 8;
+
+// CACHED: a CTA's keys stay in shared memory; else (sequences beyond
+// 8 * EV_CACHE tokens) every pass reads the weights again.
+template <bool CACHED>
 __global__ void __launch_bounds__(EV_SEL_THREADS)
 evict_select_kernel(const __grid_constant__ EvictArgs a) {
-    __shared__ int hist[256];
-    __shared__ int sums[32];
-    __shared__ int s_bad, s_digit, s_above;
-    const int row = blockIdx.x, i = row / a.Hkv, g = row - i * a.Hkv, tid = threadIdx.x;
+    __shared__ int hist[3][EV_BINS];
+    __shared__ int sums[EV_SEL_THREADS / 32];
+    __shared__ int s_bad, s_digit, s_above, s_nh, s_nf;
+    extern __shared__ uint32_t s_keys[];
+    constexpr int NT = EV_SEL_THREADS;
+    grid_dependents_launch();
+    const int C = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
+    const int row = blockIdx.x / C, i = row / a.Hkv, g = row - i * a.Hkv, tid = threadIdx.x;
     const int32_t* bt = a.tables + static_cast<size_t>(i) * a.MB;
     int32_t* kept = a.kept + static_cast<size_t>(row) * a.budget;
     int32_t* holes = a.holes + static_cast<size_t>(row) * a.budget;
@@ -104,81 +141,161 @@ evict_select_kernel(const __grid_constant__ EvictArgs a) {
     const int L = a.lens[i];
     const int n = min(L, a.budget);
     if (tid == 0) s_bad = 0;
+    for (int x = tid; x < 3 * EV_BINS; x += NT) (&hist[0][0])[x] = 0;
     __syncthreads();
     bool bad_len = L < 0 || static_cast<long long>(L) > static_cast<long long>(a.MB) * a.bs;
     if (a.new_tables) bad_len = bad_len || static_cast<long long>(n) > static_cast<long long>(a.newMB) * a.bs;
     if (!bad_len) {
         bool bad = false;
-        for (int j = tid; j < (L + a.bs - 1) >> a.shift; j += blockDim.x) bad |= bt[j] < 0 || bt[j] >= a.NB;
+        for (int j = tid; j < (L + a.bs - 1) >> a.shift; j += NT) bad |= bt[j] < 0 || bt[j] >= a.NB;
         if (a.new_tables) {
             const int32_t* nt = a.new_tables + static_cast<size_t>(i) * a.newMB;
-            for (int j = tid; j < (n + a.bs - 1) >> a.shift; j += blockDim.x) bad |= nt[j] < 0 || nt[j] >= a.NB;
+            for (int j = tid; j < (n + a.bs - 1) >> a.shift; j += NT) bad |= nt[j] < 0 || nt[j] >= a.NB;
         }
         if (bad) s_bad = 1;
     }
     __syncthreads();
+    // The CTAs of a cluster see the same lengths and tables: all leave here or none.
     if (bad_len || s_bad) {
+        if (rank != 0) return;
         if (tid == 0) {
             raise_flag(a.err, bad_len ? PA_ERRBIT_SEQ_TOO_LONG : PA_ERRBIT_BAD_BLOCK);
             a.rows[row] = EvictRow{L, a.new_tables ? 0 : L, 0, 0};
         }
-        for (int j = tid; j < a.budget; j += blockDim.x) kept[j] = -1;
+        for (int j = tid; j < a.budget; j += NT) kept[j] = -1;
         return;
     }
     if (L <= a.budget) {
-        for (int j = tid; j < a.budget; j += blockDim.x) kept[j] = j < L ? j : -1;
+        if (rank != 0) return;
+        for (int j = tid; j < a.budget; j += NT) kept[j] = j < L ? j : -1;
         if (tid == 0) a.rows[row] = EvictRow{L, L, 0, 1};
         return;
     }
     const int heavy = a.budget - a.recent, end = L - a.recent;
-    const int k = heavy - a.sink;
+    const int k = heavy - a.sink;                   // tokens chosen by weight, of [sink, end)
+    const int seg = ((end + C - 1) / C + 3) & ~3;   // this CTA: tokens [lo, hi)
+    const int lo = min(rank * seg, end), hi = min(end, lo + seg);
+    const float* wg = a.weights + static_cast<size_t>(g) * a.bs;
+    const size_t wstride = static_cast<size_t>(a.Hkv) * a.bs;
+    auto slot_of = [](int x) { return x + (x >> 5); };                 // a run per thread: no bank conflicts
     auto key_at = [&](int pos) -> uint32_t {
-        const size_t b = static_cast<size_t>(bt[pos >> a.shift]);
-        return weight_key(a.weights[(b * a.Hkv + g) * a.bs + (pos & (a.bs - 1))]);
+        if constexpr (CACHED) return s_keys[slot_of(pos - lo)];
+        return weight_key(wg[static_cast<size_t>(bt[pos >> a.shift]) * wstride + (pos & (a.bs - 1))]);
     };
-    // the k-th largest key, digit by digit from the top
+    auto cand = [&](int pos) { return pos >= a.sink; };                // and pos < end, as all here are
     uint32_t thr = 0;
     int need = k;                                   // ties with thr that are kept
-    for (int d = 24; d >= 0 && k > 0; d -= 8) {
-        for (int b = tid; b < 256; b += blockDim.x) hist[b] = 0;
-        __syncthreads();
-        for (int pos = a.sink + tid; pos < end; pos += blockDim.x) {
-            const uint32_t key = key_at(pos);
-            if (d == 24 || (key >> (d + 8)) == (thr >> (d + 8))) atomicAdd(&hist[(key >> d) & 255u], 1);
+    if (k > 0) {
+        // weights by 16 bytes, four in flight: keys, and the first digit's counts
+        constexpr int U = 4;
+        for (int p0 = lo + 4 * tid; p0 < hi; p0 += 4 * NT * U) {
+            int blk[U];
+            float4 w[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int pos = p0 + u * 4 * NT;
+                blk[u] = pos < hi ? __ldg(bt + (pos >> a.shift)) : 0;
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int pos = p0 + u * 4 * NT;
+                if (pos < hi) w[u] = *reinterpret_cast<const float4*>(wg + static_cast<size_t>(blk[u]) * wstride + (pos & (a.bs - 1)));
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int pos = p0 + u * 4 * NT;
+                const float v[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (pos + e < hi) {
+                        const uint32_t key = weight_key(v[e]);
+                        if constexpr (CACHED) s_keys[slot_of(pos + e - lo)] = key;
+                        if (cand(pos + e)) atomicAdd(&hist[0][key >> 21], 1);
+                    }
+            }
         }
-        __syncthreads();
-        // digits from the largest down: thread t < 256 holds digit 255 - t
-        int total;
-        const int c = tid < 256 ? hist[255 - tid] : 0;
-        const int before = block_scan_excl(c, sums, total);
-        if (tid < 256 && before < need && need <= before + c) { s_digit = 255 - tid; s_above = before; }
-        __syncthreads();
-        thr |= static_cast<uint32_t>(s_digit) << d;
-        need -= s_above;
-        __syncthreads();
+#pragma unroll 1
+        for (int d = 0; d < 3; ++d) {
+            const int shift = d == 0 ? 21 : d == 1 ? 10 : 0;
+            if (d > 0) {
+                const int up = d == 1 ? 21 : 10;    // bits decided so far
+                for (int pos = lo + tid; pos < hi; pos += NT) {
+                    const uint32_t key = key_at(pos);
+                    if (cand(pos) && (key >> up) == (thr >> up))
+                        atomicAdd(&hist[d][(key >> shift) & (d == 1 ? 2047u : 1023u)], 1);
+                }
+            }
+            cluster_sync();
+            // digits from the largest down, EV_BINS / NT per thread
+            constexpr int PB = EV_BINS / NT;
+            int cnt[PB], mine = 0;
+#pragma unroll
+            for (int e = 0; e < PB; ++e) {
+                const int* h = &hist[d][EV_BINS - 1 - (tid * PB + e)];
+                cnt[e] = 0;
+                for (int r = 0; r < C; ++r) cnt[e] += C == 1 ? *h : peer_int(h, r);
+                mine += cnt[e];
+            }
+            int total, before = block_scan_excl(mine, sums, total);
+            if (before < need && need <= before + mine) {
+#pragma unroll
+                for (int e = 0; e < PB; ++e) {
+                    if (before < need && need <= before + cnt[e]) {
+                        s_digit = EV_BINS - 1 - (tid * PB + e);
+                        s_above = before;
+                    }
+                    before += cnt[e];
+                }
+            }
+            __syncthreads();
+            thr |= static_cast<uint32_t>(s_digit) << shift;
+            need -= s_above;
+            __syncthreads();
+        }
     }
-    for (int j = tid; j < a.budget; j += blockDim.x) kept[j] = j < heavy ? j : end + (j - heavy);
-    int ties = 0, nh = 0, nf = 0;
-    for (int p0 = 0; p0 < end; p0 += blockDim.x) {
-        const int pos = p0 + tid;
-        uint32_t key = 0;
-        const bool cand = pos >= a.sink && pos < end && k > 0;
-        if (cand) key = key_at(pos);
-        int total;
-        const bool tie = cand && key == thr;
-        const int rank = ties + block_scan_excl(tie ? 1 : 0, sums, total);
-        ties += total;
-        const bool keep = pos < a.sink || (cand && (key > thr || (tie && rank < need)));
-        const bool hole = pos < heavy && !keep, fill = pos >= heavy && pos < end && keep;
-        const int at = block_scan_excl((hole ? 1 : 0) | (fill ? 0x10000 : 0), sums, total);
-        if (hole) holes[nh + (at & 0xffff)] = pos;
-        if (fill) fills[nf + (at >> 16)] = pos;
-        nh += total & 0xffff;
-        nf += total >> 16;
-    }
-    __syncthreads();                               // the lists are this CTA's own writes
-    for (int r = tid; r < nf; r += blockDim.x) kept[holes[r]] = fills[r];
-    if (tid == 0) a.rows[row] = EvictRow{L, a.budget, nf, 1};
+    for (int j = rank * NT + tid; j < a.budget; j += C * NT) kept[j] = j < heavy ? j : end + (j - heavy);
+    // ties in the parts before this one: counted by their last histogram
+    int ties = 0;
+    if (k > 0)
+        for (int r = 0; r < rank; ++r) ties += peer_int(&hist[2][thr & 1023u], r);
+    const int run = (hi - lo + NT - 1) / NT, r0 = min(hi, lo + tid * run), r1 = min(hi, r0 + run);
+    int total, mine = 0;
+    if (k > 0)
+        for (int pos = r0; pos < r1; ++pos) mine += (cand(pos) && key_at(pos) == thr) ? 1 : 0;
+    ties += block_scan_excl(mine, sums, total);
+    // one walk over the run: f(position, kept)
+    auto walk = [&](auto f) {
+        int t = ties;
+        for (int pos = r0; pos < r1; ++pos) {
+            bool keep = pos < a.sink;
+            if (!keep && k > 0) {
+                const uint32_t key = key_at(pos);
+                keep = key > thr;
+                if (key == thr) keep = t++ < need;
+            }
+            f(pos, keep);
+        }
+    };
+    int h = 0, f = 0;
+    walk([&](int pos, bool keep) {
+        h += (pos < heavy && !keep) ? 1 : 0;
+        f += (pos >= heavy && keep) ? 1 : 0;
+    });
+    int th, tf;
+    int h0 = block_scan_excl(h, sums, th), f0 = block_scan_excl(f, sums, tf);
+    if (tid == 0) { s_nh = th; s_nf = tf; }
+    cluster_sync();
+    for (int r = 0; r < rank; ++r) { h0 += peer_int(&s_nh, r); f0 += peer_int(&s_nf, r); }
+    int nf = 0;
+    for (int r = 0; r < C; ++r) nf += peer_int(&s_nf, r);
+    walk([&](int pos, bool keep) {
+        if (pos < heavy && !keep) holes[h0++] = pos;
+        if (pos >= heavy && keep) fills[f0++] = pos;
+    });
+    __threadfence();
+    cluster_sync();                                // every list entry written, every peer's counts read
+    for (int r = rank * NT + tid; r < nf; r += C * NT) kept[__ldcg(holes + r)] = __ldcg(fills + r);
+    if (rank == 0 && tid == 0) a.rows[row] = EvictRow{L, a.budget, nf, 1};
 }
 
 template <typename T>
@@ -210,40 +327,38 @@ __device__ __forceinline__ void evict_move(const EvictArgs& a, const EvictPlane&
         }
         return;
     }
-    // kept rows from behind `heavy` into the free places below it
+    // First the kept rows from behind `heavy`, into the free places below it,
+    // then the recent rows, in order.  A new place of a recent row may be the
+    // old one of a row that comes no later in this list, and one below `heavy`
+    // of none: a step's rows are all read before any of them is written.
+    if (r.len <= a.budget) return;
     const int32_t* holes = a.holes + static_cast<size_t>(row) * a.budget;
     const int32_t* fills = a.fills + static_cast<size_t>(row) * a.budget;
-    for (int j0 = rr; j0 < r.moves && on; j0 += R * U) {
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (j0 + u * R < r.moves) v[u] = *at(bt, fills[j0 + u * R]);
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (j0 + u * R < r.moves) *at(bt, holes[j0 + u * R]) = v[u];
-    }
-    if (r.len <= a.budget) return;
-    // The recent rows, in order: a row's new place may be another recent
-    // row's old one, always an earlier row of the list, so a step's rows are
-    // all read before any of them is written.
-    const int from = r.len - a.recent, to = a.budget - a.recent;
-    for (int b0 = 0; b0 < a.recent; b0 += R * U) {
-        __syncthreads();
+    const int n = r.moves + a.recent, from = r.len - a.recent - r.moves, to = a.budget - a.recent - r.moves;
+    for (int b0 = 0; b0 < n; b0 += R * U) {
+        T* dst[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int j = b0 + rr + u * R;
-            if (on && j < a.recent) v[u] = *at(bt, from + j);
+            const bool fill = j < r.moves;
+            const int src = !on || j >= n ? -1 : fill ? fills[j] : from + j;
+            if (src >= 0) {
+                v[u] = *at(bt, src);
+                dst[u] = at(bt, fill ? holes[j] : to + j);
+            } else {
+                dst[u] = nullptr;
+            }
         }
         __syncthreads();
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int j = b0 + rr + u * R;
-            if (on && j < a.recent) *at(bt, to + j) = v[u];
-        }
+        for (int u = 0; u < U; ++u)
+            if (dst[u]) *dst[u] = v[u];
     }
 }
 
 __global__ void __launch_bounds__(EV_MOVE_THREADS)
 evict_move_kernel(const __grid_constant__ EvictArgs a) {
+    grid_dependency_wait();
     const int row = blockIdx.x;
     const EvictRow r = a.rows[row];
     if (threadIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && row % a.Hkv == 0) a.new_lens[row / a.Hkv] = r.new_len;
@@ -337,13 +452,41 @@ extern "C" pa_status pa_evict(void* k_cache, void* v_cache, pa_dtype kv_dtype, f
     a.kept = kept ? kept : reinterpret_cast<int32_t*>(ws);
     a.per_part = new_block_tables ? 1024 : budget;
 
-    evict_select_kernel<<<static_cast<unsigned>(rows), EV_SEL_THREADS, 0, stream>>>(a);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return fail_cuda("evict: selection launch", e);
+    // Clusters: as many CTAs as keep a part within EV_CACHE tokens, and more
+    // while the rows would leave SMs idle and parts stay above 2048 tokens.
+    const int max_len = max_blocks_per_seq * block_size;
+    int C = 1;
+    while (C < EV_MAX_CLUSTER && (max_len > C * EV_CACHE || (rows * C < 256 && max_len > C * 2048))) C *= 2;
+    const bool cached = max_len <= C * EV_CACHE;
+    const int part = std::min(EV_CACHE, (max_len + C - 1) / C + 4);
+    const size_t smem = cached ? sizeof(uint32_t) * static_cast<size_t>(part + part / 32 + 1) : 0;
+    const void* sel = cached ? reinterpret_cast<const void*>(&evict_select_kernel<true>)
+                             : reinterpret_cast<const void*>(&evict_select_kernel<false>);
+    cudaError_t e = cudaFuncSetAttribute(sel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return fail_cuda("evict: set shared memory size", e);
     const dim3 grid(static_cast<unsigned>(rows), static_cast<unsigned>(ns),
                     static_cast<unsigned>((budget + a.per_part - 1) / a.per_part));
-    if (grid.z > 65535u) return fail(PA_ERR_UNSUPPORTED, "evict: budget too large");
-    evict_move_kernel<<<grid, EV_MOVE_THREADS, 0, stream>>>(a);
-    e = cudaGetLastError();
+    if (grid.z > 65535u || rows * C > 0x7fffffffu) return fail(PA_ERR_UNSUPPORTED, "evict: budget or batch too large");
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(C);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(rows * C));
+    cfg.blockDim = dim3(EV_SEL_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    void* args[] = {&a};
+    e = cudaLaunchKernelExC(&cfg, sel, args);
+    if (e != cudaSuccess) return fail_cuda("evict: selection launch", e);
+    // becomes resident while the selection runs, and waits for it
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(EV_MOVE_THREADS);
+    cfg.dynamicSmemBytes = 0;
+    e = cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(&evict_move_kernel), args);
     return e == cudaSuccess ? PA_OK : fail_cuda("evict: move launch", e);
 }

@@ -123,6 +123,23 @@ def test_a_long_sequence():
     c.on_gpu().run().check()
 
 
+@pytest.mark.parametrize("weights", ["heavy", "ties"])
+@pytest.mark.parametrize("width", [20000, 60000, 150000, 210000])
+def test_tables_for_more_tokens_than_any_sequence_has(weights, width):
+    """The selection is cut over 1 to 8 CTAs, and its keys kept or read again, by what the tables could hold."""
+    c = Case([3000, 40, 1201], 2, 64, 16, "f16", 500, 4, 100, seed=41, weights=weights)
+    wide = np.full((3, width // 16), -1, np.int32)
+    wide[:, :c.tables.shape[1]] = c.tables
+    c.tables = wide
+    c.on_gpu().run().check()
+    assert c.err.item() == 0
+
+
+def test_one_row_over_a_whole_cluster():
+    c = Case([30000], 1, 64, 32, "f16", 29000, 7, 3000, seed=42, weights="ties")
+    c.on_gpu().run().check()
+
+
 def test_many_sequences():
     rng = np.random.default_rng(33)
     c = Case(rng.integers(0, 150, 300), 2, 64, 16, "f16", 64, 1, 9, seed=34)
