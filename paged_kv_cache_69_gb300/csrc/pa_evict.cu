@@ -14,15 +14,19 @@
 // evict_select_kernel: a cluster of 1 to 8 CTAs per (sequence, KV head), each
 // with a contiguous part of its tokens.  The weights are read once, turned
 // into order-preserving 32-bit keys and kept in shared memory; the k-th
-// largest is found by a radix select of three digits (11, 11, 10 bits), whose
-// histograms the CTAs read from one another (distributed shared memory).  The
-// last histogram also tells each CTA how many ties lie in the parts before
-// its own.  A thread then owns a run of consecutive tokens: it ranks its
-// ties, counts the free places below `heavy` and the kept rows behind it,
-// and writes both lists in position order.
-// evict_move_kernel: a CTA moves a slice of 64 bytes (or less) of a head's
-// rows of one plane (K, V, the 4-bit parameters, the weights).  Slices share
-// no bytes, so the order that an in-place move needs holds inside a CTA.
+// largest is found by a radix select of three digits (11, 11, 10 bits): each
+// CTA counts its part, adds its bins that are not empty to the first CTA's
+// (atomics in distributed shared memory; reading all bins of all CTAs took
+// most of 160 us on 64 rows of 32k to 131k tokens), and that one finds the
+// digit.  A thread then owns a run of consecutive tokens: it ranks its ties,
+// counts the free places below `heavy` and the kept rows behind it, and
+// writes both lists in position order.
+// evict_move_kernel: a CTA moves a slice of a head's rows of one plane (K, V,
+// the 4-bit parameters, the weights).  Slices share no bytes, so the order
+// that an in-place move needs holds inside a CTA.  In place a slice is 64 bytes
+// wide, so that the few hundred rows of a steady eviction take one or two
+// steps; into other blocks 256 bytes, and the rows are cut over CTAs as well
+// (64-byte slices of 4096 rows moved 4.5 TB/s, 256-byte ones 5.6).
 #include <algorithm>
 
 #include "pa_common.h"
@@ -108,6 +112,11 @@ __device__ __forceinline__ uint32_t cluster_size() {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+__device__ __forceinline__ void peer_add(int* p, int v, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("red.relaxed.cluster.shared::cluster.add.s32 [%0], %1;" :: "r"(a), "r"(v) : "memory");
+}
 // The int at the same shared address in CTA `rank` of the cluster.
 __device__ __forceinline__ int peer_int(const int* p, uint32_t rank) {
     uint32_t a;
@@ -115,6 +124,14 @@ __device__ __forceinline__ int peer_int(const int* p, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
     asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
     return v;
+}
+
+// Sum of the ints at *p in the CTAs of lower rank, and in all; every lane.
+__device__ __forceinline__ void peer_prefix(const int* p, int rank, int C, int& lower, int& all) {
+    const int lane = threadIdx.x & 31;
+    const int v = lane < C ? peer_int(p, lane) : 0;
+    lower = __reduce_add_sync(0xffffffffu, lane < rank ? v : 0);
+    all = __reduce_add_sync(0xffffffffu, v);
 }
 
 constexpr int EV_BINS = 2048;
@@ -128,7 +145,7 @@ __global__ void __launch_bounds__(EV_SEL_THREADS)
 evict_select_kernel(const __grid_constant__ EvictArgs a) {
     __shared__ int hist[3][EV_BINS];
     __shared__ int sums[EV_SEL_THREADS / 32];
-    __shared__ int s_bad, s_digit, s_above, s_nh, s_nf;
+    __shared__ int s_bad, s_digit, s_above, s_ties, s_nh, s_nf;
     extern __shared__ uint32_t s_keys[];
     constexpr int NT = EV_SEL_THREADS;
     grid_dependents_launch();
@@ -172,6 +189,7 @@ evict_select_kernel(const __grid_constant__ EvictArgs a) {
         return;
     }
     const int heavy = a.budget - a.recent, end = L - a.recent;
+    auto sync = [&] { if (C > 1) cluster_sync(); else __syncthreads(); };
     const int k = heavy - a.sink;                   // tokens chosen by weight, of [sink, end)
     const int seg = ((end + C - 1) / C + 3) & ~3;   // this CTA: tokens [lo, hi)
     const int lo = min(rank * seg, end), hi = min(end, lo + seg);
@@ -214,6 +232,7 @@ evict_select_kernel(const __grid_constant__ EvictArgs a) {
                     }
             }
         }
+        if (C > 1) cluster_sync();                  // the first CTA's bins are zeroed
 #pragma unroll 1
         for (int d = 0; d < 3; ++d) {
             const int shift = d == 0 ? 21 : d == 1 ? 10 : 0;
@@ -225,44 +244,51 @@ evict_select_kernel(const __grid_constant__ EvictArgs a) {
                         atomicAdd(&hist[d][(key >> shift) & (d == 1 ? 2047u : 1023u)], 1);
                 }
             }
-            cluster_sync();
-            // digits from the largest down, EV_BINS / NT per thread
-            constexpr int PB = EV_BINS / NT;
-            int cnt[PB], mine = 0;
-#pragma unroll
-            for (int e = 0; e < PB; ++e) {
-                const int* h = &hist[d][EV_BINS - 1 - (tid * PB + e)];
-                cnt[e] = 0;
-                for (int r = 0; r < C; ++r) cnt[e] += C == 1 ? *h : peer_int(h, r);
-                mine += cnt[e];
+            if (C > 1) {
+                __syncthreads();
+                if (rank > 0)
+                    for (int x = tid; x < EV_BINS; x += NT)
+                        if (const int v = hist[d][x]) peer_add(&hist[d][x], v, 0);
             }
-            int total, before = block_scan_excl(mine, sums, total);
-            if (before < need && need <= before + mine) {
+            sync();
+            if (rank == 0) {
+                // digits from the largest down, EV_BINS / NT per thread
+                constexpr int PB = EV_BINS / NT;
+                int cnt[PB], mine = 0;
 #pragma unroll
                 for (int e = 0; e < PB; ++e) {
-                    if (before < need && need <= before + cnt[e]) {
-                        s_digit = EV_BINS - 1 - (tid * PB + e);
-                        s_above = before;
+                    cnt[e] = hist[d][EV_BINS - 1 - (tid * PB + e)];
+                    mine += cnt[e];
+                }
+                int total, before = block_scan_excl(mine, sums, total);
+                if (before < need && need <= before + mine) {
+#pragma unroll
+                    for (int e = 0; e < PB; ++e) {
+                        if (before < need && need <= before + cnt[e]) {
+                            s_digit = EV_BINS - 1 - (tid * PB + e);
+                            s_above = before;
+                        }
+                        before += cnt[e];
                     }
-                    before += cnt[e];
                 }
             }
-            __syncthreads();
-            thr |= static_cast<uint32_t>(s_digit) << shift;
-            need -= s_above;
-            __syncthreads();
+            sync();
+            thr |= static_cast<uint32_t>(C > 1 ? peer_int(&s_digit, 0) : s_digit) << shift;
+            need -= C > 1 ? peer_int(&s_above, 0) : s_above;
         }
     }
     for (int j = rank * NT + tid; j < a.budget; j += C * NT) kept[j] = j < heavy ? j : end + (j - heavy);
-    // ties in the parts before this one: counted by their last histogram
-    int ties = 0;
-    if (k > 0)
-        for (int r = 0; r < rank; ++r) ties += peer_int(&hist[2][thr & 1023u], r);
     const int run = (hi - lo + NT - 1) / NT, r0 = min(hi, lo + tid * run), r1 = min(hi, r0 + run);
-    int total, mine = 0;
+    int total, mine = 0, lower, all;
     if (k > 0)
         for (int pos = r0; pos < r1; ++pos) mine += (cand(pos) && key_at(pos) == thr) ? 1 : 0;
-    ties += block_scan_excl(mine, sums, total);
+    int ties = block_scan_excl(mine, sums, total);
+    if (C > 1) {
+        if (tid == 0) s_ties = total;
+        cluster_sync();
+        peer_prefix(&s_ties, rank, C, lower, all);
+        ties += lower;
+    }
     // one walk over the run: f(position, kept)
     auto walk = [&](auto f) {
         int t = ties;
@@ -281,19 +307,30 @@ evict_select_kernel(const __grid_constant__ EvictArgs a) {
         h += (pos < heavy && !keep) ? 1 : 0;
         f += (pos >= heavy && keep) ? 1 : 0;
     });
-    int th, tf;
-    int h0 = block_scan_excl(h, sums, th), f0 = block_scan_excl(f, sums, tf);
-    if (tid == 0) { s_nh = th; s_nf = tf; }
-    cluster_sync();
-    for (int r = 0; r < rank; ++r) { h0 += peer_int(&s_nh, r); f0 += peer_int(&s_nf, r); }
-    int nf = 0;
-    for (int r = 0; r < C; ++r) nf += peer_int(&s_nf, r);
+    int h0, f0, nf;
+    if constexpr (CACHED) {                        // counts of at most EV_CACHE: both in one scan
+        const int at = block_scan_excl(h | (f << 16), sums, total);
+        h0 = at & 0xffff; f0 = at >> 16;
+        h = total & 0xffff; nf = total >> 16;
+    } else {
+        h0 = block_scan_excl(h, sums, h);
+        f0 = block_scan_excl(f, sums, nf);
+    }
+    if (C > 1) {
+        if (tid == 0) { s_nh = h; s_nf = nf; }
+        cluster_sync();
+        peer_prefix(&s_nh, rank, C, lower, all);
+        h0 += lower;
+        peer_prefix(&s_nf, rank, C, lower, all);
+        f0 += lower;
+        nf = all;
+    }
     walk([&](int pos, bool keep) {
         if (pos < heavy && !keep) holes[h0++] = pos;
         if (pos >= heavy && keep) fills[f0++] = pos;
     });
     __threadfence();
-    cluster_sync();                                // every list entry written, every peer's counts read
+    sync();                                        // every list entry written, every peer's counts read
     for (int r = rank * NT + tid; r < nf; r += C * NT) kept[__ldcg(holes + r)] = __ldcg(fills + r);
     if (rank == 0 && tid == 0) a.rows[row] = EvictRow{L, a.budget, nf, 1};
 }
@@ -422,7 +459,8 @@ extern "C" pa_status pa_evict(void* k_cache, void* v_cache, pa_dtype kv_dtype, f
     int ns = 0, np = 0;
     auto add_plane = [&](uint8_t* base, size_t bstride, uint32_t tstride, uint32_t hstride, int width, int unit) {
         a.plane[np] = EvictPlane{base, bstride, tstride, hstride};
-        for (int c = 0; c < width; c += 64) a.slice[ns++] = EvictSlice{np, c, std::min(64, width - c), unit};
+        const int w = new_block_tables ? 256 : 64;
+        for (int c = 0; c < width; c += w) a.slice[ns++] = EvictSlice{np, c, std::min(w, width - c), unit};
         ++np;
     };
     for (int kv = 0; kv < 2; ++kv) {
@@ -450,7 +488,7 @@ extern "C" pa_status pa_evict(void* k_cache, void* v_cache, pa_dtype kv_dtype, f
     a.holes = reinterpret_cast<int32_t*>(ws); ws += list;
     a.fills = reinterpret_cast<int32_t*>(ws); ws += list;
     a.kept = kept ? kept : reinterpret_cast<int32_t*>(ws);
-    a.per_part = new_block_tables ? 1024 : budget;
+    a.per_part = new_block_tables ? 256 : budget;
 
     // Clusters: as many CTAs as keep a part within EV_CACHE tokens, and more
     // while the rows would leave SMs idle and parts stay above 2048 tokens.
