@@ -11,6 +11,15 @@
 // nibble of a byte) or 16 c * 2^-24 (high nibble), with no conversion, and the
 // powers of two are taken out of the sums.
 //
+// The second product sums thousands of tokens in f32, and all codes are
+// positive: its sum would grow with the number of tokens, while the output is
+// what is left of it after low's part is taken off, so that every rounding of
+// the accumulator weighs the more the longer the sequence is (0.0029 relative
+// error at 131072 tokens, against 0.0017 of the bf16 output itself).  So the
+// sum of 8 times the weights is formed beside it, by one more MMA per 16 tokens,
+// and taken off every four chunks: the sums are then over (c - 8) step, and
+// low + 8 step takes the place of low.
+//
 // Both products are transposed: S^T = K Q^T with 16 tokens and O^T = V^T P^T
 // with 16 dimensions as the M rows of mma.sync m16n8k16 and 8 query rows as N,
 // so a GQA group of up to 8 heads fills the tile.  head_dim is summed in an
@@ -351,11 +360,12 @@ __device__ __forceinline__ uint32_t pack_out(float a, float b) {
 
 // ---------------------------------------------------------------------------
 // consumer: warp w owns NQT tiles of 8 query rows of one KV head.
-// HL: each weight enters the second product as a pair of f16 numbers (the
-// rounded weight and what the rounding lost).  WT: pa_decode_weights, the
-// scores and (m, l) are kept.
+// The weights enter the second product rounded to f16 (11 bits), whatever the
+// output's type: each rounding meets a (c - 8) step, a value about its row's
+// middle, so the output's error is that of rounding p itself.  WT:
+// pa_decode_weights, the scores and (m, l) are kept.
 // ---------------------------------------------------------------------------
-template <class QT, int D, int NQT, bool HL, bool WT>
+template <class QT, int D, int NQT, bool WT>
 __device__ __forceinline__ void int4_consumer(const Int4Params& a, const Plan& pl, int hg, int w, uint8_t* base,
                                               uint64_t* full, uint64_t* empty, uint64_t* qempty, uint64_t* joined,
                                               const I4Desc* descs) {
@@ -396,14 +406,14 @@ __device__ __forceinline__ void int4_consumer(const Int4Params& a, const Plan& p
     const uint32_t ov0 = tv0 * (D / 2) + g4 * (D / 16), ov1 = tv1 * (D / 2) + g4 * (D / 16);   // and of two value rows
 
     float acc[OT][NQT][4];
+    float eight[NQT][4];                          // 8 * (sum of the weights) since it was last taken off acc
     // The warp's query operand, [tile][word][lane] 16 bytes, kept in shared
     // memory: the registers it would take buy another CTA per SM.
     const uint32_t qf = base32 + a.frag_off + static_cast<uint32_t>(w * NQT * KW * 512) + lane * 16u;
     // rows 2 t4 and 2 t4 + 1 of each tile: reference of the exponent (a row's
     // largest score within 2^8, 0 while it has none), sum of the weights, sum
-    // of weight * low; the last two over the lane's tokens
+    // of weight * (low + 8 step); the last two over the lane's tokens
     float m[NQT][2], l[NQT][2], c0[NQT][2];
-    float top[NQT][2], mu[NQT][2];                // m + 8, and m or 0 while it is -infinity
     float sq[NQT][2];                             // sum of the query row, times the score scale
     float unit_qk = 0.f;                          // score of one unit of the codes' dot product
     int jt[NQT][2], lim[NQT][2];
@@ -509,9 +519,10 @@ __device__ __forceinline__ void int4_consumer(const Int4Params& a, const Plan& p
             for (int n = 0; n < NQT; ++n) {
 #pragma unroll
                 for (int o = 0; o < OT; ++o) acc[o][n][0] = acc[o][n][1] = acc[o][n][2] = acc[o][n][3] = 0.f;
+                eight[n][0] = eight[n][1] = eight[n][2] = eight[n][3] = 0.f;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    m[n][e] = top[n][e] = -INFINITY; mu[n][e] = l[n][e] = c0[n][e] = 0.f;
+                    m[n][e] = -INFINITY; l[n][e] = c0[n][e] = 0.f;
                     if (p.q_start) lim[n][e] = ((in_rows >> (2 * n + e)) & 1) && jt[n][e] < d.qn ? d.qpos0 + jt[n][e] : -1;
                 }
             }
@@ -609,7 +620,7 @@ __device__ __forceinline__ void int4_consumer(const Int4Params& a, const Plan& p
                             }
                         }
             }
-            // ---- V parameters: (step, low) of the lane's two tokens of each tile ----
+            // ---- V parameters: step and low + 8 step of the lane's two tokens of each tile ----
             float vs[MT][2], vl[MT][2];
             float smax = 0.f;
 #pragma unroll
@@ -617,7 +628,7 @@ __device__ __forceinline__ void int4_consumer(const Int4Params& a, const Plan& p
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const float2 v = lds_params(pr[2 * mt + e] + VOFF + POFF);
-                    vs[mt][e] = v.x; vl[mt][e] = v.y;
+                    vs[mt][e] = v.x; vl[mt][e] = fmaf(8.f, v.x, v.y);
                 }
             if (!all) {                               // the pool may hold NaN where no token is
 #pragma unroll
@@ -642,7 +653,7 @@ __device__ __forceinline__ void int4_consumer(const Int4Params& a, const Plan& p
                     mx[n][e] = -INFINITY;
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) mx[n][e] = fmaxf(mx[n][e], fmaxf(s[mt][n][e], s[mt][n][e + 2]));
-                    far = far || mx[n][e] > top[n][e];
+                    far = far || mx[n][e] > m[n][e] + 8.f;
                 }
             if (__any_sync(0xffffffffu, far)) {
                 smax = max_g4(smax);
@@ -662,8 +673,6 @@ __device__ __forceinline__ void int4_consumer(const Int4Params& a, const Plan& p
                         const float mn = fmaxf(m[n][e], max_g4(mx[n][e]));
                         const float al = m[n][e] == mn ? 1.f : ex2_approx(m[n][e] - mn);
                         m[n][e] = mn;
-                        top[n][e] = mn + 8.f;
-                        mu[n][e] = mn == -INFINITY ? 0.f : mn;
                         l[n][e] *= al;
                         c0[n][e] *= al;
                         f[e] = al * grow;
@@ -672,17 +681,19 @@ __device__ __forceinline__ void int4_consumer(const Int4Params& a, const Plan& p
                     for (int o = 0; o < OT; ++o) {
                         acc[o][n][0] *= f[0]; acc[o][n][1] *= f[1]; acc[o][n][2] *= f[0]; acc[o][n][3] *= f[1];
                     }
+                    eight[n][0] *= f[0]; eight[n][1] *= f[1]; eight[n][2] *= f[0]; eight[n][3] *= f[1];
                 }
             }
-            uint32_t pf[MT][NQT][2], pl_[HL ? MT : 1][NQT][2];
+            uint32_t pf[MT][NQT][2];
 #pragma unroll
             for (int n = 0; n < NQT; ++n)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
+                    const float mu = m[n][e] == -INFINITY ? 0.f : m[n][e];
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) {
-                        s[mt][n][e] = ex2_approx(s[mt][n][e] - mu[n][e]);
-                        s[mt][n][e + 2] = ex2_approx(s[mt][n][e + 2] - mu[n][e]);
+                        s[mt][n][e] = ex2_approx(s[mt][n][e] - mu);
+                        s[mt][n][e + 2] = ex2_approx(s[mt][n][e + 2] - mu);
                         l[n][e] += s[mt][n][e] + s[mt][n][e + 2];
                         c0[n][e] = fmaf(s[mt][n][e], vl[mt][0], fmaf(s[mt][n][e + 2], vl[mt][1], c0[n][e]));
                     }
@@ -696,12 +707,6 @@ __device__ __forceinline__ void int4_consumer(const Int4Params& a, const Plan& p
                     const uint32_t h0 = f32x2_to_f16x2(x0, x1), h1 = f32x2_to_f16x2(x2, x3);
                     pf[mt][n][0] = movmatrix(h0);
                     pf[mt][n][1] = movmatrix(h1);
-                    if constexpr (HL) {
-                        const float2 y0 = __half22float2(*reinterpret_cast<const __half2*>(&h0));
-                        const float2 y1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
-                        pl_[mt][n][0] = movmatrix(f32x2_to_f16x2(x0 - y0.x, x1 - y0.y));
-                        pl_[mt][n][1] = movmatrix(f32x2_to_f16x2(x2 - y1.x, x3 - y1.y));
-                    }
                 }
             }
             // ---- O^T += V^T P^T ----
@@ -732,6 +737,9 @@ __device__ __forceinline__ void int4_consumer(const Int4Params& a, const Plan& p
                         q8[x][2 * y] = q[x][2 * y] >> 8;
                         q8[x][2 * y + 1] = q[x][2 * y + 1] >> 8;
                     }
+                const uint32_t mid[4] = {0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u};   // code 8
+#pragma unroll
+                for (int n = 0; n < NQT; ++n) mma_16816<false>(eight[n], mid, pf[mt][n][0], pf[mt][n][1]);
 #pragma unroll
                 for (int o = 0; o < OT; ++o) {
                     // head_dim 128: tile o has dimensions 16 g4 + o and 16 g4 + 8 + o (nibble o of both words);
@@ -745,10 +753,19 @@ __device__ __forceinline__ void int4_consumer(const Int4Params& a, const Plan& p
 #pragma unroll
                     for (int n = 0; n < NQT; ++n) {
                         mma_16816<false>(acc[o][n], A, pf[mt][n][0], pf[mt][n][1]);
-                        if constexpr (HL) mma_16816<false>(acc[o][n], A, pl_[mt][n][0], pl_[mt][n][1]);
                     }
                 }
             }
+        }
+        if ((st & 3) == 3 || (d.flags & SEG_END)) {
+#pragma unroll
+            for (int n = 0; n < NQT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+#pragma unroll
+                    for (int o = 0; o < OT; ++o) acc[o][n][e] = fmaf(eight[n][e], (o & 1) ? -16.f : -1.f, acc[o][n][e]);
+                    eight[n][e] = 0.f;
+                }
         }
         if constexpr (WT) sdst += static_cast<size_t>(p.Hq) << ct_log2;
         __syncwarp();
@@ -852,7 +869,7 @@ __device__ __forceinline__ void int4_consumer(const Int4Params& a, const Plan& p
 
 // MAXW: consumer warps at most, CTAS: CTAs per SM that the registers are
 // limited for.
-template <class QT, int D, int NQT, bool HL, bool WT, int MAXW, int CTAS>
+template <class QT, int D, int NQT, bool WT, int MAXW, int CTAS>
 __global__ void __launch_bounds__((MAXW + 1) * 32, CTAS)
 int4_decode_kernel(const __grid_constant__ Int4Params a) {
     extern __shared__ uint8_t smem_raw[];
@@ -891,20 +908,20 @@ int4_decode_kernel(const __grid_constant__ Int4Params a) {
     }
     __syncthreads();
     if (warp == p.NCW) int4_producer<D, WT>(a, pl, hg, base, full, empty, qempty, descs);
-    else if (warp < p.NCW) int4_consumer<QT, D, NQT, HL, WT>(a, pl, hg, warp, base, full, empty, qempty, joined, descs);
+    else if (warp < p.NCW) int4_consumer<QT, D, NQT, WT>(a, pl, hg, warp, base, full, empty, qempty, joined, descs);
 }
 
-template <class QT, int D, int NQT, bool HL, bool WT>
+template <class QT, int D, int NQT, bool WT>
 static const void* int4_fn_w(int ncw) {
     // more than four row tiles of a head: 65 to 128 rows, 16 per warp
     if constexpr (NQT == 2)
-        if (ncw > I4_WARPS) return reinterpret_cast<const void*>(&int4_decode_kernel<QT, D, NQT, HL, WT, 8, 1>);
-    return reinterpret_cast<const void*>(&int4_decode_kernel<QT, D, NQT, HL, WT, I4_WARPS, i4_ctas(NQT)>);
+        if (ncw > I4_WARPS) return reinterpret_cast<const void*>(&int4_decode_kernel<QT, D, NQT, WT, 8, 1>);
+    return reinterpret_cast<const void*>(&int4_decode_kernel<QT, D, NQT, WT, I4_WARPS, i4_ctas(NQT)>);
 }
-template <class QT, bool HL, bool WT>
+template <class QT, bool WT>
 static const void* int4_fn(int D, int nqt, int ncw) {
-    if (D == 128) return nqt == 1 ? int4_fn_w<QT, 128, 1, HL, WT>(ncw) : int4_fn_w<QT, 128, 2, HL, WT>(ncw);
-    return nqt == 1 ? int4_fn_w<QT, 64, 1, HL, WT>(ncw) : int4_fn_w<QT, 64, 2, HL, WT>(ncw);
+    if (D == 128) return nqt == 1 ? int4_fn_w<QT, 128, 1, WT>(ncw) : int4_fn_w<QT, 128, 2, WT>(ncw);
+    return nqt == 1 ? int4_fn_w<QT, 64, 1, WT>(ncw) : int4_fn_w<QT, 64, 2, WT>(ncw);
 }
 
 static int cdiv_ll(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
@@ -970,8 +987,8 @@ pa_status decode_int4(const Int4Call& c) {
     p.part_ml = c.ws.part_ml; p.part_acc = c.ws.part_acc;
 
     const bool h = c.q_dtype == PA_F16;
-    const void* kern = c.weights ? (h ? int4_fn<F16T, true, true>(D, nqt, NCW) : int4_fn<BF16T, false, true>(D, nqt, NCW))
-                                 : (h ? int4_fn<F16T, true, false>(D, nqt, NCW) : int4_fn<BF16T, false, false>(D, nqt, NCW));
+    const void* kern = c.weights ? (h ? int4_fn<F16T, true>(D, nqt, NCW) : int4_fn<BF16T, true>(D, nqt, NCW))
+                                 : (h ? int4_fn<F16T, false>(D, nqt, NCW) : int4_fn<BF16T, false>(D, nqt, NCW));
     if (c.weights) { p.scores = c.weights->scores; p.lse = c.weights->lse; p.chunk0 = c.weights->chunk0; }
     cudaError_t ce = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (ce != cudaSuccess) return fail_cuda("decode: set shared memory size", ce);
