@@ -246,7 +246,8 @@ pa_status pa_decode_noalloc(void* out, const void* q, pa_dtype q_dtype,
  * nearest even, saturation to +-448; NaN becomes the NaN code.  Sources for
  * an fp8 cache may be f32, f16 or bf16; other caches need src == kv dtype.
  * A 4-bit cache quantises each row on write (head of this file) from f32, f16
- * or bf16; it needs head_dim 64 or 128 and a block_size of a multiple of 8.
+ * or bf16; it needs head_dim 64 or 128, a block_size of a multiple of 8, and
+ * fewer than 2^31 rows (tokens x heads) and pool slots.
  * Duplicate slots within one call leave one of the writes (unspecified which).
  */
 pa_status pa_reshape_and_cache(void* k_cache, void* v_cache, pa_dtype kv_dtype,
@@ -266,7 +267,8 @@ pa_status pa_reshape_and_cache(void* k_cache, void* v_cache, pa_dtype kv_dtype,
  * f32, f16 and bf16 caches need dst_dtype == kv_dtype and move bits; fp8
  * caches (code times k_scale or v_scale) and 4-bit caches (low + step * c)
  * give f32, f16 or bf16, computed in f32 and rounded to nearest even.  The
- * same slot may appear more than once.  head_dim 64 or 128.
+ * same slot may appear more than once.  head_dim 64 or 128; fewer than 2^31
+ * rows (tokens x heads) and pool slots.
  */
 pa_status pa_gather_cache(void* key, void* value, pa_dtype dst_dtype,
                           const void* k_cache, const void* v_cache, pa_dtype kv_dtype,

@@ -43,15 +43,26 @@ __device__ __forceinline__ float two_sum(float a, float b, float& lost) {
     return s;
 }
 
-// (step, low) of a row with the given extremes.  The quotient is rounded to
-// odd in f32 before its rounding to f16, so that the two roundings give what
-// one from the exact value would.
+// 1 / x to 1 ulp (PTX ISA: rcp.approx.ftz.f32).
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// (step, low) of a row with the given extremes.  The quotient a / 15 is
+// rounded to odd in f32 before its rounding to f16, so that the two roundings
+// give what one from the exact value would: a product with 1 / 15, corrected
+// once, is the nearest f32 or next to it, and the residual a - 15 s, exact, says
+// on which side the quotient lies.
 __device__ __forceinline__ void int4_params(float mn, float mx, __half& step, __half& low) {
     low = __float2half_rn(mn);
     float lost;
-    const float a = two_sum(mx, -__half2float(low), lost);
-    float s = a > 0.f ? __fdiv_rn(a, 15.f) : 0.f;
-    const float r = __fadd_rn(__fmaf_rn(-s, 15.f, a), lost);       // sign of the exact quotient minus s
+    const float a = fmaxf(two_sum(mx, -__half2float(low), lost), 0.f);
+    constexpr float R15 = 1.f / 15.f;
+    float s = a * R15;
+    s = __fmaf_rn(__fmaf_rn(-s, 15.f, a), R15, s);
+    const float r = __fadd_rn(__fmaf_rn(-s, 15.f, a), lost);
     uint32_t b = __float_as_uint(s);
     if (s > 0.f && r != 0.f && !(b & 1u)) b += r > 0.f ? 1u : 0xffffffffu;
     step = __float2half_rn(__uint_as_float(b));
@@ -69,6 +80,37 @@ __device__ __forceinline__ uint32_t int4_code(float x, float low, float step, fl
     const uint32_t ci = static_cast<uint32_t>(c);
     return min(ci + ((t > 0.f || (t == 0.f && (ci & 1u))) ? 1u : 0u), 15u);
 }
+
+// The codes of 8 elements as one word, for r15 = 1 / (15 step).  The quotient
+// in plain f32 is off by less than 2^-17 (two roundings of 2^-24 and r15's
+// 2^-23, at most 15), so it decides the code unless it lies that near a half; `near`
+// then asks for int4_code.  The multiplication saturates to [0, 1], and
+// adding 1.5 * 2^23 rounds to the nearest integer and leaves it in the low
+// bits, whose constant upper part is taken off the finished word.
+__device__ __forceinline__ uint32_t int4_codes8(const float (&x)[8], float low, float r15, float& near) {
+    constexpr float MAGIC = 12582912.f;                    // bits 0x4b400000
+    uint32_t w = 0;
+#pragma unroll
+    for (int k = 7; k >= 0; --k) {
+        const float q = __saturatef((x[k] - low) * r15);
+        const float t = __fmaf_rn(q, 15.f, MAGIC);
+        near = fmaxf(near, fabsf(__fmaf_rn(q, 15.f, -__fsub_rn(t, MAGIC))));
+        w = w * 16u + __float_as_uint(t);
+    }
+    return w - 0x4b400000u * 0x11111111u;
+}
+// Smaller and larger, NaN if either is.
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+constexpr float INT4_NEAR = 0.5f - 1.52587890625e-5f;      // 1/2 - 2^-16
 
 // The value of a code: step * c is exact in f32, the sum is rounded once.
 __device__ __forceinline__ float int4_value(uint32_t c, float low, float step) {
