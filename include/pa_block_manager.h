@@ -93,6 +93,17 @@ pa_bm_status pa_bm_append_slots(pa_bm* m, int32_t n, const int64_t* reqs, int64_
  * it. */
 pa_bm_status pa_bm_cache_block(pa_bm* m, int64_t req, int32_t j, const uint8_t* hash);
 
+/* Cut a complete request down to its first num_tokens places, for pa_evict in
+ * place: the blocks behind them are released, last block first, and every
+ * block it keeps loses its prefix-cache hash, since pa_evict rewrites them.
+ * A request that is no longer than num_tokens is left as it is.  Call it
+ * before pa_evict is enqueued, with the block table taken before this call:
+ * later writes into the released blocks follow it on the stream.
+ * PA_BM_BAD_REQUEST (nothing changed) also if one of its blocks is shared:
+ * evict such a request into the blocks of a new one (pa_bm_allocate of
+ * num_tokens tokens) and free it then. */
+pa_bm_status pa_bm_shrink(pa_bm* m, int64_t req, int64_t num_tokens);
+
 /* Release a request (complete or waiting). */
 pa_bm_status pa_bm_free(pa_bm* m, int64_t req);
 

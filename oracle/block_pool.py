@@ -266,6 +266,26 @@ class BlockManager:
     def cache_block(self, req_id: int, j: int, h: bytes) -> None:
         self.pool.cache_full_block(self.reqs[req_id].blocks[j], h)
 
+    def shrink(self, req_id: int, num_tokens: int) -> None:
+        """Keep the request's first ``num_tokens`` places (its rows are
+        rewritten in place by an eviction): blocks behind them are freed last
+        first, and no block of it can be found by its hash any more."""
+        r = self.reqs[req_id]
+        if r.swapped or len(r.blocks) != r.need:
+            raise RuntimeError("shrink of a waiting or swapped-out request")
+        if r.num_tokens <= num_tokens:
+            return
+        if any(b.ref_cnt != 1 for b in r.blocks):
+            raise RuntimeError("shrink of a request with shared blocks")
+        for b in r.blocks:
+            self.pool._maybe_evict_cached_block(b)
+        r.hashes = []
+        r.need = -(-num_tokens // self.block_size)
+        behind = r.blocks[r.need:]
+        r.blocks = r.blocks[:r.need]
+        self.pool.free_blocks(behind[::-1])
+        r.num_tokens = num_tokens
+
     def free(self, req_id: int) -> None:
         r = self.reqs.pop(req_id)
         self.pool.free_blocks([b for b in reversed(r.blocks) if b is not None])

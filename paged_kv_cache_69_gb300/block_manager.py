@@ -29,7 +29,7 @@ EXPORTED = ("pa_bm_create", "pa_bm_destroy", "pa_bm_num_free", "pa_bm_ref_cnt", 
             "pa_bm_allocate", "pa_bm_resume", "pa_bm_fork", "pa_bm_append_slots", "pa_bm_cache_block",
             "pa_bm_free", "pa_bm_num_tokens", "pa_bm_block_table", "pa_bm_block_tables",
             "pa_bm_block_tables_update", "pa_bm_set_host_pool", "pa_bm_num_host_free", "pa_bm_swap_out",
-            "pa_bm_swap_in")
+            "pa_bm_swap_in", "pa_bm_shrink")
 ROW_DTYPE = np.dtype([("req", "<i8"), ("epoch", "<u4"), ("len", "<i4")])
 
 _lib = None
@@ -66,6 +66,8 @@ def host_lib():
         L.pa_bm_cache_block.argtypes = [vp, i64, i32, vp]
         L.pa_bm_free.restype = ctypes.c_int
         L.pa_bm_free.argtypes = [vp, i64]
+        L.pa_bm_shrink.restype = ctypes.c_int
+        L.pa_bm_shrink.argtypes = [vp, i64, i64]
         L.pa_bm_num_tokens.restype = i64
         L.pa_bm_num_tokens.argtypes = [vp, i64]
         L.pa_bm_block_table.restype = i32
@@ -202,6 +204,14 @@ class HostBlockManager:
         st = self.lib.pa_bm_free(self._h, int(req))
         if st != BM_OK:
             raise BlockManagerError(st, f"free request {req}")
+
+    def shrink(self, req: int, num_tokens: int) -> None:
+        """Cut a request down to ``num_tokens`` places, for pa_evict in place
+        over the block table taken before this call; raises (nothing changed)
+        if one of its blocks is shared."""
+        st = self.lib.pa_bm_shrink(self._h, int(req), int(num_tokens))
+        if st != BM_OK:
+            raise BlockManagerError(st, f"shrink request {req}")
 
     # -- preemption by swapping ------------------------------------------------
     def set_host_pool(self, num_host_blocks: int, order: Optional[Sequence[int]] = None) -> None:

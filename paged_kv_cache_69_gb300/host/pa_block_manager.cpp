@@ -277,6 +277,28 @@ pa_bm_status pa_bm_cache_block(pa_bm* m, int64_t req, int32_t j, const uint8_t* 
     return PA_BM_OK;
 }
 
+pa_bm_status pa_bm_shrink(pa_bm* m, int64_t req, int64_t num_tokens) {
+    if (!m || num_tokens < 0) return PA_BM_INVALID_ARG;
+    auto it = m->reqs.find(req);
+    if (it == m->reqs.end()) return PA_BM_BAD_REQUEST;
+    Request& r = it->second;
+    if (r.swapped || static_cast<int32_t>(r.blocks.size()) != r.need) return PA_BM_BAD_REQUEST;
+    if (r.num_tokens <= num_tokens) return PA_BM_OK;
+    for (int32_t b : r.blocks)
+        if (m->ref[b] != 1) return PA_BM_BAD_REQUEST;
+    const size_t keep = static_cast<size_t>((num_tokens + m->bs - 1) / m->bs);
+    for (int32_t b : r.blocks) m->evict(b);                    // rewritten: findable no longer
+    r.hashes.clear();
+    while (r.blocks.size() > keep) {                            // last block first
+        m->release(r.blocks.back());
+        r.blocks.pop_back();
+    }
+    r.num_tokens = num_tokens;
+    r.need = static_cast<int32_t>(keep);
+    r.epoch = m->next_epoch++;
+    return PA_BM_OK;
+}
+
 pa_bm_status pa_bm_free(pa_bm* m, int64_t req) {
     if (!m) return PA_BM_INVALID_ARG;
     auto it = m->reqs.find(req);

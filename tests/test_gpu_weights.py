@@ -319,3 +319,52 @@ def test_decode_and_evict_as_a_server_runs_them(kv):
             lens = [min(L, budget) for L in lens]
             assert sl.tolist() == lens
     assert evictions >= 3 and err.item() == 0
+
+
+def test_manager_gives_back_what_eviction_frees():
+    """The host manager's tables through prompts, decode steps and evictions: blocks that a shrink released are taken
+    and overwritten by another request, and the evicted one still attends exactly its kept rows."""
+    from paged_kv_cache_69_gb300 import block_manager as hbm
+    rng = np.random.default_rng(51)
+    bs, nb, Hkv, D, Hq, budget, maxb = 16, 24, 2, 64, 4, 48, 16
+    m = hbm.HostBlockManager(nb, bs, rng.permutation(nb).tolist())
+    k = torch.zeros(nb, bs, Hkv, D, dtype=torch.float16, device="cuda")
+    v = torch.zeros_like(k)
+    wd = torch.zeros(nb, Hkv, bs, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def tokens(req, lo, hi):
+        x = [torch.from_numpy(rng.standard_normal((hi - lo, Hkv, D))).half() for _ in range(2)]
+        t = m.block_table(req)
+        s = torch.tensor([t[p // bs] * bs + p % bs for p in range(lo, hi)])
+        pa.pa_reshape_and_cache(k, v, x[0].cuda(), x[1].cuda(), s.cuda(), err_flag=err)
+        return x
+
+    m.allocate(0, 150)
+    pk, pv = tokens(0, 0, 150)
+    q = torch.from_numpy(rng.standard_normal((1, Hq, D))).half().cuda()
+    bt = torch.as_tensor(m.block_tables([0], maxb).copy()).cuda()
+    sl = torch.tensor([150], dtype=torch.int32, device="cuda")
+    out = torch.empty_like(q)
+    pa.pa_decode_weights(out, wd, q, k, v, bt, sl, 0.125, fresh=sl.clone(), err_flag=err)
+    kept = torch.empty(1, Hkv, budget, dtype=torch.int32, device="cuda")
+    free = m.num_free()
+    m.shrink(0, budget)
+    assert m.num_free() == free + 7
+    pa.pa_evict(k, v, wd, bt, sl, sl, budget, num_sink=2, num_recent=8, kept=kept, err_flag=err)
+    m.allocate(1, m.num_free() * bs)                       # takes the released blocks
+    tokens(1, 0, m.num_tokens(1))
+    bt = torch.as_tensor(m.block_tables([0], maxb).copy()).cuda()
+    pa.pa_decode(out, q, k, v, bt, sl, 0.125, err_flag=err)
+    got = out.double().cpu().numpy()
+    src = kept.cpu().numpy()[0]
+    assert sl.item() == budget and err.item() == 0
+    for h in range(Hq):
+        t = src[h // 2]
+        assert len(set(t.tolist())) == budget and set(range(2)) <= set(t.tolist()) and t[-8:].tolist() == list(range(142, 150))
+        K, V = pk[t, h // 2].double().numpy(), pv[t, h // 2].double().numpy()
+        s = K @ q[0, h].double().cpu().numpy() * 0.125
+        p = np.exp(s - s.max())
+        p /= p.sum()
+        # f16 output, probabilities rounded to f16; scores in f32
+        assert (np.abs(got[0, h] - p @ V) <= 2.0 ** -11 * np.abs(p @ V) + (2.0 ** -11 + 2.0 ** -17) * (p @ np.abs(V)) + 2.0 ** -25).all()
