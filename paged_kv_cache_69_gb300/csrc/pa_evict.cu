@@ -162,28 +162,33 @@ evict_select_kernel(const __grid_constant__ EvictArgs a) {
     __syncthreads();
     bool bad_len = L < 0 || static_cast<long long>(L) > static_cast<long long>(a.MB) * a.bs;
     if (a.new_tables) bad_len = bad_len || static_cast<long long>(n) > static_cast<long long>(a.newMB) * a.bs;
-    if (!bad_len) {
+    // blocks of table t from j0 on, up to j1, over `of` CTAs of the cluster
+    auto check = [&](const int32_t* t, int j0, int j1, int of) {
         bool bad = false;
-        for (int j = tid; j < (L + a.bs - 1) >> a.shift; j += NT) bad |= bt[j] < 0 || bt[j] >= a.NB;
-        if (a.new_tables) {
-            const int32_t* nt = a.new_tables + static_cast<size_t>(i) * a.newMB;
-            for (int j = tid; j < (n + a.bs - 1) >> a.shift; j += NT) bad |= nt[j] < 0 || nt[j] >= a.NB;
-        }
+        for (int j = j0 + (of > 1 ? rank * NT : 0) + tid; j < j1; j += of * NT) bad |= t[j] < 0 || t[j] >= a.NB;
         if (bad) s_bad = 1;
-    }
-    __syncthreads();
-    // The CTAs of a cluster see the same lengths and tables: all leave here or none.
-    if (bad_len || s_bad) {
-        if (rank != 0) return;
+    };
+    auto blocks = [&](int tokens) { return (tokens + a.bs - 1) >> a.shift; };
+    const int32_t* nt = a.new_tables ? a.new_tables + static_cast<size_t>(i) * a.newMB : nullptr;
+    auto skip = [&](uint32_t bit) {
         if (tid == 0) {
-            raise_flag(a.err, bad_len ? PA_ERRBIT_SEQ_TOO_LONG : PA_ERRBIT_BAD_BLOCK);
+            raise_flag(a.err, bit);
             a.rows[row] = EvictRow{L, a.new_tables ? 0 : L, 0, 0};
         }
         for (int j = tid; j < a.budget; j += NT) kept[j] = -1;
+    };
+    // The CTAs of a cluster see the same lengths and tables: where one leaves,
+    // all do, and before the first cluster barrier or behind one.
+    if (bad_len) {
+        if (rank == 0) skip(PA_ERRBIT_SEQ_TOO_LONG);
         return;
     }
     if (L <= a.budget) {
         if (rank != 0) return;
+        check(bt, 0, blocks(L), 1);
+        if (nt) check(nt, 0, blocks(n), 1);
+        __syncthreads();
+        if (s_bad) { skip(PA_ERRBIT_BAD_BLOCK); return; }
         for (int j = tid; j < a.budget; j += NT) kept[j] = j < L ? j : -1;
         if (tid == 0) a.rows[row] = EvictRow{L, L, 0, 1};
         return;
@@ -203,6 +208,9 @@ evict_select_kernel(const __grid_constant__ EvictArgs a) {
     auto cand = [&](int pos) { return pos >= a.sink; };                // and pos < end, as all here are
     uint32_t thr = 0;
     int need = k;                                   // ties with thr that are kept
+    // blocks that the weights below do not pass
+    check(bt, k > 0 ? end >> a.shift : 0, blocks(L), C);
+    if (nt) check(nt, 0, blocks(n), C);
     if (k > 0) {
         // weights by 16 bytes, four in flight: keys, and the first digit's counts
         constexpr int U = 4;
@@ -213,6 +221,7 @@ evict_select_kernel(const __grid_constant__ EvictArgs a) {
             for (int u = 0; u < U; ++u) {
                 const int pos = p0 + u * 4 * NT;
                 blk[u] = pos < hi ? __ldg(bt + (pos >> a.shift)) : 0;
+                if (blk[u] < 0 || blk[u] >= a.NB) { blk[u] = 0; s_bad = 1; }
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -232,12 +241,22 @@ evict_select_kernel(const __grid_constant__ EvictArgs a) {
                     }
             }
         }
-        if (C > 1) cluster_sync();                  // the first CTA's bins are zeroed
+    }
+    sync();                                         // the first CTA's bins are zeroed, every part's blocks checked
+    int total, lower, bad = s_bad;
+    if (C > 1) peer_prefix(&s_bad, rank, C, lower, bad);
+    if (bad) {
+        sync();                                     // every peer has read
+        if (rank == 0) skip(PA_ERRBIT_BAD_BLOCK);
+        return;
+    }
+    if (k > 0) {
 #pragma unroll 1
         for (int d = 0; d < 3; ++d) {
             const int shift = d == 0 ? 21 : d == 1 ? 10 : 0;
             if (d > 0) {
                 const int up = d == 1 ? 21 : 10;    // bits decided so far
+#pragma unroll 4
                 for (int pos = lo + tid; pos < hi; pos += NT) {
                     const uint32_t key = key_at(pos);
                     if (cand(pos) && (key >> up) == (thr >> up))
@@ -260,7 +279,7 @@ evict_select_kernel(const __grid_constant__ EvictArgs a) {
                     cnt[e] = hist[d][EV_BINS - 1 - (tid * PB + e)];
                     mine += cnt[e];
                 }
-                int total, before = block_scan_excl(mine, sums, total);
+                int before = block_scan_excl(mine, sums, total);
                 if (before < need && need <= before + mine) {
 #pragma unroll
                     for (int e = 0; e < PB; ++e) {
@@ -279,8 +298,9 @@ evict_select_kernel(const __grid_constant__ EvictArgs a) {
     }
     for (int j = rank * NT + tid; j < a.budget; j += C * NT) kept[j] = j < heavy ? j : end + (j - heavy);
     const int run = (hi - lo + NT - 1) / NT, r0 = min(hi, lo + tid * run), r1 = min(hi, r0 + run);
-    int total, mine = 0, lower, all;
+    int mine = 0, all;
     if (k > 0)
+#pragma unroll 4
         for (int pos = r0; pos < r1; ++pos) mine += (cand(pos) && key_at(pos) == thr) ? 1 : 0;
     int ties = block_scan_excl(mine, sums, total);
     if (C > 1) {
@@ -292,6 +312,7 @@ evict_select_kernel(const __grid_constant__ EvictArgs a) {
     // one walk over the run: f(position, kept)
     auto walk = [&](auto f) {
         int t = ties;
+#pragma unroll 4
         for (int pos = r0; pos < r1; ++pos) {
             bool keep = pos < a.sink;
             if (!keep && k > 0) {
@@ -500,8 +521,11 @@ extern "C" pa_status pa_evict(void* k_cache, void* v_cache, pa_dtype kv_dtype, f
     const size_t smem = cached ? sizeof(uint32_t) * static_cast<size_t>(part + part / 32 + 1) : 0;
     const void* sel = cached ? reinterpret_cast<const void*>(&evict_select_kernel<true>)
                              : reinterpret_cast<const void*>(&evict_select_kernel<false>);
-    cudaError_t e = cudaFuncSetAttribute(sel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return fail_cuda("evict: set shared memory size", e);
+    cudaError_t e = cudaSuccess;
+    if (smem > 16 * 1024) {                        // with the 24.2 KB that the kernel declares, beyond the default 48
+        e = cudaFuncSetAttribute(sel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (e != cudaSuccess) return fail_cuda("evict: set shared memory size", e);
+    }
     const dim3 grid(static_cast<unsigned>(rows), static_cast<unsigned>(ns),
                     static_cast<unsigned>((budget + a.per_part - 1) / a.per_part));
     if (grid.z > 65535u || rows * C > 0x7fffffffu) return fail(PA_ERR_UNSUPPORTED, "evict: budget or batch too large");
