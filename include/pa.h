@@ -133,10 +133,14 @@ size_t pa_decode_workspace_size(int num_seqs, int num_q_heads, int max_seq_len,
  * on the same stream.
  *   partition_tokens  0 lets the library choose split points; otherwise a
  *                     positive multiple of 16: sequences are additionally
- *                     split every partition_tokens tokens.
+ *                     split every partition_tokens tokens (4-bit caches: that
+ *                     rounded up to a multiple of 32 to 128 tokens).
  * Precision: scores and sums accumulate in fp32.  The probabilities enter
  * P*V rounded to the MMA operand type: bf16 (8 significant bits) for bf16
- * caches, f16 (11 bits) for f16 caches and fp8 caches on 16-token chunks.
+ * caches, f16 (11 bits) for f16 and 4-bit caches and fp8 caches on 16-token
+ * chunks.  With a 4-bit cache a bf16 query is scaled by a power of two into
+ * f16; its elements below 2^-28 of the largest in a group of 8 or 16 rows are
+ * rounded to a multiple of 2^-38 of that.
  * On the fp8 32-token path (e4m3 and e5m2 caches: the key and value bytes
  * are MMA operands as stored) the query and the probabilities are each carried
  * as two e4m3 terms, 8 significant bits (exact for bf16 queries, except
@@ -193,7 +197,7 @@ pa_status pa_decode_simt(void* out, const void* q, pa_dtype q_dtype,
  * pa_decode's output.
  *   fresh             int32 [num_seqs] on the device, or null
  *   workspace         at least pa_decode_weights_workspace_size(...) bytes
- * Other arguments as for pa_decode.
+ * Other arguments as for pa_decode; at most 65535 sequences.
  */
 size_t pa_decode_weights_workspace_size(int num_seqs, int num_q_heads, int max_seq_len,
                                         int head_dim);
@@ -248,7 +252,9 @@ pa_status pa_decode_noalloc(void* out, const void* q, pa_dtype q_dtype,
  * A 4-bit cache quantises each row on write (head of this file) from f32, f16
  * or bf16; it needs head_dim 64 or 128, a block_size of a multiple of 8, and
  * fewer than 2^31 rows (tokens x heads) and pool slots.
- * Duplicate slots within one call leave one of the writes (unspecified which).
+ * Duplicate slots within one call leave one of the writes (unspecified which);
+ * in a 4-bit cache such a row may mix the codes of one with the (step, low) of
+ * another.
  */
 pa_status pa_reshape_and_cache(void* k_cache, void* v_cache, pa_dtype kv_dtype,
                                const void* key, const void* value, pa_dtype src_dtype,

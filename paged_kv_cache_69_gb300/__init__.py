@@ -152,11 +152,18 @@ def _stream(stream) -> ctypes.c_void_p:
 
 
 def _dev(*ts):
+    device = None
     for t in ts:
-        if t is not None and not t.is_cuda:
+        if t is None:
+            continue
+        if not t.is_cuda:
             raise ValueError("libpa works on CUDA tensors only")
-        if t is not None and not t.is_contiguous():
+        if not t.is_contiguous():
             raise ValueError("libpa expects contiguous tensors")
+        if device is None:
+            device = torch.cuda.current_device()     # kernels launch there
+        if t.get_device() != device:
+            raise ValueError("libpa works on tensors of the current device")
 
 
 def _pools(k: torch.Tensor, v: torch.Tensor, kv_dtype=None):

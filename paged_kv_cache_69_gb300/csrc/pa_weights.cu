@@ -80,7 +80,6 @@ weights_kernel(const __grid_constant__ DecodeParams p, float* __restrict__ weigh
 }
 
 pa_status launch_weights(const DecodeParams& p, const WeightsOut& w, cudaStream_t stream) {
-    if (p.B > 65535) return fail(PA_ERR_UNSUPPORTED, "decode_weights: more than 65535 sequences");
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -159,6 +158,7 @@ extern "C" pa_status pa_decode_weights(void* out, float* weights, const void* q,
     clear_error();
     if (num_seqs > 0 && !weights) return fail(PA_ERR_INVALID_ARG, "decode_weights: null pointer");
     if (num_seqs > 0 && !aligned16(weights)) return fail(PA_ERR_INVALID_ARG, "decode_weights: weights must be 16-byte aligned");
+    if (num_seqs > 65535) return fail(PA_ERR_UNSUPPORTED, "decode_weights: more than 65535 sequences");
     WeightsOut w{weights, fresh, nullptr, nullptr, nullptr};
     if (num_seqs > 0 && num_q_heads > 0 && head_dim > 0 && max_blocks_per_seq > 0 && block_size > 0 &&
         static_cast<long long>(max_blocks_per_seq) * block_size < (1LL << 30) && workspace) {

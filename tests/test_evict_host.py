@@ -139,3 +139,30 @@ def test_decode_weights_host_validation(lib, over, status):
 def test_decode_weights_of_no_sequences_is_a_noop(lib):
     a = _decode_args(B=0)
     assert lib.pa_decode_weights(a[0], None, *a[1:9], None, *a[9:18], *a[19:]) == 0
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    class OnDevice:
+        is_cuda = True
+
+        def __init__(self, index):
+            self.index = index
+
+        def is_contiguous(self):
+            return True
+
+        def get_device(self):
+            return self.index
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    pa._dev(OnDevice(1), None, OnDevice(1))
+    for bad in ((OnDevice(0),), (OnDevice(1), OnDevice(0))):
+        with pytest.raises(ValueError):
+            pa._dev(*bad)
+    with pytest.raises(ValueError):
+        pa._dev(torch.zeros(2))
+
+
+def test_decode_weights_refuses_more_sequences_than_its_grid(lib):
+    a = _decode_args(B=65536)
+    assert lib.pa_decode_weights(a[0], 256, *a[1:9], None, *a[9:18], *a[19:]) == 2

@@ -234,3 +234,51 @@ def test_new_tables_too_narrow_or_outside_the_pool():
     c.nt[1, 0] = -1
     c.run()
     assert c.err.item() == pa.ERRBIT_BAD_BLOCK and c.nl.tolist() == [64, 0]
+
+
+def test_two_evictions_at_once_with_a_workspace_each():
+    a = Case([3000, 90], 2, 64, 16, "f16", 200, 2, 30, seed=43, out_of_place=True).on_gpu()
+    b = Case([900] * 6, 4, 128, 16, "int4", 640, 2, 30, seed=44, out_of_place=True).on_gpu()
+    wants = a.want(), b.want()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    ws = [torch.empty(pa.pa_evict_workspace_size(len(c.lens), c.Hkv, c.bt.shape[1] * c.bs, c.budget), dtype=torch.uint8,
+                      device="cuda") for c in (a, b)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for c, s, w in zip((a, b), streams, ws):
+            pa.pa_evict(c.k, c.v, c.wd, c.bt, c.sl, c.nl, c.budget, c.kv, num_sink=c.sink, num_recent=c.recent,
+                        new_block_tables=c.nt, kept=c.kept, workspace=w, stream=s)
+    torch.cuda.synchronize()
+    for c, want in zip((a, b), wants):
+        c.check(want)
+
+
+@pytest.mark.parametrize("D,kv", [(24, "f16"), (80, "bf16"), (256, "f32"), (16, "fp8_e4m3")])
+@pytest.mark.parametrize("out_of_place", [False, True])
+def test_other_head_dims(D, kv, out_of_place):
+    c = Case([150, 90], 3, D, 8, kv, 60, 2, 20, seed=45, out_of_place=out_of_place)
+    c.on_gpu().run().check()
+
+
+def test_pools_of_more_than_four_gigabytes():
+    """Rows whose byte offsets pass 32 bits."""
+    NB, bs, Hkv, D = 70000, 16, 16, 128                # 4.6 GB per pool
+    k = torch.zeros(NB, bs, Hkv, D, dtype=torch.float16, device="cuda")
+    v = torch.zeros_like(k)
+    w = torch.zeros(NB, Hkv, bs, device="cuda")
+    bt = torch.arange(NB - 1, NB - 5, -1, dtype=torch.int32, device="cuda").view(1, 4)
+    pos = torch.arange(64, device="cuda")
+    blk, off = bt[0].long()[pos // bs], pos % bs
+    for h in range(Hkv):
+        k[blk, off, h] = (pos[:, None] + 100 * h).half()
+        v[blk, off, h] = -(pos[:, None] + 100 * h).half()
+        w[blk, h, off] = ((pos * 37 + h) % 64).float()
+    sl = torch.tensor([64], dtype=torch.int32, device="cuda")
+    kept = torch.empty(1, Hkv, 20, dtype=torch.int32, device="cuda")
+    score = [[float((t * 37 + h) % 64) for t in range(64)] for h in range(Hkv)]
+    pa.pa_evict(k, v, w, bt, sl, sl, 20, num_sink=1, num_recent=4, kept=kept)
+    for h in range(Hkv):
+        src = _evict.kept_positions(score[h], 20, 1, 4)
+        assert kept[0, h].tolist() == src
+        for name, sign in ((k, 1), (v, -1)):
+            assert torch.equal(name[blk[:20], off[:20], h, 0], sign * (torch.tensor(src, device="cuda") + 100 * h).half())

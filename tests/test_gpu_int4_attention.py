@@ -295,3 +295,37 @@ def test_bad_query_offsets_skip_the_sequence():
     assert (out[2:8] == 5.0).all()
     rows = [0, 1, 8, 9, 10]
     check(out[rows], want[rows], tol[rows])
+
+
+def test_two_calls_at_once_with_a_workspace_each():
+    a = Case([3000, 100, 700], 28, 4, 128, 16, "f16", seed=30).on_gpu()
+    b = Case([2000, 2001], 8, 2, 128, 32, "bf16", seed=31, counts=[3, 5]).on_gpu()
+    ra, rb = a.run(), b.run()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    wa = pa.alloc_workspace(3, 28, a.bt.shape[1] * 16, 128)
+    wb = torch.empty(pa.pa_attention_workspace_size(2, 5, 8, b.bt.shape[1] * 32, 128, 0), dtype=torch.uint8, device="cuda")
+    oa, ob = torch.zeros_like(ra), torch.zeros_like(rb)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        pa.pa_decode(oa, a.qd, a.k, a.v, a.bt, a.sl, a.scale, "int4", workspace=wa, stream=streams[0])
+        pa.pa_attention(ob, b.qd, b.k, b.v, b.bt, b.sl, b.qs, b.scale, 5, "int4", workspace=wb, stream=streams[1])
+    torch.cuda.synchronize()
+    assert torch.equal(oa, ra) and torch.equal(ob, rb)
+
+
+def test_many_heads_and_a_group_of_nine():
+    """More KV heads than CTAs per range, and groups just over the 8 rows of a warp."""
+    c = Case([40, 300], 256, 256, 64, 8, "f16", seed=32).on_gpu()
+    check(c.run(), *c.want())
+    c = Case([200, 33], 27, 3, 128, 16, "bf16", seed=33).on_gpu()
+    check(c.run(), *c.want())
+
+
+def test_an_infinite_query_element_spoils_only_its_head():
+    c = Case([100, 70], 4, 2, 64, 16, "f16", seed=34)
+    want, tol = c.want()
+    c.q[0, 1, 3] = float("inf")
+    got = c.on_gpu().run()
+    assert not torch.isfinite(got[0, 1]).all()
+    got[0, 1] = torch.from_numpy(want[0, 1]).to(got)
+    check(got, want, tol)
