@@ -23,10 +23,9 @@ constexpr int WT_THREADS = 256;
 constexpr int WT_STEPS = 4;                   // token spans of a CTA, one after another
 
 // NH: heads of a group whose scores are loaded at once.
-// What the decode kernel and those before it wrote is final when this grid
-// starts (the merge, whose start it follows, starts behind the decode
-// kernel's prologue), so lengths, tables and first chunks are read before the
-// wait for the scores and (m, l).
+// What kernels before the decode kernel wrote is final when this grid starts
+// (it follows the merge's start, that the decode kernel's wait), so lengths
+// and tables are read before the wait for this call's own results.
 template <int NH>
 __global__ void __launch_bounds__(WT_THREADS, NH == 4 ? 4 : 3)
 weights_kernel(const __grid_constant__ DecodeParams p, float* __restrict__ weights, const int32_t* __restrict__ fresh,
@@ -40,9 +39,9 @@ weights_kernel(const __grid_constant__ DecodeParams p, float* __restrict__ weigh
     const int32_t* bt = p.block_tables + static_cast<size_t>(i) * p.MB;
     int next = t < maxL ? __ldg(bt + (t >> bs_log2)) : -1;
     const int old_until = L - (fresh ? min(max(fresh[i], 0), L) : 1);
-    const float* scores = score_row(p, __ldcg(p.chunk0 + i), g * p.G);
     grid_dependency_wait();
     if (t0 >= L || g >= p.Hkv) return;
+    const float* scores = score_row(p, p.chunk0[i], g * p.G);
     const float2* lse = p.lse + static_cast<size_t>(i) * p.Hq + g * p.G;
     const size_t chunk = static_cast<size_t>(p.Hq) << ct_log2;
 #pragma unroll 1
