@@ -29,11 +29,24 @@
 //
 // Work split, partials and the merge are the paged decode kernel's: the chunks
 // of all sequences form one stream, cut into ranges of equal cost for
-// persistent CTAs; one warp fills a ring of stages with contiguous bulk copies
-// (a block's codes of the CTA's heads are one span, its parameters another),
-// the other warps each own 8 or 16 query rows of one KV head.  TS such warps
-// share a chunk of 32 TS tokens, 32 each, and join their results in shared
-// memory at the end of a segment.
+// persistent CTAs; one warp fills a ring of stages (a block's codes of the
+// CTA's heads are one span, one bulk copy; its (step, low) pairs go by 16-byte
+// cp.async, as short spans), the other warps each own 8 or 16 query rows of one
+// KV head.  TS such warps share a chunk of 32 TS tokens, 32 each, and join
+// their results in shared memory at the end of a segment.
+//
+// Measured (us, one call, against the bytes alone at the copy rate): the
+// 7B-like batch of 64 (28 heads on 4, f16) 51 (23), the same with 1-4 query
+// tokens 129 (23), 1024 sequences of 20-2048 tokens 64 (26), 8 sequences of
+// 32k-131k tokens 179 (120).  Bound by issue: every key costs its masks, its
+// two numbers and the softmax of 8 rows whatever the rows hold, and 16 rows
+// hold both products' tiles.  The copies alone, the arithmetic left out, take
+// 39, 66, 46 and 134.  What was tried beside this form: two CTAs per SM with 64
+// tokens per warp (171 on the long sequences, but 76 on the short ones, where
+// 32 tokens then took 70); four CTAs of 96 registers (227 on the long ones,
+// spills); separate barriers for keys and values (193); for 8 rows one
+// 16-token tile at a time (190; for 16 rows that form is the faster one, 146
+// against 175 on 1-4 query tokens, the registers holding one tile).
 #include <algorithm>
 #include <cmath>
 #include <cuda.h>
