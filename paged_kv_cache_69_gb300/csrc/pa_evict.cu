@@ -18,9 +18,13 @@
 // CTA counts its part, adds its bins that are not empty to the first CTA's
 // (atomics in distributed shared memory; reading all bins of all CTAs took
 // most of 160 us on 64 rows of 32k to 131k tokens), and that one finds the
-// digit.  A thread then owns a run of consecutive tokens: it ranks its ties,
-// counts the free places below `heavy` and the kept rows behind it, and
-// writes both lists in position order.
+// digit; where a whole bin is kept, the digits behind it are left out.  A
+// thread then owns a run of consecutive tokens: it turns its keys into two masks
+// (above the threshold, tied with it), ranks its ties, counts the free places
+// below `heavy` and the kept rows behind it, and writes both lists in position
+// order.  Those 64 rows to 4096 tokens each: 52 us, bound by the passes over
+// shared memory and the barriers between them (24 MB of weights; three CTAs per
+// SM instead of two 7 us slower, copies of the bins by lane 2 to 17).
 // evict_move_kernel: a CTA moves a slice of a head's rows of one plane (K, V,
 // the 4-bit parameters, the weights).  Slices share no bytes, so the order
 // that an in-place move needs holds inside a CTA.  In place a slice is 64 bytes
@@ -143,9 +147,9 @@ constexpr int EV_MAX_CLUSTER = 8;
 template <bool CACHED>
 __global__ void __launch_bounds__(EV_SEL_THREADS)
 evict_select_kernel(const __grid_constant__ EvictArgs a) {
-    __shared__ int hist[3][EV_BINS];
+    __shared__ int hist[EV_BINS];
     __shared__ int sums[EV_SEL_THREADS / 32];
-    __shared__ int s_bad, s_digit, s_above, s_ties, s_nh, s_nf;
+    __shared__ int s_bad, s_digit, s_above, s_count, s_ties, s_nh, s_nf;
     extern __shared__ uint32_t s_keys[];
     constexpr int NT = EV_SEL_THREADS;
     grid_dependents_launch();
@@ -158,7 +162,7 @@ evict_select_kernel(const __grid_constant__ EvictArgs a) {
     const int L = a.lens[i];
     const int n = min(L, a.budget);
     if (tid == 0) s_bad = 0;
-    for (int x = tid; x < 3 * EV_BINS; x += NT) (&hist[0][0])[x] = 0;
+    for (int x = tid; x < EV_BINS; x += NT) hist[x] = 0;
     __syncthreads();
     bool bad_len = L < 0 || static_cast<long long>(L) > static_cast<long long>(a.MB) * a.bs;
     if (a.new_tables) bad_len = bad_len || static_cast<long long>(n) > static_cast<long long>(a.newMB) * a.bs;
@@ -205,7 +209,7 @@ evict_select_kernel(const __grid_constant__ EvictArgs a) {
         if constexpr (CACHED) return s_keys[slot_of(pos - lo)];
         return weight_key(wg[static_cast<size_t>(bt[pos >> a.shift]) * wstride + (pos & (a.bs - 1))]);
     };
-    auto cand = [&](int pos) { return pos >= a.sink; };                // and pos < end, as all here are
+    const int first = max(lo, a.sink);              // candidates: [first, hi)
     uint32_t thr = 0;
     int need = k;                                   // ties with thr that are kept
     // blocks that the weights below do not pass
@@ -237,7 +241,7 @@ evict_select_kernel(const __grid_constant__ EvictArgs a) {
                     if (pos + e < hi) {
                         const uint32_t key = weight_key(v[e]);
                         if constexpr (CACHED) s_keys[slot_of(pos + e - lo)] = key;
-                        if (cand(pos + e)) atomicAdd(&hist[0][key >> 21], 1);
+                        if (pos + e >= first) atomicAdd(&hist[key >> 21], 1);
                     }
             }
         }
@@ -257,17 +261,19 @@ evict_select_kernel(const __grid_constant__ EvictArgs a) {
             if (d > 0) {
                 const int up = d == 1 ? 21 : 10;    // bits decided so far
 #pragma unroll 4
-                for (int pos = lo + tid; pos < hi; pos += NT) {
+                for (int pos = first + tid; pos < hi; pos += NT) {
                     const uint32_t key = key_at(pos);
-                    if (cand(pos) && (key >> up) == (thr >> up))
-                        atomicAdd(&hist[d][(key >> shift) & (d == 1 ? 2047u : 1023u)], 1);
+                    if ((key >> up) == (thr >> up)) atomicAdd(&hist[(key >> shift) & (d == 1 ? 2047u : 1023u)], 1);
                 }
             }
             if (C > 1) {
                 __syncthreads();
                 if (rank > 0)
                     for (int x = tid; x < EV_BINS; x += NT)
-                        if (const int v = hist[d][x]) peer_add(&hist[d][x], v, 0);
+                        if (const int v = hist[x]) {
+                            peer_add(&hist[x], v, 0);
+                            hist[x] = 0;
+                        }
             }
             sync();
             if (rank == 0) {
@@ -276,7 +282,8 @@ evict_select_kernel(const __grid_constant__ EvictArgs a) {
                 int cnt[PB], mine = 0;
 #pragma unroll
                 for (int e = 0; e < PB; ++e) {
-                    cnt[e] = hist[d][EV_BINS - 1 - (tid * PB + e)];
+                    cnt[e] = hist[EV_BINS - 1 - (tid * PB + e)];
+                    hist[EV_BINS - 1 - (tid * PB + e)] = 0;         // for the next digit
                     mine += cnt[e];
                 }
                 int before = block_scan_excl(mine, sums, total);
@@ -286,6 +293,7 @@ evict_select_kernel(const __grid_constant__ EvictArgs a) {
                         if (before < need && need <= before + cnt[e]) {
                             s_digit = EV_BINS - 1 - (tid * PB + e);
                             s_above = before;
+                            s_count = cnt[e];
                         }
                         before += cnt[e];
                     }
@@ -294,14 +302,49 @@ evict_select_kernel(const __grid_constant__ EvictArgs a) {
             sync();
             thr |= static_cast<uint32_t>(C > 1 ? peer_int(&s_digit, 0) : s_digit) << shift;
             need -= C > 1 ? peer_int(&s_above, 0) : s_above;
+            // the whole bin is kept: the other digits decide nothing
+            if (need == (C > 1 ? peer_int(&s_count, 0) : s_count) && d < 2 && thr > 0) {
+                --thr;
+                need = 0;
+                break;
+            }
         }
     }
     for (int j = rank * NT + tid; j < a.budget; j += C * NT) kept[j] = j < heavy ? j : end + (j - heavy);
     const int run = (hi - lo + NT - 1) / NT, r0 = min(hi, lo + tid * run), r1 = min(hi, r0 + run);
     int mine = 0, all;
-    if (k > 0)
+    // One pass over a thread's run: which keys pass the threshold and which
+    // tie with it, a bit each (a run has at most EV_CACHE / NT of them); without
+    // the keys at hand, the ties are counted here and the rest is walked below.
+    static_assert(EV_CACHE / NT <= 64, "a run's bits");
+    uint64_t above = 0, tie = 0;
+    auto bits = [](int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; };
+    const uint64_t in_run = bits(r1 - r0);
+    if constexpr (CACHED) {
+        if (k > 0) {
+            uint32_t gt[2] = {0, 0}, eq[2] = {0, 0};
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                const int from = r0 + 32 * w, n = min(32, r1 - from);
+                uint32_t bit = 1;
 #pragma unroll 4
-        for (int pos = r0; pos < r1; ++pos) mine += (cand(pos) && key_at(pos) == thr) ? 1 : 0;
+                for (int x = 0; x < n; ++x, bit += bit) {
+                    const uint32_t key = key_at(from + x);
+                    if (key > thr) gt[w] |= bit;
+                    if (key == thr) eq[w] |= bit;
+                }
+            }
+            above = static_cast<uint64_t>(gt[1]) << 32 | gt[0];
+            tie = static_cast<uint64_t>(eq[1]) << 32 | eq[0];
+        }
+        const uint64_t sinks = bits(a.sink - r0) & in_run;
+        above |= sinks;
+        tie &= ~sinks;
+        mine = __popcll(tie);
+    } else if (k > 0) {
+#pragma unroll 4
+        for (int pos = max(r0, a.sink); pos < r1; ++pos) mine += key_at(pos) == thr ? 1 : 0;
+    }
     int ties = block_scan_excl(mine, sums, total);
     if (C > 1) {
         if (tid == 0) s_ties = total;
@@ -324,10 +367,21 @@ evict_select_kernel(const __grid_constant__ EvictArgs a) {
         }
     };
     int h = 0, f = 0;
-    walk([&](int pos, bool keep) {
-        h += (pos < heavy && !keep) ? 1 : 0;
-        f += (pos >= heavy && keep) ? 1 : 0;
-    });
+    uint64_t hole = 0, fill = 0;
+    if constexpr (CACHED) {
+        uint64_t kept_ties = tie;
+        for (int drop = mine - max(need - ties, 0); drop > 0; --drop) kept_ties &= ~(1ull << (63 - __clzll(kept_ties)));
+        const uint64_t keep = above | kept_ties, below = bits(heavy - r0);
+        hole = in_run & below & ~keep;
+        fill = keep & ~below;
+        h = __popcll(hole);
+        f = __popcll(fill);
+    } else {
+        walk([&](int pos, bool keep) {
+            h += (pos < heavy && !keep) ? 1 : 0;
+            f += (pos >= heavy && keep) ? 1 : 0;
+        });
+    }
     int h0, f0, nf;
     if constexpr (CACHED) {                        // counts of at most EV_CACHE: both in one scan
         const int at = block_scan_excl(h | (f << 16), sums, total);
@@ -346,10 +400,15 @@ evict_select_kernel(const __grid_constant__ EvictArgs a) {
         f0 += lower;
         nf = all;
     }
-    walk([&](int pos, bool keep) {
-        if (pos < heavy && !keep) holes[h0++] = pos;
-        if (pos >= heavy && keep) fills[f0++] = pos;
-    });
+    if constexpr (CACHED) {
+        for (; hole; hole &= hole - 1) holes[h0++] = r0 + __ffsll(hole) - 1;
+        for (; fill; fill &= fill - 1) fills[f0++] = r0 + __ffsll(fill) - 1;
+    } else {
+        walk([&](int pos, bool keep) {
+            if (pos < heavy && !keep) holes[h0++] = pos;
+            if (pos >= heavy && keep) fills[f0++] = pos;
+        });
+    }
     __threadfence();
     sync();                                        // every list entry written, every peer's counts read
     for (int r = rank * NT + tid; r < nf; r += C * NT) kept[__ldcg(holes + r)] = __ldcg(fills + r);
@@ -522,7 +581,7 @@ extern "C" pa_status pa_evict(void* k_cache, void* v_cache, pa_dtype kv_dtype, f
     const void* sel = cached ? reinterpret_cast<const void*>(&evict_select_kernel<true>)
                              : reinterpret_cast<const void*>(&evict_select_kernel<false>);
     cudaError_t e = cudaSuccess;
-    if (smem > 16 * 1024) {                        // with the 24.2 KB that the kernel declares, beyond the default 48
+    if (smem > 16 * 1024) {                        // beyond the default of 48 KB with what the kernel declares
         e = cudaFuncSetAttribute(sel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
         if (e != cudaSuccess) return fail_cuda("evict: set shared memory size", e);
     }
