@@ -135,6 +135,14 @@ def test_tables_for_more_tokens_than_any_sequence_has(weights, width):
     assert c.err.item() == 0
 
 
+@pytest.mark.parametrize("weights", ["heavy", "ties", "equal"])
+@pytest.mark.parametrize("budget,out_of_place", [(5000, False), (150007, False), (5000, True)])
+def test_long_runs_of_one_thread(weights, budget, out_of_place):
+    """47 keys of one thread, the sinks and the place where the recent rows go inside such a run."""
+    c = Case([190001], 1, 16, 32, "f16", budget, 40, 1003, seed=46, weights=weights, out_of_place=out_of_place)
+    c.on_gpu().run().check()
+
+
 def test_one_row_over_a_whole_cluster():
     c = Case([30000], 1, 64, 32, "f16", 29000, 7, 3000, seed=42, weights="ties")
     c.on_gpu().run().check()
