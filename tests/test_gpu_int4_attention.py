@@ -329,3 +329,15 @@ def test_an_infinite_query_element_spoils_only_its_head():
     assert not torch.isfinite(got[0, 1]).all()
     got[0, 1] = torch.from_numpy(want[0, 1]).to(got)
     check(got, want, tol)
+
+
+@pytest.mark.parametrize("wide", [1, 40])
+@pytest.mark.parametrize("lens", [[1], [5000, 12000, 17001], [129, 0, 260, 1], [39000]])
+def test_fewer_chunks_than_ranges(lens, wide):
+    """Few long sequences of one KV head, also under tables for many more tokens."""
+    c = Case(lens, 7, 1, 128, 32, "f16", seed=35)
+    if wide > 1:
+        t = np.full((len(lens), c.tables.shape[1] * wide), -1, np.int32)
+        t[:, :c.tables.shape[1]] = c.tables
+        c.tables = t
+    check(c.on_gpu().run(), *c.want())
