@@ -38,7 +38,7 @@
 // Measured (us, one call, against the bytes alone at the copy rate): the
 // 7B-like batch of 64 (28 heads on 4, f16) 51 (23), the same with 1-4 query
 // tokens 129 (23), 1024 sequences of 20-2048 tokens 64 (26), 8 sequences of
-// 32k-131k tokens 179 (120).  Bound by issue: every key costs its masks, its
+// 32k-131k tokens 181 (120).  Bound by issue: every key costs its masks, its
 // two numbers and the softmax of 8 rows whatever the rows hold, and 16 rows
 // hold both products' tiles.  The copies alone, the arithmetic left out, take
 // 39, 66, 46 and 134.  What was tried beside this form: two CTAs per SM with 64
@@ -880,9 +880,15 @@ __device__ __forceinline__ void int4_consumer(const Int4Params& a, const Plan& p
     }
 }
 
-// Ranges that hold a chunk each.  With fewer chunks than ranges some would be
-// empty, and the merge would look for a sequence's partials range by range: 123
-// of the 134 us of a call on three sequences of 5k to 23k tokens and one KV head.
+// How many ranges a call without partitions is cut into.  With fewer chunks
+// than ranges some would be empty, and the merge would look for a sequence's
+// partials range by range: 123 of the 134 us of a call on three sequences of 5k
+// to 23k tokens and one KV head.  And a chunk costs a CTA about 0.7 us, a
+// partial the merge about 0.11: a sequence of n chunks in k ranges, 0.7 n / k +
+// 0.11 k, is best off with k = sqrt(6 n) of them, so few sequences take
+// sequences * sqrt(6 chunks per sequence) ranges where the GPU has more.  One
+// sequence of 9000 tokens, 8 heads: 25 us (48 with a range per chunk); those
+// three: 23 (39); one of 131072, one KV head 39 (60), 8 heads 76 (74).
 __device__ __forceinline__ int int4_ranges(const DecodeParams& p, int2* scratch) {
     int c = 0;
     for (int i = threadIdx.x; i < p.B; i += blockDim.x) c += cdiv_i(clamp_len(p.seq_lens[i], p.MB * p.bs), p.ct);
@@ -892,7 +898,8 @@ __device__ __forceinline__ int int4_ranges(const DecodeParams& p, int2* scratch)
     c = 0;
     for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) c += scratch[w].x;
     __syncthreads();                           // the plan writes there
-    return min(p.NR, max(1, c));
+    const int even = static_cast<int>(sqrtf(6.f * static_cast<float>(c) * static_cast<float>(p.B)));
+    return min(p.NR, max(1, min(c, even)));
 }
 
 // MAXW: consumer warps at most, CTAS: CTAs per SM that the registers are
