@@ -137,8 +137,10 @@ size_t pa_decode_workspace_size(int num_seqs, int num_q_heads, int max_seq_len,
  *                     rounded up to a multiple of 32 to 128 tokens).
  * Precision: scores and sums accumulate in fp32.  The probabilities enter
  * P*V rounded to the MMA operand type: bf16 (8 significant bits) for bf16
- * caches, f16 (11 bits) for f16 and 4-bit caches and fp8 caches on 16-token
- * chunks.  With a 4-bit cache a bf16 query is scaled by a power of two into
+ * caches, f16 (11 bits) for f16 caches and fp8 caches on 16-token chunks.  With
+ * a 4-bit cache it is the product of a probability and its value row's step that
+ * is rounded, to f16: 11 bits down to 2^-20 of the largest such product of the
+ * query row, fewer below.  There a bf16 query is scaled by a power of two into
  * f16; its elements below 2^-28 of the largest in a group of 8 or 16 rows are
  * rounded to a multiple of 2^-38 of that.
  * On the fp8 32-token path (e4m3 and e5m2 caches: the key and value bytes

@@ -67,6 +67,10 @@ constexpr int i4_tiles(int nqt) { return nqt == 1 ? 2 : 1; }
 constexpr int i4_ctas(int nqt) { return nqt == 1 ? 3 : 2; }
 constexpr int I4_MAX_STAGES = 8;
 constexpr int I4_NQ = 2;                    // query ring slots
+// log2 of how far above a row's reference its largest product may lie, and of
+// where it lies when the reference has just moved: below 2^15, within f16, and
+// few moves (8 apart, as of a softmax's reference)
+constexpr float I4_ROOM = 14.f, I4_LIFT = 6.f;
 
 struct I4Head {
     int tok0, slot, qrow0, qpos0, qn, qslot;
@@ -366,6 +370,13 @@ __device__ __forceinline__ float sum_g4(float x) {
     return x + __shfl_xor_sync(0xffffffffu, x, 16);
 }
 
+// The exponent of a row's step, whole: that of the smallest f16 for a step of
+// 0 (its row still weighs by its low), and of the largest for what is none.
+__device__ __forceinline__ float step_log2(float step) {
+    const int e = static_cast<int>((__float_as_uint(step) >> 23) & 255u) - 127;
+    return static_cast<float>(min(max(e, -24), 15));
+}
+
 template <typename T>
 __device__ __forceinline__ uint32_t pack_out(float a, float b) {
     return pack2(a, b, std::is_same<T, __nv_bfloat16>::value);
@@ -373,10 +384,17 @@ __device__ __forceinline__ uint32_t pack_out(float a, float b) {
 
 // ---------------------------------------------------------------------------
 // consumer: warp w owns NQT tiles of 8 query rows of one KV head.
-// The weights enter the second product rounded to f16 (11 bits), whatever the
-// output's type: each rounding meets a (c - 8) step, a value about its row's
-// middle, so the output's error is that of rounding p itself.  WT:
-// pa_decode_weights, the scores and (m, l) are kept.
+// The products p step enter the second product rounded to f16 (11 bits),
+// whatever the output's type: each rounding meets a c - 8, so the output's
+// error is that of rounding p itself while the product is a normal f16.  The
+// exponent's reference m is therefore one of the products, not of the scores:
+// a row's largest s + log2(step) lies within [m + 6, m + 14], its largest
+// product within [2^6, 2^15), and those down to 2^-20 to 2^-29 of it keep all
+// 11 bits.  (References of scores and steps apart let one row with a large step
+// and no weight push the others' products into subnormals: outputs of order one
+// over 32768 keys were off by 0.07 to 0.17 with a step 8000 times the others'.
+// Neither form is faster.)  Weights alone are then at most 2^38 and summed in
+// f32.  WT: pa_decode_weights, the scores and (m, l) are kept.
 // ---------------------------------------------------------------------------
 template <class QT, int D, int NQT, bool WT>
 __device__ __forceinline__ void int4_consumer(const Int4Params& a, const Plan& pl, int hg, int w, uint8_t* base,
@@ -423,9 +441,8 @@ __device__ __forceinline__ void int4_consumer(const Int4Params& a, const Plan& p
     // The warp's query operand, [tile][word][lane] 16 bytes, kept in shared
     // memory: the registers it would take buy another CTA per SM.
     const uint32_t qf = base32 + a.frag_off + static_cast<uint32_t>(w * NQT * KW * 512) + lane * 16u;
-    // rows 2 t4 and 2 t4 + 1 of each tile: reference of the exponent (a row's
-    // largest score within 2^8, 0 while it has none), sum of the weights, sum
-    // of weight * (low + 8 step); the last two over the lane's tokens
+    // rows 2 t4 and 2 t4 + 1 of each tile: reference of the exponent, sum of the
+    // weights, sum of weight * (low + 8 step); the last two over the lane's tokens
     float m[NQT][2], l[NQT][2], c0[NQT][2];
     float sq[NQT][2];                             // sum of the query row, times the score scale
     float unit_qk = 0.f;                          // score of one unit of the codes' dot product
@@ -437,7 +454,6 @@ __device__ __forceinline__ void int4_consumer(const Int4Params& a, const Plan& p
         while ((1 << ct_log2) < p.ct) ++ct_log2;
         sdst = score_row(p, pl.cs, (hg * p.HPC + hl) * p.G + rt * NQT * 8 + 2 * t4) + I4_WT * ts + tk;
     }
-    float inv = 0.f, step_top = 0.f;              // power of two on step in the weights (0: not set yet); 2^7 over it
     int in_rows = 0, joins = 0;
 #pragma unroll
     for (int n = 0; n < NQT; ++n)
@@ -539,7 +555,6 @@ __device__ __forceinline__ void int4_consumer(const Int4Params& a, const Plan& p
                     if (p.q_start) lim[n][e] = ((in_rows >> (2 * n + e)) & 1) && jt[n][e] < d.qn ? d.qpos0 + jt[n][e] : -1;
                 }
             }
-            inv = step_top = 0.f;
         }
 #pragma unroll 1
         for (int sub = 0; sub < SUBS; ++sub) {
@@ -635,7 +650,6 @@ __device__ __forceinline__ void int4_consumer(const Int4Params& a, const Plan& p
             }
             // ---- V parameters: step and low + 8 step of the lane's two tokens of each tile ----
             float vs[MT][2], vl[MT][2];
-            float smax = 0.f;
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -650,45 +664,47 @@ __device__ __forceinline__ void int4_consumer(const Int4Params& a, const Plan& p
                     for (int e = 0; e < 2; ++e)
                         if (!((vm >> (16 * mt + 8 * e + tk)) & 1u)) vs[mt][e] = vl[mt][e] = 0.f;
             }
+            // ---- online softmax (log2 domain) ----
+            // The reference of a row moves only when a product may pass it by 2^14
+            // (the lane's largest score and largest step, of different tokens at
+            // worst, say when to look): a chunk mostly needs no exchange between
+            // lanes but one vote.
+            float smax = 0.f;
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) smax = fmaxf(smax, fmaxf(fabsf(vs[mt][0]), fabsf(vs[mt][1])));
-            // ---- online softmax (log2 domain) ----
-            // The reference of a row moves only when a score passes it by more than
-            // 2^8, and the power of two on the steps only when a step passes 2^7
-            // with it: weights then stay below 2^15, within f16, and a chunk mostly
-            // needs no exchange between lanes but one vote.
-            float mx[NQT][2];
-            bool far = smax > step_top;
+            const float top = I4_ROOM - step_log2(smax);
+            bool far = false;
 #pragma unroll
             for (int n = 0; n < NQT; ++n)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    mx[n][e] = -INFINITY;
+                    float mx = -INFINITY;
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) mx[n][e] = fmaxf(mx[n][e], fmaxf(s[mt][n][e], s[mt][n][e + 2]));
-                    far = far || mx[n][e] > m[n][e] + 8.f;
+                    for (int mt = 0; mt < MT; ++mt) mx = fmaxf(mx, fmaxf(s[mt][n][e], s[mt][n][e + 2]));
+                    far = far || mx > m[n][e] + top;
                 }
             if (__any_sync(0xffffffffu, far)) {
-                smax = max_g4(smax);
-                float grow = 1.f;
-                if (smax > step_top) {
-                    const int ex = static_cast<int>(__float_as_uint(smax) >> 23) - 127;
-                    const float ni = __uint_as_float(static_cast<uint32_t>(1 - ex + 127) << 23);   // steps into [2, 4)
-                    if (inv != 0.f) grow = ni / inv;
-                    inv = ni;
-                    step_top = 128.f / ni;
-                }
+                float ls[MT][2];
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) ls[mt][e] = step_log2(vs[mt][e]);
 #pragma unroll
                 for (int n = 0; n < NQT; ++n) {
                     float f[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float mn = fmaxf(m[n][e], max_g4(mx[n][e]));
-                        const float al = m[n][e] == mn ? 1.f : ex2_approx(m[n][e] - mn);
-                        m[n][e] = mn;
-                        l[n][e] *= al;
-                        c0[n][e] *= al;
-                        f[e] = al * grow;
+                        float t = -INFINITY;
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt) t = fmaxf(t, fmaxf(s[mt][n][e] + ls[mt][0], s[mt][n][e + 2] + ls[mt][1]));
+                        t = max_g4(t);
+                        f[e] = 1.f;
+                        if (t > m[n][e] + I4_ROOM) {
+                            f[e] = ex2_approx(m[n][e] - (t - I4_LIFT));
+                            m[n][e] = t - I4_LIFT;
+                            l[n][e] *= f[e];
+                            c0[n][e] *= f[e];
+                        }
                     }
 #pragma unroll
                     for (int o = 0; o < OT; ++o) {
@@ -713,7 +729,7 @@ __device__ __forceinline__ void int4_consumer(const Int4Params& a, const Plan& p
                 }
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-                const float w0 = vs[mt][0] * inv, w1 = vs[mt][1] * inv;
+                const float w0 = vs[mt][0], w1 = vs[mt][1];
 #pragma unroll
                 for (int n = 0; n < NQT; ++n) {
                     const float x0 = s[mt][n][0] * w0, x1 = s[mt][n][1] * w0, x2 = s[mt][n][2] * w1, x3 = s[mt][n][3] * w1;
@@ -785,7 +801,6 @@ __device__ __forceinline__ void int4_consumer(const Int4Params& a, const Plan& p
         if (lane == 0) mbar_arrive(&empty[slot]);
         if (d.flags & SEG_END) {
             const bool direct = (d.flags & DIRECT) != 0;
-            const float back = inv > 0.f ? UNIT / inv : 0.f;
             // warps ts > 0 hand (m, l, values) of their tokens to warp ts = 0
             constexpr int JF = D / 8 + 2;                 // floats per lane, tile and row of the pair
             float* jb = reinterpret_cast<float*>(base + a.join_off) + static_cast<size_t>(tile * (a.TS - 1)) * NQT * 2 * JF * 32 + lane;
@@ -813,7 +828,8 @@ __device__ __forceinline__ void int4_consumer(const Int4Params& a, const Plan& p
                     float v[D / 8];
 #pragma unroll
                     for (int o = 0; o < OT; ++o) {
-                        const float u = (o & 1) ? back * 0.0625f : back;
+                        constexpr float LOW = UNIT, HIGH = UNIT * 0.0625f;
+                        const float u = (o & 1) ? HIGH : LOW;
                         v[o] = fmaf(acc[o][n][e], u, ct);
                         v[OT + o] = fmaf(acc[o][n][2 + e], u, ct);
                     }
