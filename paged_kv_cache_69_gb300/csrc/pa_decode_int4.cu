@@ -671,9 +671,9 @@ __device__ __forceinline__ void int4_consumer(const Int4Params& a, const Plan& p
             // lanes but one vote.
             float smax = 0.f;
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) smax = fmaxf(smax, fmaxf(fabsf(vs[mt][0]), fabsf(vs[mt][1])));
+            for (int mt = 0; mt < MT; ++mt) smax = max_nan(smax, max_nan(fabsf(vs[mt][0]), fabsf(vs[mt][1])));
             const float top = I4_ROOM - step_log2(smax);
-            bool far = false;
+            bool far = smax != smax;                  // a row of NaN
 #pragma unroll
             for (int n = 0; n < NQT; ++n)
 #pragma unroll
@@ -688,7 +688,19 @@ __device__ __forceinline__ void int4_consumer(const Int4Params& a, const Plan& p
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) ls[mt][e] = step_log2(vs[mt][e]);
+                    for (int e = 0; e < 2; ++e) {
+                        if (vs[mt][e] != vs[mt][e]) {
+                            // a row of NaN spoils the query rows that attend it, and
+                            // no other: its products with a weight of 0 would
+#pragma unroll
+                            for (int n = 0; n < NQT; ++n)
+#pragma unroll
+                                for (int x = 0; x < 2; ++x)
+                                    if (s[mt][n][2 * e + x] != -INFINITY) c0[n][x] = __int_as_float(0x7fffffff);
+                            vs[mt][e] = vl[mt][e] = 0.f;
+                        }
+                        ls[mt][e] = step_log2(vs[mt][e]);
+                    }
 #pragma unroll
                 for (int n = 0; n < NQT; ++n) {
                     float f[2];
