@@ -34,6 +34,10 @@ pa_status fail_cuda(const char* what, cudaError_t e) {
     return PA_ERR_CUDA;
 }
 
+cudaError_t allow_shared(const void* kernel, int bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
 // ---------------------------------------------------------------------------
 // device facts (cached per device)
 // ---------------------------------------------------------------------------
@@ -443,7 +447,7 @@ static pa_status decode_impl(bool tc, void* out, const void* q, pa_dtype q_dtype
     }
 
     // grid: persistent CTAs, as many as fit, split into ranges x head groups
-    ce = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    ce = allow_shared(kern, dev.max_smem);   // all that a CTA may have: the kernel has no static shared memory
     if (ce != cudaSuccess) return fail_cuda("decode: set shared memory size", ce);
     int per_sm = 0;
     ce = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem);

@@ -23,6 +23,10 @@ inline int dtype_bytes(pa_dtype d) { return d == PA_F32 ? 4 : (is_fp8(d) ? 1 : 2
 // bytes of one token's K (or V) row of one head in a pool: 4-bit codes and
 // their (step, low) pair, or the elements
 inline int row_bytes(pa_dtype d, int head_dim) { return is_int4(d) ? head_dim / 2 + 4 : head_dim * dtype_bytes(d); }
+// The limit on a kernel's dynamic shared memory belongs to the kernel, not to a
+// launch: every call sets the same value, so that calls of other host threads
+// between this one and its launch change nothing.
+cudaError_t allow_shared(const void* kernel, int bytes);
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool isfinite_host(float x) { return std::isfinite(x); }
 

@@ -1059,7 +1059,7 @@ pa_status decode_int4(const Int4Call& c) {
     const void* kern = c.weights ? (h ? int4_fn<F16T, true>(D, nqt, NCW) : int4_fn<BF16T, true>(D, nqt, NCW))
                                  : (h ? int4_fn<F16T, false>(D, nqt, NCW) : int4_fn<BF16T, false>(D, nqt, NCW));
     if (c.weights) { p.scores = c.weights->scores; p.lse = c.weights->lse; p.chunk0 = c.weights->chunk0; }
-    cudaError_t ce = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    cudaError_t ce = allow_shared(kern, c.max_smem);
     if (ce != cudaSuccess) return fail_cuda("decode: set shared memory size", ce);
     int per_sm = 0;
     ce = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem);

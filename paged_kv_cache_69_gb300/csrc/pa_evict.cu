@@ -581,8 +581,8 @@ extern "C" pa_status pa_evict(void* k_cache, void* v_cache, pa_dtype kv_dtype, f
     const void* sel = cached ? reinterpret_cast<const void*>(&evict_select_kernel<true>)
                              : reinterpret_cast<const void*>(&evict_select_kernel<false>);
     cudaError_t e = cudaSuccess;
-    if (smem > 16 * 1024) {                        // beyond the default of 48 KB with what the kernel declares
-        e = cudaFuncSetAttribute(sel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (cached) {
+        e = allow_shared(sel, static_cast<int>(sizeof(uint32_t) * (EV_CACHE + EV_CACHE / 32 + 1)));
         if (e != cudaSuccess) return fail_cuda("evict: set shared memory size", e);
     }
     const dim3 grid(static_cast<unsigned>(rows), static_cast<unsigned>(ns),
