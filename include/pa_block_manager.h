@@ -90,12 +90,15 @@ pa_bm_status pa_bm_append_slots(pa_bm* m, int32_t n, const int64_t* reqs, int64_
 
 /* Register the hash of logical block j of a request once it is full (a
  * block filled by decode appends).  A block that already has a hash keeps
- * it. */
+ * it.  PA_BM_BAD_REQUEST for a request that pa_bm_shrink has cut, and for its
+ * forks: block j no longer holds the tokens from j * block_size on.  Blocks that
+ * pa_evict has filled as new ones must not be given a hash either. */
 pa_bm_status pa_bm_cache_block(pa_bm* m, int64_t req, int32_t j, const uint8_t* hash);
 
 /* Cut a complete request down to its first num_tokens places, for pa_evict in
  * place: the blocks behind them are released, last block first, and every
- * block it keeps loses its prefix-cache hash, since pa_evict rewrites them.
+ * block it keeps loses its prefix-cache hash, since pa_evict rewrites them, and
+ * takes none again.
  * A request that is no longer than num_tokens is left as it is.  Call it
  * before pa_evict is enqueued, with the block table taken before this call:
  * later writes into the released blocks follow it on the stream.

@@ -168,6 +168,7 @@ class Request:
         self.hashes: List[bytes] = []       # hashes of its full prompt blocks
         self.host: Dict[int, int] = {}      # swapped out: table entry -> host block
         self.swapped = False
+        self.rewritten = False              # cut down: entry j no longer holds tokens j*bs ..
 
 
 class BlockManager:
@@ -233,6 +234,7 @@ class BlockManager:
         c.blocks = list(p.blocks)
         c.num_tokens = p.num_tokens
         c.need = p.need
+        c.rewritten = p.rewritten
         for b in c.blocks:
             b.ref_cnt += 1
         self.reqs[child] = c
@@ -264,6 +266,8 @@ class BlockManager:
         return r.blocks[j].block_id * bs + off, pair
 
     def cache_block(self, req_id: int, j: int, h: bytes) -> None:
+        if self.reqs[req_id].rewritten:
+            raise RuntimeError("a hash for blocks that an eviction has rewritten")
         self.pool.cache_full_block(self.reqs[req_id].blocks[j], h)
 
     def shrink(self, req_id: int, num_tokens: int) -> None:
@@ -280,6 +284,7 @@ class BlockManager:
         for b in r.blocks:
             self.pool._maybe_evict_cached_block(b)
         r.hashes = []
+        r.rewritten = True
         r.need = -(-num_tokens // self.block_size)
         behind = r.blocks[r.need:]
         r.blocks = r.blocks[:r.need]

@@ -36,6 +36,7 @@ struct Request {
     int64_t num_tokens = 0;
     int32_t need = 0;             // blocks its tokens take
     uint32_t epoch = 0;           // changes whenever an existing table entry changes
+    bool rewritten = false;       // cut by pa_bm_shrink: entry j no longer holds tokens j*bs ..
     bool swapped = false;         // swapped out: host[j] >= 0 names the host block of entry j,
     std::vector<int32_t> host;    // whose GPU entry blocks[j] is then -1
 };
@@ -215,6 +216,7 @@ pa_bm_status pa_bm_fork(pa_bm* m, int64_t parent, int64_t child) {
         c.blocks = p.blocks;
         c.num_tokens = p.num_tokens;
         c.need = p.need;
+        c.rewritten = p.rewritten;
         for (int32_t b : c.blocks) m->ref[b] += 1;
         m->reqs.emplace(child, std::move(c));
     } catch (...) {
@@ -265,7 +267,7 @@ pa_bm_status pa_bm_append_slots(pa_bm* m, int32_t n, const int64_t* reqs, int64_
 pa_bm_status pa_bm_cache_block(pa_bm* m, int64_t req, int32_t j, const uint8_t* hash) {
     if (!m || !hash) return PA_BM_INVALID_ARG;
     auto it = m->reqs.find(req);
-    if (it == m->reqs.end() || it->second.swapped) return PA_BM_BAD_REQUEST;
+    if (it == m->reqs.end() || it->second.swapped || it->second.rewritten) return PA_BM_BAD_REQUEST;
     if (j < 0 || j >= static_cast<int32_t>(it->second.blocks.size())) return PA_BM_INVALID_ARG;
     Hash32 h;
     std::memcpy(h.b, hash, PA_BM_HASH_BYTES);
@@ -289,6 +291,7 @@ pa_bm_status pa_bm_shrink(pa_bm* m, int64_t req, int64_t num_tokens) {
     const size_t keep = static_cast<size_t>((num_tokens + m->bs - 1) / m->bs);
     for (int32_t b : r.blocks) m->evict(b);                    // rewritten: findable no longer
     r.hashes.clear();
+    r.rewritten = true;
     while (r.blocks.size() > keep) {                            // last block first
         m->release(r.blocks.back());
         r.blocks.pop_back();
