@@ -151,6 +151,19 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _scratch(nbytes: int, device, stream) -> torch.Tensor:
+    """The workspace of one call, from the memory of the stream that the call
+    runs on: torch hands it out again only to work behind the call's kernels."""
+    if nbytes == 0:
+        raise PaError(1, "invalid workspace bounds")
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 def _dev(*ts):
     device = None
     for t in ts:
@@ -235,7 +248,7 @@ def pa_decode(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache
     _flag(err_flag)
     MB = block_tables.shape[1]
     if workspace is None:
-        workspace = alloc_workspace(B, Hq, MB * bs, D, partition_tokens, device=q.device)
+        workspace = _scratch(pa_decode_workspace_size(B, Hq, MB * bs, D, partition_tokens), q.device, stream)
     fn = lib().pa_decode_simt if simt else lib().pa_decode
     _check(fn(_ptr(out), _ptr(q), _code(q), _ptr(k_cache), _ptr(v_cache), _code(k_cache, kv_dtype),
               _ptr(block_tables), MB, _ptr(seq_lens), B, Hq, Hkv, D, bs, NB, float(scale),
@@ -388,9 +401,7 @@ def pa_attention(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_ca
     MB = block_tables.shape[1]
     if workspace is None:
         n = pa_attention_workspace_size(B, max_q_len, Hq, MB * bs, D, partition_tokens)
-        if n == 0:
-            raise PaError(1, "invalid workspace bounds")
-        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+        workspace = _scratch(n, q.device, stream)
     _check(lib().pa_attention(_ptr(out), _ptr(q), _code(q), _ptr(k_cache), _ptr(v_cache), _code(k_cache, kv_dtype),
                               _ptr(block_tables), MB, _ptr(seq_lens), _ptr(q_start), B, T, int(max_q_len), Hq, Hkv,
                               D, bs, NB, float(scale), float(k_scale), float(v_scale), int(partition_tokens),
@@ -429,10 +440,7 @@ def pa_decode_weights(out: torch.Tensor, weights: torch.Tensor, q: torch.Tensor,
         raise ValueError("fresh must be int32 [num_seqs]")
     MB = block_tables.shape[1]
     if workspace is None:
-        n = pa_decode_weights_workspace_size(B, Hq, MB * bs, D)
-        if n == 0:
-            raise PaError(1, "invalid workspace bounds")
-        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+        workspace = _scratch(pa_decode_weights_workspace_size(B, Hq, MB * bs, D), q.device, stream)
     _check(lib().pa_decode_weights(_ptr(out), _ptr(weights), _ptr(q), _code(q), _ptr(k_cache), _ptr(v_cache),
                                    _code(k_cache, kv_dtype), _ptr(block_tables), MB, _ptr(seq_lens), _ptr(fresh), B, Hq,
                                    Hkv, D, bs, NB, float(scale), float(k_scale), float(v_scale), _ptr(workspace),
@@ -471,10 +479,7 @@ def pa_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, weights: torch.Tensor
         _tables(new_block_tables, seq_lens, B)
     MB = block_tables.shape[1]
     if workspace is None:
-        n = pa_evict_workspace_size(B, Hkv, MB * bs, int(budget))
-        if n == 0:
-            raise PaError(1, "invalid workspace bounds")
-        workspace = torch.empty(n, dtype=torch.uint8, device=k_cache.device)
+        workspace = _scratch(pa_evict_workspace_size(B, Hkv, MB * bs, int(budget)), k_cache.device, stream)
     _check(lib().pa_evict(_ptr(k_cache), _ptr(v_cache), _code(k_cache, kv_dtype), _ptr(weights), _ptr(block_tables), MB,
                           _ptr(seq_lens), _ptr(new_block_tables),
                           0 if new_block_tables is None else new_block_tables.shape[1], _ptr(new_seq_lens), _ptr(kept),
