@@ -365,7 +365,7 @@ pa_status pa_attention(void* out, const void* q, pa_dtype q_dtype,
  * with a block outside the pool among the blocks it uses
  * (PA_ERRBIT_BAD_BLOCK), is skipped: kept is -1 throughout, its new length is
  * L in place and 0 otherwise.
- * Any cache type; a head's row must be a multiple of 16 bytes.
+ * Any cache type; a head's row must be a multiple of 16 bytes; budget <= 2^30.
  *   workspace         at least pa_evict_workspace_size(...) bytes, 256-byte
  *                     aligned, no initialisation; calls sharing one must not
  *                     overlap on the GPU.

@@ -42,6 +42,9 @@ constexpr int EV_SEL_THREADS = 512;
 constexpr int EV_MOVE_THREADS = 256;
 constexpr int EV_MAX_SLICES = 64;
 constexpr int EV_UNROLL = 4;
+// Tables hold less than 2^30 tokens; a position past the budget by a grid's
+// stride still fits 32 bits.
+constexpr int EV_MAX_BUDGET = 1 << 30;
 
 // A row's place: base + block * block_stride + offset * tok_stride + head * head_stride.
 struct EvictPlane {
@@ -497,7 +500,7 @@ static size_t evict_ws(int B, int Hkv, int budget) {
 using namespace pa;
 
 extern "C" size_t pa_evict_workspace_size(int num_seqs, int num_kv_heads, int max_seq_len, int budget) {
-    if (num_seqs < 0 || num_kv_heads <= 0 || max_seq_len < 0 || budget <= 0) return 0;
+    if (num_seqs < 0 || num_kv_heads <= 0 || max_seq_len < 0 || budget <= 0 || budget > EV_MAX_BUDGET) return 0;
     return std::max<size_t>(256, evict_ws(num_seqs, num_kv_heads, budget));
 }
 
@@ -517,6 +520,7 @@ extern "C" pa_status pa_evict(void* k_cache, void* v_cache, pa_dtype kv_dtype, f
     if (!k_cache || !v_cache || !weights || !block_tables || !seq_lens || !new_seq_lens)
         return fail(PA_ERR_INVALID_ARG, "evict: null pointer");
     if (!valid_cache_dtype(kv_dtype)) return fail(PA_ERR_INVALID_ARG, "evict: unknown dtype");
+    if (budget > EV_MAX_BUDGET) return fail(PA_ERR_UNSUPPORTED, "evict: budget above 2^30");
     if (block_size != 8 && block_size != 16 && block_size != 32 && block_size != 64 && block_size != 128)
         return fail(PA_ERR_UNSUPPORTED, "evict: block_size must be 8, 16, 32, 64 or 128");
     if (is_int4(kv_dtype) && head_dim != 64 && head_dim != 128)
