@@ -252,8 +252,8 @@ pa_status pa_decode_noalloc(void* out, const void* q, pa_dtype q_dtype,
  * nearest even, saturation to +-448; NaN becomes the NaN code.  Sources for
  * an fp8 cache may be f32, f16 or bf16; other caches need src == kv dtype.
  * A 4-bit cache quantises each row on write (head of this file) from f32, f16
- * or bf16; it needs head_dim 64 or 128, a block_size of a multiple of 8, and
- * fewer than 2^31 rows (tokens x heads) and pool slots.
+ * or bf16; it needs head_dim 64 or 128, a block_size of a multiple of 8, blocks
+ * of less than 2 GB, and fewer than 2^31 rows (tokens x heads) and pool slots.
  * Duplicate slots within one call leave one of the writes (unspecified which);
  * in a 4-bit cache such a row may mix the codes of one with the (step, low) of
  * another.
@@ -276,7 +276,7 @@ pa_status pa_reshape_and_cache(void* k_cache, void* v_cache, pa_dtype kv_dtype,
  * caches (code times k_scale or v_scale) and 4-bit caches (low + step * c)
  * give f32, f16 or bf16, computed in f32 and rounded to nearest even.  The
  * same slot may appear more than once.  head_dim 64 or 128; fewer than 2^31
- * rows (tokens x heads) and pool slots.
+ * rows (tokens x heads) and pool slots; 4-bit blocks of less than 2 GB.
  */
 pa_status pa_gather_cache(void* key, void* value, pa_dtype dst_dtype,
                           const void* k_cache, const void* v_cache, pa_dtype kv_dtype,
@@ -365,7 +365,8 @@ pa_status pa_attention(void* out, const void* q, pa_dtype q_dtype,
  * with a block outside the pool among the blocks it uses
  * (PA_ERRBIT_BAD_BLOCK), is skipped: kept is -1 throughout, its new length is
  * L in place and 0 otherwise.
- * Any cache type; a head's row must be a multiple of 16 bytes; budget <= 2^30.
+ * Any cache type; a head's row must be a multiple of 16 bytes, at most 1024, and
+ * a block less than 2 GB; budget <= 2^30.
  *   workspace         at least pa_evict_workspace_size(...) bytes, 256-byte
  *                     aligned, no initialisation; calls sharing one must not
  *                     overlap on the GPU.

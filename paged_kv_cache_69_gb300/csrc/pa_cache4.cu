@@ -243,6 +243,7 @@ pa_status write_int4(void* kc, void* vc, const void* key, const void* value, pa_
     if (D != 64 && D != 128) return fail(PA_ERR_UNSUPPORTED, "reshape_and_cache: a 4-bit cache needs head_dim 64 or 128");
     if (bs % 8 != 0) return fail(PA_ERR_UNSUPPORTED, "reshape_and_cache: a 4-bit cache needs a block_size of a multiple of 8");
     if (!rows_fit(T, Hkv, bs, NB)) return fail(PA_ERR_UNSUPPORTED, "reshape_and_cache: pool or call too large for 32-bit row numbers");
+    if (!block_fits(PA_INT4, Hkv, D, bs)) return fail(PA_ERR_UNSUPPORTED, "reshape_and_cache: a 4-bit block of 2 GB or more");
     const RowArgs a = row_args(slots, T, Hkv, bs, NB, err);
     const dim3 grid = row_grid(a, D / EPL);
 #define PA_W4(ST, DD)                                                                                              \
@@ -298,6 +299,8 @@ extern "C" pa_status pa_gather_cache(void* key, void* value, pa_dtype dst_dtype,
         return fail(PA_ERR_INVALID_ARG, "gather_cache: caches and destinations must be 16-byte aligned");
     if (!rows_fit(num_tokens, num_kv_heads, block_size, num_blocks))
         return fail(PA_ERR_UNSUPPORTED, "gather_cache: pool or call too large for 32-bit row numbers");
+    if (is_int4(kv_dtype) && !block_fits(kv_dtype, num_kv_heads, head_dim, block_size))
+        return fail(PA_ERR_UNSUPPORTED, "gather_cache: a 4-bit block of 2 GB or more");
     if (is_fp8(dst_dtype)) return fail(PA_ERR_UNSUPPORTED, "gather_cache: the destination must be f32, f16 or bf16");
     if (is_fp8(kv_dtype) && (!(k_scale > 0.f) || !(v_scale > 0.f) || !isfinite_host(k_scale) || !isfinite_host(v_scale)))
         return fail(PA_ERR_INVALID_ARG, "gather_cache: fp8 scales must be finite and > 0");

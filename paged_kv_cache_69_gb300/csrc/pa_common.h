@@ -27,6 +27,10 @@ inline int row_bytes(pa_dtype d, int head_dim) { return is_int4(d) ? head_dim / 
 // launch: every call sets the same value, so that calls of other host threads
 // between this one and its launch change nothing.
 cudaError_t allow_shared(const void* kernel, int bytes);
+// Blocks of 2 GB and more: places inside a block are counted in 32 bits.
+inline bool block_fits(pa_dtype d, int num_kv_heads, int head_dim, int block_size) {
+    return static_cast<double>(num_kv_heads) * block_size * row_bytes(d, head_dim) < 2147483648.0;
+}
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool isfinite_host(float x) { return std::isfinite(x); }
 

@@ -525,6 +525,9 @@ extern "C" pa_status pa_evict(void* k_cache, void* v_cache, pa_dtype kv_dtype, f
         return fail(PA_ERR_UNSUPPORTED, "evict: block_size must be 8, 16, 32, 64 or 128");
     if (is_int4(kv_dtype) && head_dim != 64 && head_dim != 128)
         return fail(PA_ERR_UNSUPPORTED, "evict: a 4-bit cache needs head_dim 64 or 128");
+    if (head_dim > 1024 || !block_fits(kv_dtype, num_kv_heads, head_dim, block_size) ||
+        !block_fits(PA_F32, num_kv_heads, 1, block_size))
+        return fail(PA_ERR_UNSUPPORTED, "evict: a row above 1024 elements, or a block of 2 GB or more");
     const int rb = is_int4(kv_dtype) ? head_dim / 2 : head_dim * dtype_bytes(kv_dtype);
     if (rb % 16 != 0 || rb > 1024) return fail(PA_ERR_UNSUPPORTED, "evict: a head's row must be a multiple of 16 bytes, at most 1024");
     if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(weights))
