@@ -51,7 +51,9 @@
  *   c = (x - low) / step rounded to nearest even and limited to 0..15,
  *   and read as low + step * c;
  * x is limited to +-65504 first, a row of equal values has step 0, and a row
- * that holds a NaN reads as NaN throughout.  A block of a K (or V) pool is
+ * that holds a NaN reads as NaN throughout.  f16 outputs (values read back and
+ * attention) are limited to +-65504: step may be rounded up, and the top of a row
+ * that reaches 65504 then lies at up to 65536.  A block of a K (or V) pool is
  * block_size * num_kv_heads * (head_dim / 2 + 4) bytes: codes [num_kv_heads,
  * block_size, head_dim / 2], dimension 2b in the low nibble of byte b, then
  * (step, low) [num_kv_heads, block_size, 2].  k_scale and v_scale are ignored.

@@ -318,6 +318,7 @@ static pa_status decode_impl(bool tc, void* out, const void* q, pa_dtype q_dtype
     p.out = out; p.q = q; p.block_tables = block_tables; p.seq_lens = seq_lens; p.err_flag = err_flag;
     p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.G = G; p.D = D; p.bs = bs; p.NB = NB; p.MB = MB;
     p.out_bytes = eq;
+    p.out_top = INFINITY;
     p.HPC = HPC; p.NHG = NHG; p.MT = MT; p.NCW = NCW;
     p.ct = CT;
     p.PC = partition_tokens / CT;

@@ -179,7 +179,10 @@ gather4_kernel(uint8_t* __restrict__ key, uint8_t* __restrict__ value, const uin
     for (int y = 0; y < 2; ++y) {
         float x[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = int4_value(((y ? w.y : w.x) >> (4 * k)) & 15u, p.y, p.x);
+        for (int k = 0; k < 8; ++k) {
+            x[k] = int4_value(((y ? w.y : w.x) >> (4 * k)) & 15u, p.y, p.x);
+            if constexpr (S::code == PA_F16) x[k] = limit_f16(x[k]);
+        }
         store8<S>(dst + 8 * y * S::bytes, x);
     }
 }

@@ -874,7 +874,10 @@ __device__ __forceinline__ void int4_consumer(const Int4Params& a, const Plan& p
                     if (direct) {
                         const float sc = lt == 0.f ? 0.f : 1.f / lt;
 #pragma unroll
-                        for (int x = 0; x < D / 8; ++x) v[x] *= sc;
+                        for (int x = 0; x < D / 8; ++x) {
+                            v[x] *= sc;
+                            if constexpr (QT::code == PA_F16) v[x] = limit_f16(v[x]);
+                        }
                         uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(p.out) +
                                                             (static_cast<size_t>(d.qrow0 + jt[n][e]) * p.Hq + head) * D + g4 * (D / 8));
 #pragma unroll
@@ -1013,6 +1016,7 @@ pa_status decode_int4(const Int4Call& c) {
     p.out = c.out; p.q = c.q; p.block_tables = c.tables; p.seq_lens = c.lens; p.err_flag = c.err;
     p.B = c.B; p.Hq = c.Hq; p.Hkv = c.Hkv; p.G = G; p.D = D; p.bs = c.bs; p.NB = c.NB; p.MB = c.MB;
     p.out_bytes = 2;
+    p.out_top = c.q_dtype == PA_F16 ? INT4_F16_TOP : INFINITY;
     p.HPC = HPC; p.NHG = c.Hkv / HPC; p.MT = RT; p.NCW = NCW;
     p.ct = CT;
     // partitions are whole chunks

@@ -25,6 +25,10 @@
 namespace pa {
 
 constexpr int INT4_PARAM_BYTES = 4;           // (step, low) of a row
+// The largest value that a f16 output takes.  step may have been rounded up, so
+// that a row which reaches 65504 reads as up to 65536 at its top, which f16
+// would round to infinity.
+constexpr float INT4_F16_TOP = 65504.f;
 
 // Byte offsets of a row's codes and parameters inside its block.
 __device__ __forceinline__ uint32_t int4_code_off(int h, int off, int bs, int D) {
@@ -110,6 +114,8 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
+// x within f16's largest values, NaN as it is.
+__device__ __forceinline__ float limit_f16(float x) { return min_nan(max_nan(x, -INT4_F16_TOP), INT4_F16_TOP); }
 constexpr float INT4_NEAR = 0.5f - 1.52587890625e-5f;      // 1/2 - 2^-16
 
 // The value of a code: step * c is exact in f32, the sum is rounded once.
