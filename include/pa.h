@@ -195,7 +195,8 @@ pa_status pa_decode_simt(void* out, const void* q, pa_dtype q_dtype,
  * owner left.  After a prompt of n tokens pass n once, then null.  weights is
  * f32 [num_blocks, num_kv_heads, block_size]; entries of other slots are left
  * as they were.  Sequences must not share blocks in one call (every holder
- * would add to the same entries); the sums are f32, one addition per call.
+ * would add to the same entries); the sums are f32, one addition per call.  A
+ * head whose scores are all -infinity (output 0) adds nothing.
  * Any cache type of pa_decode; fp8 caches run a kernel that converts K and V
  * to f16, so that the scores keep the query's full precision; the others give
  * pa_decode's output.

@@ -70,11 +70,12 @@ weights_kernel(const __grid_constant__ DecodeParams p, float* __restrict__ weigh
             for (int r = 0; r < NH; ++r)
                 if (r0 + r < p.G) {
                     const float2 ml = lse[r0 + r];
-                    const float inv = 1.f / ml.y;
-                    w[0] = fmaf(ex2_approx(s[r].x - ml.x), inv, w[0]);
-                    w[1] = fmaf(ex2_approx(s[r].y - ml.x), inv, w[1]);
-                    w[2] = fmaf(ex2_approx(s[r].z - ml.x), inv, w[2]);
-                    w[3] = fmaf(ex2_approx(s[r].w - ml.x), inv, w[3]);
+                    // a head whose scores are all -infinity has the output 0, and no weights
+                    const float m = ml.x == -INFINITY ? 0.f : ml.x, inv = ml.y == 0.f ? 0.f : 1.f / ml.y;
+                    w[0] = fmaf(ex2_approx(s[r].x - m), inv, w[0]);
+                    w[1] = fmaf(ex2_approx(s[r].y - m), inv, w[1]);
+                    w[2] = fmaf(ex2_approx(s[r].z - m), inv, w[2]);
+                    w[3] = fmaf(ex2_approx(s[r].w - m), inv, w[3]);
                 }
         }
         float o[4] = {old.x, old.y, old.z, old.w};
