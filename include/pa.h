@@ -196,7 +196,9 @@ pa_status pa_decode_simt(void* out, const void* q, pa_dtype q_dtype,
  * f32 [num_blocks, num_kv_heads, block_size]; entries of other slots are left
  * as they were.  Sequences must not share blocks in one call (every holder
  * would add to the same entries); the sums are f32, one addition per call.  A
- * head whose scores are all -infinity (output 0) adds nothing.
+ * head whose scores are all -infinity (output 0) adds nothing.  Block copies and
+ * swaps of K and V leave the weights behind: a copied or swapped block's go by
+ * the same calls with the weights as K pool and V pool, f32 of head_dim 1.
  * Any cache type of pa_decode; fp8 caches run a kernel that converts K and V
  * to f16, so that the scores keep the query's full precision; the others give
  * pa_decode's output.
