@@ -163,8 +163,9 @@ static pa_status carve_workspace(void* workspace, size_t bytes, int B, int prow,
     return PA_OK;
 }
 
-pa_status launch_merge(const DecodeParams& p, pa_dtype out, bool split_heads, int sms, cudaStream_t stream) {
-    const void* rkern = p.scores ? reduce_kernel_weights(out, p.D) : reduce_kernel(out, p.D, split_heads);
+pa_status launch_merge(const DecodeParams& p, pa_dtype out, bool split_heads, int sms, cudaStream_t stream,
+                       bool limit) {
+    const void* rkern = p.scores ? reduce_kernel_weights(out, p.D, limit) : reduce_kernel(out, p.D, split_heads, limit);
     if (!rkern) return fail(PA_ERR_UNSUPPORTED, "decode: no reduce kernel for this output dtype");
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -318,7 +319,6 @@ static pa_status decode_impl(bool tc, void* out, const void* q, pa_dtype q_dtype
     p.out = out; p.q = q; p.block_tables = block_tables; p.seq_lens = seq_lens; p.err_flag = err_flag;
     p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.G = G; p.D = D; p.bs = bs; p.NB = NB; p.MB = MB;
     p.out_bytes = eq;
-    p.out_top = INFINITY;
     p.HPC = HPC; p.NHG = NHG; p.MT = MT; p.NCW = NCW;
     p.ct = CT;
     p.PC = partition_tokens / CT;

@@ -1016,7 +1016,6 @@ pa_status decode_int4(const Int4Call& c) {
     p.out = c.out; p.q = c.q; p.block_tables = c.tables; p.seq_lens = c.lens; p.err_flag = c.err;
     p.B = c.B; p.Hq = c.Hq; p.Hkv = c.Hkv; p.G = G; p.D = D; p.bs = c.bs; p.NB = c.NB; p.MB = c.MB;
     p.out_bytes = 2;
-    p.out_top = c.q_dtype == PA_F16 ? INT4_F16_TOP : INFINITY;
     p.HPC = HPC; p.NHG = c.Hkv / HPC; p.MT = RT; p.NCW = NCW;
     p.ct = CT;
     // partitions are whole chunks
@@ -1088,7 +1087,7 @@ pa_status decode_int4(const Int4Call& c) {
     void* args[] = {&a};
     ce = cudaLaunchKernelExC(&cfg, kern, args);
     if (ce != cudaSuccess) return fail_cuda("decode: main kernel launch", ce);
-    const pa_status st = launch_merge(p, c.q_dtype, c.partition_tokens > 0, c.sms, c.stream);
+    const pa_status st = launch_merge(p, c.q_dtype, c.partition_tokens > 0, c.sms, c.stream, true);
     return st == PA_OK && c.weights ? launch_weights(p, *c.weights, c.stream) : st;
 }
 

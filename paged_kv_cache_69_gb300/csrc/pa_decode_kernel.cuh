@@ -106,7 +106,6 @@ struct DecodeParams {
     int per_head_copies;      // 1: one TMA copy per (head, 128-B column block)
     int q_tma;                // 1: query rows arrive by a 128-B-swizzled tensor copy
     uint32_t q_plane_bytes;   // tcgen05 path: distance between the query slot's 128-B column planes
-    float out_top;            // the merge limits outputs to +- this: 4-bit caches with f16 outputs, else infinity
     int um_rows;              // tcgen05 path: tile rows per KV head (its query rows padded to 32)
     // pa_decode_weights (else null): the scores of every chunk of the stream,
     // [chunk][Hq][ct] in log2 units; (m, l) of every sequence and head; each
@@ -2317,11 +2316,7 @@ pa_reduce_kernel(const __grid_constant__ DecodeParams p) {
         }
         const float inv = den > 0.f ? 1.f / den : 0.f;
 #pragma unroll
-        for (int c = 0; c < DPL; ++c) {
-            float x = num[c] * inv;
-            if (fabsf(x) > p.out_top) x = copysignf(p.out_top, x);        // (NaN stays)
-            o[c] = from_float<OutT>(x);
-        }
+        for (int c = 0; c < DPL; ++c) o[c] = from_float<OutT>(num[c] * inv);
     }
 }
 

@@ -27,7 +27,7 @@ const void* decode_kernel_simt(pa_dtype kv, pa_dtype q, int D) {
     return nullptr;
 }
 
-const void* reduce_kernel(pa_dtype out, int D, bool split_heads) {
+const void* reduce_kernel(pa_dtype out, int D, bool split_heads, bool limit) {
 #define PA_RED(T) \
     if (D == 128) return split_heads ? reinterpret_cast<const void*>(&pa_reduce_kernel<T, 128, RED_SPLIT_WARPS>) \
                                      : reinterpret_cast<const void*>(&pa_reduce_kernel<T, 128, 1>);          \
@@ -35,6 +35,7 @@ const void* reduce_kernel(pa_dtype out, int D, bool split_heads) {
                                     : reinterpret_cast<const void*>(&pa_reduce_kernel<T, 64, 1>);            \
     return nullptr;
     if (out == PA_F32) { PA_RED(float) }
+    if (out == PA_F16 && limit) { PA_RED(LimitedHalf) }
     if (out == PA_F16) { PA_RED(__half) }
     if (out == PA_BF16) { PA_RED(__nv_bfloat16) }
 #undef PA_RED

@@ -38,6 +38,11 @@ __device__ __forceinline__ float e5m2_to_float(uint8_t b) {
 template <typename X> __device__ __forceinline__ X from_float(float x);
 template <> __device__ __forceinline__ float from_float<float>(float x) { return x; }
 template <> __device__ __forceinline__ __half from_float<__half>(float x) { return __float2half_rn(x); }
+// A f16 output that stays within +-65504 (NaN as it is).
+struct LimitedHalf { __half h; };
+template <> __device__ __forceinline__ LimitedHalf from_float<LimitedHalf>(float x) {
+    return LimitedHalf{__float2half_rn(fabsf(x) > 65504.f ? copysignf(65504.f, x) : x)};
+}
 template <> __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
 // ---------------------------------------------------------------------------

@@ -127,11 +127,11 @@ const void* decode_kernel_weights(pa_dtype kv, pa_dtype q, int D) {
     return nullptr;
 }
 
-const void* reduce_kernel_weights(pa_dtype out, int D) {
+const void* reduce_kernel_weights(pa_dtype out, int D, bool limit) {
 #define PA_RED(T) (D == 128 ? reinterpret_cast<const void*>(&pa_reduce_kernel<T, 128, 1, true>) \
                    : D == 64 ? reinterpret_cast<const void*>(&pa_reduce_kernel<T, 64, 1, true>) : nullptr)
     if (out == PA_F32) return PA_RED(float);
-    if (out == PA_F16) return PA_RED(__half);
+    if (out == PA_F16) return limit ? PA_RED(LimitedHalf) : PA_RED(__half);
     if (out == PA_BF16) return PA_RED(__nv_bfloat16);
 #undef PA_RED
     return nullptr;
