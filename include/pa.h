@@ -129,7 +129,8 @@ size_t pa_decode_workspace_size(int num_seqs, int num_q_heads, int max_seq_len,
  * zeros.
  *
  * The work is split into chunks of 16 tokens (32 for fp8 caches with
- * head_dim 128 and at most 8 query heads per KV head), balanced over
+ * head_dim 128 and at most 8 query heads per KV head, 32 to 128 for 4-bit
+ * caches), balanced over
  * persistent CTAs; sequences spanning several CTAs (or longer than
  * partition_tokens) are merged afterwards by a log-sum-exp reduction kernel
  * on the same stream.
@@ -203,7 +204,9 @@ pa_status pa_decode_simt(void* out, const void* q, pa_dtype q_dtype,
  * to f16, so that the scores keep the query's full precision; the others give
  * pa_decode's output.
  *   fresh             int32 [num_seqs] on the device, or null
- *   workspace         at least pa_decode_weights_workspace_size(...) bytes
+ *   workspace         at least pa_decode_weights_workspace_size(...) bytes: that of
+ *                     pa_decode and 4 bytes per query head and place of the tables
+ *                     (num_seqs * max_blocks_per_seq * block_size places)
  * Other arguments as for pa_decode; at most 65535 sequences.
  */
 size_t pa_decode_weights_workspace_size(int num_seqs, int num_q_heads, int max_seq_len,
@@ -370,6 +373,8 @@ pa_status pa_attention(void* out, const void* q, pa_dtype q_dtype,
  * with a block outside the pool among the blocks it uses
  * (PA_ERRBIT_BAD_BLOCK), is skipped: kept is -1 throughout, its new length is
  * L in place and 0 otherwise.
+ * The time grows with the width of the tables, not with the lengths alone: no
+ * wider than the batch needs is best.
  * Any cache type; a head's row must be a multiple of 16 bytes, at most 1024, and
  * a block less than 2 GB; budget <= 2^30.
  *   workspace         at least pa_evict_workspace_size(...) bytes, 256-byte

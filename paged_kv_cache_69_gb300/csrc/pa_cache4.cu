@@ -11,6 +11,9 @@
 // its elements; codes come from plain f32 quotients but for the few next to
 // a border), the gather by HBM, both by the launch for the tokens of a step.
 // 65536 tokens of 8 heads x 128, bf16: 105 us (HBM alone 50) and 64 us (50).
+// Reads of the other caches move bits, or widen fp8: the same tokens of f16 82 us
+// (79), f32 166 (159), e4m3 to bf16 72 (60), 4 bits and e4m3 to f32 137 and 140
+// (90 and 99).
 #include <cstdio>
 
 #include "pa_cache4.h"

@@ -37,16 +37,20 @@
 //
 // Measured (us, one call, against the bytes alone at the copy rate): the
 // 7B-like batch of 64 (28 heads on 4, f16) 51 (23), the same with 1-4 query
-// tokens 129 (23), 1024 sequences of 20-2048 tokens 64 (26), 8 sequences of
-// 32k-131k tokens 181 (120).  Bound by issue: every key costs its masks, its
-// two numbers and the softmax of 8 rows whatever the rows hold, and 16 rows
-// hold both products' tiles.  The copies alone, the arithmetic left out, take
-// 39, 66, 46 and 134.  What was tried beside this form: two CTAs per SM with 64
-// tokens per warp (171 on the long sequences, but 76 on the short ones, where
-// 32 tokens then took 70); four CTAs of 96 registers (227 on the long ones,
-// spills); separate barriers for keys and values (193); for 8 rows one
-// 16-token tile at a time (190; for 16 rows that form is the faster one, 146
-// against 175 on 1-4 query tokens, the registers holding one tile).
+// tokens 132 (23), 1024 sequences of 20-2048 tokens 62 (26), 8 sequences of
+// 32k-131k tokens 183 (120).  The copies alone, the arithmetic left out, take
+// 39, 66, 46 and 134, of which about 12 are the plan, the pipeline's fill and
+// the merge.  No unit is full (issue 39 to 51%, tensor pipe 16 to 27%): beyond
+// the copies the latency of one chunk's chain sets the pace, masks, products,
+// scale, exponent, transpose, products, with 3 consumer warps per scheduler
+// (2 of 16 rows); and every key costs its masks, its two numbers and the
+// softmax of 8 rows whatever the rows hold.  What was tried beside this form,
+// at the times of then (181, 64 and 129): two CTAs per SM with 64 tokens per
+// warp (171 on the long sequences, but 76 on the short ones, where 32 tokens
+// then took 70); four CTAs of 96 registers (227 on the long ones, spills);
+// separate barriers for keys and values (193); for 8 rows one 16-token tile at a
+// time (190; for 16 rows that form is the faster one, 146 against 175 on 1-4
+// query tokens, the registers holding one tile).
 #include <algorithm>
 #include <cmath>
 #include <cuda.h>

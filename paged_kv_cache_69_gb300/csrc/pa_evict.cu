@@ -31,6 +31,15 @@
 // wide, so that the few hundred rows of a steady eviction take one or two
 // steps; into other blocks 256 bytes, and the rows are cut over CTAs as well
 // (64-byte slices of 4096 rows moved 4.5 TB/s, 256-byte ones 5.6).
+//
+// The launch follows what the table could hold, since the host does not see the
+// lengths: 64 sequences of 2064 tokens one block over their budget take 27 us in
+// f16, 22 in e4m3 and 20 in 4 bits under a tight table, but 111, 106 and 105
+// under one for 131072 tokens (8 CTAs per row, most with little to do) and 123,
+// 118 and 117 under one for 262144 (weights read again in every pass); 8 prompts
+// of 47k to 131k tokens brought to 4096 102, 83 and 80 under 131072, and 154, 138
+// and 130 under 262144.  So tables no wider than the batch needs are the faster
+// ones.
 #include <algorithm>
 
 #include "pa_common.h"

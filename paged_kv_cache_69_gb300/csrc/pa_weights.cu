@@ -15,9 +15,14 @@
 // Measured: the 7B-like batch of 64 in f16 118 us, of which pa_decode alone
 // takes 92 (514 MB of keys and values; 28 MB of scores written and read, 8 MB
 // of weights updated); 8 sequences of 32k-131k tokens in 4 bits 221 against
-// 179 (83 MB of scores, written and read).  The rest is the merge's and this
+// 183 (83 MB of scores, written and read).  The rest is the merge's and this
 // kernel's start and end behind the decode kernel.  Keys and values are marked
 // to leave L2 first, so that most scores are still there when they are read.
+// A batch of 64 and 287306 tokens in e4m3 takes 105 us (pa_decode's own fp8
+// kernel 71, bytes 45), in 4 bits 60 (52, 25), in f32 3720 (3830, 175; CUDA
+// cores).  The scores have room for every place of the table, 4 bytes per query
+// head, and the grid covers it: under tables for 131072 tokens those 64
+// sequences need 945 MB of workspace instead of 64 and 7 to 10 us more.
 #include <cuda.h>
 
 #include "pa_common.h"
