@@ -10,6 +10,9 @@
  *   pa_decode             one decode step of attention over a paged pool,
  *   pa_decode_weights     the same, and the keys' weights added up,
  *   pa_attention          several causal query tokens per sequence,
+ *   pa_prefill            causal attention of whole prompts, packed,
+ *   pa_prefill_cached     the same over the paged pool (prompt chunks, prompts
+ *                         behind a cached prefix),
  *   pa_evict              bring sequences down to a budget of tokens by their
  *                         accumulated attention weight.
  *
@@ -342,6 +345,58 @@ pa_status pa_attention(void* out, const void* q, pa_dtype q_dtype,
                        int head_dim, int block_size, int num_blocks, float scale,
                        float k_scale, float v_scale, int partition_tokens, void* workspace,
                        size_t workspace_bytes, int32_t* err_flag, cudaStream_t stream);
+
+/*
+ * pa_prefill -- causal attention of whole prompts, packed one behind the other,
+ * with K and V contiguous (as a projection leaves them, or pa_gather_cache).
+ * Sequence i owns query rows q_start[i] .. q_start[i+1]-1 of q and out
+ * ([total_q, num_q_heads, head_dim]) and rows k_start[i] .. k_start[i+1]-1 of key
+ * and value ([total_k, num_kv_heads, head_dim]; k_start null: q_start).  Its n_i
+ * query tokens are the last n_i of its L_i tokens; query token j, at position
+ * p = L_i - n_i + j, attends keys 0..p:
+ *   out[q_start[i] + j, h] = sum_{t<=p} softmax_t(scale * <q, K_t>) V_t.
+ * A token with p < 0 gets zeros, and so does one whose scores are all -infinity.
+ * Keys and values that a token may not attend have no influence on it, whatever
+ * they hold.  q_start and k_start: int32 [num_seqs + 1] on the device,
+ * non-decreasing within [0, total_q] and [0, total_k]; rows of q and out that
+ * belong to no sequence are left as they are.  A sequence whose entries do not
+ * fit is skipped with PA_ERRBIT_BAD_QUERY.  Sequences may have any length,
+ * 0 and 1 among them.
+ * f16 or bf16, q, K, V and out of one type; head_dim 64 or 128; at most 128 query
+ * heads per KV head; tensors 16-byte aligned.  Scores, sums and outputs are held
+ * in f32; the weights enter P*V rounded to the type (f16: 11 bits down to 2^-21 of
+ * the row's largest, fewer below; bf16: 8 bits).
+ *   workspace         at least pa_prefill_workspace_size(...) bytes, 256-byte
+ *                     aligned, no initialisation; calls sharing one must not
+ *                     overlap on the GPU.  It holds the partial results of batches
+ *                     too small to fill the GPU; others do not touch it.
+ */
+size_t pa_prefill_workspace_size(int num_seqs, int total_q, int num_q_heads, int num_kv_heads,
+                                 int head_dim);
+pa_status pa_prefill(void* out, const void* q, const void* key, const void* value, pa_dtype dtype,
+                     const int32_t* q_start, const int32_t* k_start, int num_seqs, int total_q,
+                     int total_k, int num_q_heads, int num_kv_heads, int head_dim, float scale,
+                     void* workspace, size_t workspace_bytes, int32_t* err_flag,
+                     cudaStream_t stream);
+
+/*
+ * pa_prefill_cached -- pa_prefill with K and V in the paged pool (written by
+ * pa_rope_and_cache or pa_reshape_and_cache): sequence i has L_i = seq_lens[i]
+ * tokens there, the last n_i of them new.  For prompts whose first blocks were in
+ * the prefix cache and for prompts that come in chunks; pa_attention does the same
+ * for up to 128 (token, head) rows per KV head.  Keys of a block outside the pool
+ * are left out (PA_ERRBIT_BAD_BLOCK); a sequence longer than its table is skipped
+ * (PA_ERRBIT_SEQ_TOO_LONG).  f16 and bf16 pools; of others, pa_gather_cache makes
+ * the contiguous K and V that pa_prefill takes.  Block sizes as for pa_decode;
+ * fewer than 2^31 - 128 pool slots.
+ */
+pa_status pa_prefill_cached(void* out, const void* q, pa_dtype q_dtype,
+                            const void* k_cache, const void* v_cache, pa_dtype kv_dtype,
+                            const int32_t* block_tables, int max_blocks_per_seq,
+                            const int32_t* seq_lens, const int32_t* q_start, int num_seqs,
+                            int total_q, int num_q_heads, int num_kv_heads, int head_dim,
+                            int block_size, int num_blocks, float scale, void* workspace,
+                            size_t workspace_bytes, int32_t* err_flag, cudaStream_t stream);
 
 /*
  * pa_evict -- bring every sequence longer than `budget` down to it, per KV

@@ -28,7 +28,8 @@ EXPORTED = ("pa_status_string", "pa_last_error_detail", "pa_decode_workspace_siz
             "pa_decode_simt", "pa_decode_noalloc", "pa_reshape_and_cache", "pa_copy_blocks",
             "pa_copy_blocks_layers", "pa_swap_blocks", "pa_attention", "pa_attention_workspace_size",
             "pa_gather_cache", "pa_block_bytes", "pa_evict", "pa_evict_workspace_size",
-            "pa_decode_weights", "pa_decode_weights_workspace_size")
+            "pa_decode_weights", "pa_decode_weights_workspace_size", "pa_prefill", "pa_prefill_cached",
+            "pa_prefill_workspace_size")
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
 _DTYPE_CODE = {torch.float32: PA_F32, torch.float16: PA_F16, torch.bfloat16: PA_BF16,
@@ -90,6 +91,14 @@ def _configure(L):
     L.pa_decode_weights.restype = c_int
     L.pa_decode_weights.argtypes = [vp, vp, vp, c_int, vp, vp, c_int, vp, c_int, vp, vp, c_int, c_int, c_int, c_int,
                                     c_int, c_int, c_float, c_float, c_float, vp, sz, vp, vp]
+    L.pa_prefill_workspace_size.restype = sz
+    L.pa_prefill_workspace_size.argtypes = [c_int] * 5
+    L.pa_prefill.restype = c_int
+    L.pa_prefill.argtypes = [vp, vp, vp, vp, c_int, vp, vp, c_int, c_int, c_int, c_int, c_int, c_int, c_float, vp, sz, vp,
+                             vp]
+    L.pa_prefill_cached.restype = c_int
+    L.pa_prefill_cached.argtypes = [vp, vp, c_int, vp, vp, c_int, vp, c_int, vp, vp, c_int, c_int, c_int, c_int, c_int,
+                                    c_int, c_int, c_float, vp, sz, vp, vp]
     L.pa_evict_workspace_size.restype = sz
     L.pa_evict_workspace_size.argtypes = [c_int, c_int, c_int, c_int]
     L.pa_evict.restype = c_int
@@ -162,6 +171,10 @@ def _scratch(nbytes: int, device, stream) -> torch.Tensor:
         stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
     with torch.cuda.stream(stream):
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _nbytes(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
 
 
 def _dev(*ts):
@@ -407,6 +420,70 @@ def pa_attention(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_ca
                               D, bs, NB, float(scale), float(k_scale), float(v_scale), int(partition_tokens),
                               _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(err_flag),
                               _stream(stream)))
+    return out
+
+
+def _starts(t: torch.Tensor, B: int, name: str):
+    if t.dtype != torch.int32 or t.numel() != B + 1:
+        raise ValueError(f"{name} must be int32 with num_seqs + 1 entries")
+
+
+def pa_prefill_workspace_size(num_seqs: int, total_q: int, num_q_heads: int, num_kv_heads: int, head_dim: int) -> int:
+    return int(lib().pa_prefill_workspace_size(num_seqs, total_q, num_q_heads, num_kv_heads, head_dim))
+
+
+def pa_prefill(out: torch.Tensor, q: torch.Tensor, key: torch.Tensor, value: torch.Tensor, q_start: torch.Tensor,
+               scale: float, *, k_start: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+               err_flag: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Causal attention of whole prompts, packed.  q/out [T, Hq, D]; key/value
+    [Tk, Hkv, D]; sequence i has query rows q_start[i] .. q_start[i+1]-1 and key
+    rows k_start[i] .. k_start[i+1]-1 (int32 [B+1]; None: q_start), its query
+    tokens being the last of its tokens."""
+    _dev(out, q, key, value, q_start, k_start, workspace, err_flag)
+    if q.dim() != 3 or key.dim() != 3 or tuple(out.shape) != tuple(q.shape) or out.dtype != q.dtype:
+        raise ValueError("q and out must be [total_q, num_q_heads, head_dim] of one dtype")
+    T, Hq, D = q.shape
+    Tk, Hkv, D2 = key.shape
+    if D2 != D or tuple(value.shape) != tuple(key.shape) or key.dtype != q.dtype or value.dtype != q.dtype:
+        raise ValueError("key and value must be [total_k, num_kv_heads, head_dim], head_dim and dtype those of q")
+    B = q_start.numel() - 1
+    _starts(q_start, B, "q_start")
+    if k_start is not None:
+        _starts(k_start, B, "k_start")
+    _flag(err_flag)
+    if workspace is None and B > 0 and T > 0:
+        workspace = _scratch(pa_prefill_workspace_size(B, T, Hq, Hkv, D), q.device, stream)
+    _check(lib().pa_prefill(_ptr(out), _ptr(q), _ptr(key), _ptr(value), _code(q), _ptr(q_start), _ptr(k_start), B, T, Tk,
+                            Hq, Hkv, D, float(scale), _ptr(workspace), _nbytes(workspace), _ptr(err_flag),
+                            _stream(stream)))
+    return out
+
+
+def pa_prefill_cached(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                      block_tables: torch.Tensor, seq_lens: torch.Tensor, q_start: torch.Tensor, scale: float,
+                      kv_dtype=None, *, workspace: Optional[torch.Tensor] = None,
+                      err_flag: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """pa_prefill over the paged pool: sequence i's query rows q_start[i] ..
+    q_start[i+1]-1 (int32 [B+1]) are the last tokens of its seq_lens[i], all of
+    them in the pool already; any number of query tokens."""
+    _dev(out, q, k_cache, v_cache, block_tables, seq_lens, q_start, workspace, err_flag)
+    if q.dim() != 3:
+        raise ValueError("q and out must be [total_q, num_q_heads, head_dim]")
+    T, Hq, D = q.shape
+    NB, bs, Hkv, D2 = _pools(k_cache, v_cache, kv_dtype)
+    B = seq_lens.numel()
+    if D2 != D or tuple(out.shape) != (T, Hq, D) or out.dtype != q.dtype:
+        raise ValueError("q and out must be [total_q, num_q_heads, head_dim] of one dtype, head_dim "
+                         "that of the pools")
+    _tables(block_tables, seq_lens, B)
+    _starts(q_start, B, "q_start")
+    _flag(err_flag)
+    if workspace is None and B > 0 and T > 0:
+        workspace = _scratch(pa_prefill_workspace_size(B, T, Hq, Hkv, D), q.device, stream)
+    _check(lib().pa_prefill_cached(_ptr(out), _ptr(q), _code(q), _ptr(k_cache), _ptr(v_cache), _code(k_cache, kv_dtype),
+                                   _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens), _ptr(q_start), B, T, Hq,
+                                   Hkv, D, bs, NB, float(scale), _ptr(workspace), _nbytes(workspace), _ptr(err_flag),
+                                   _stream(stream)))
     return out
 
 

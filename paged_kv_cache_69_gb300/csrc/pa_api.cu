@@ -14,6 +14,7 @@
 #include "pa_decode_int4.h"
 #include "pa_decode_kernel.cuh"
 #include "pa_kernels.h"
+#include "pa_launch.h"
 
 namespace pa {
 
@@ -41,9 +42,7 @@ cudaError_t allow_shared(const void* kernel, int bytes) {
 // ---------------------------------------------------------------------------
 // device facts (cached per device)
 // ---------------------------------------------------------------------------
-struct DeviceInfo { int sms = 0; int max_smem = 0; };
-
-static bool device_info(DeviceInfo& info) {
+bool device_info(DeviceInfo& info) {
     static std::mutex mu;
     static DeviceInfo cache[64];
     int dev = 0;
@@ -63,12 +62,7 @@ static bool device_info(DeviceInfo& info) {
 // ---------------------------------------------------------------------------
 // tensor-map encoding through the driver entry point
 // ---------------------------------------------------------------------------
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
-                                   CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
-                                   CUtensorMapFloatOOBfill);
-
-static EncodeTiledFn encode_fn() {
+EncodeTiledFn encode_fn() {
     static EncodeTiledFn fn = nullptr;
     static std::once_flag once;
     std::call_once(once, [] {
@@ -81,7 +75,7 @@ static EncodeTiledFn encode_fn() {
     return fn;
 }
 
-static CUtensorMapDataType tmap_type(pa_dtype d) {
+CUtensorMapDataType tmap_type(pa_dtype d) {
     switch (d) {
         case PA_F32: return CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
         case PA_F16: return CU_TENSOR_MAP_DATA_TYPE_FLOAT16;

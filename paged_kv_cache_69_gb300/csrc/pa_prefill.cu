@@ -1,0 +1,196 @@
+// pa_prefill.cu -- pa_prefill and pa_prefill_cached: causal attention of whole
+// prompts, with K and V contiguous or in the paged pool.  Argument checks, the
+// plan and the launches; the kernel is in pa_prompt_kernel.cuh.
+#include <cuda.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdio>
+
+#include "pa_kernels.h"
+#include "pa_launch.h"
+#include "pa_prompt.h"
+#include "pa_prompt_kernel.cuh"
+
+namespace pa {
+
+static size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+
+PromptPlan prompt_plan(int B, int total_q, int Hq, int Hkv, int D, int max_keys, bool shared, int sms) {
+    PromptPlan pl;
+    const long long TT = 2LL * (PT_M / (Hq / Hkv));
+    const long long items = (total_q / TT + B) * Hkv;      // at most
+    const long long chunks = std::max(1, (max_keys + PT_M - 1) / PT_M);
+    pl.splits = static_cast<int>(std::max(1LL, std::min({sms / std::max(1LL, items), chunks, 64LL})));
+    if (pl.splits == 1 && !shared) return pl;
+    pl.slots = static_cast<size_t>(total_q / TT + B + 1) * Hkv * pl.splits;
+    pl.ml_bytes = up256(pl.slots * 2 * PT_M * sizeof(float2));
+    pl.acc_bytes = up256(pl.slots * 2 * PT_M * D * sizeof(float));
+    return pl;
+}
+
+static CUresult encode4(CUtensorMap* m, pa_dtype dt, const void* base, cuuint64_t d1, cuuint64_t d2, cuuint64_t planes,
+                        cuuint64_t s1, cuuint64_t s2, cuuint32_t b1, cuuint32_t b2) {
+    const EncodeTiledFn enc = encode_fn();
+    if (!enc) return CUDA_ERROR_NOT_FOUND;
+    const cuuint64_t dims[4] = {64, d1, d2, planes};
+    const cuuint64_t strides[3] = {s1, s2, 128};
+    const cuuint32_t box[4] = {64, b1, b2, 1}, es[4] = {1, 1, 1, 1};
+    return enc(m, tmap_type(dt), 4, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
+template <class KV, int D>
+static cudaError_t launch(const PromptParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                          int grid, cudaStream_t stream) {
+    const void* kern = reinterpret_cast<const void*>(&prompt_kernel<KV, D>);
+    cudaError_t e = allow_shared(kern, PromptLayout<D>::BYTES);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(PT_THREADS);
+    cfg.dynamicSmemBytes = PromptLayout<D>::BYTES;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    void* args[] = {const_cast<PromptParams*>(&p), const_cast<CUtensorMap*>(&tq), const_cast<CUtensorMap*>(&tk),
+                    const_cast<CUtensorMap*>(&tv)};
+    if ((e = cudaLaunchKernelExC(&cfg, kern, args)) != cudaSuccess || p.splits == 1 || p.shared) return e;
+    const long long warps = static_cast<long long>(p.total_q) * p.Hq;
+    cfg.gridDim = dim3(static_cast<unsigned>((warps + 7) / 8));
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(&prompt_merge_kernel<KV, D>), args);
+}
+
+static pa_status bad(const PromptCall& c, pa_status st, const char* what) {
+    char msg[192];
+    std::snprintf(msg, sizeof msg, "%s: %s", c.who, what);
+    return fail(st, msg);
+}
+
+pa_status launch_prompt(const PromptCall& c, const PromptPlan& plan, void* parts, PromptParams* p_out) {
+    DeviceInfo dev;
+    if (!device_info(dev)) return bad(c, PA_ERR_CUDA, "cannot query the current device");
+    const int G = c.Hq / c.Hkv;
+    PromptParams p{};
+    p.out = c.out;
+    p.q_start = c.q_start; p.k_start = c.k_start; p.seq_lens = c.seq_lens; p.block_tables = c.block_tables;
+    p.err_flag = c.err_flag;
+    p.B = c.B; p.Hq = c.Hq; p.Hkv = c.Hkv; p.G = G; p.bs = c.bs; p.NB = c.NB; p.MB = c.MB;
+    p.total_q = c.total_q; p.total_k = c.total_k;
+    p.tokens = PT_M / G;
+    p.splits = plan.splits;
+    p.causal = !c.shared;
+    p.shared = c.shared;
+    p.min_rows = c.min_rows;
+    p.rpb = c.k_start ? PT_M : std::min(c.bs, PT_M);
+    if (plan.slots) {
+        p.part_ml = static_cast<float2*>(parts);
+        p.part_acc = reinterpret_cast<float*>(static_cast<uint8_t*>(parts) + plan.ml_bytes);
+    }
+    // scale enters as a positive factor of the scores' exponent; its sign goes into the MMA
+    p.c = std::max(std::fabs(c.scale) * 1.4426950408889634f, 1.17549435e-38f);
+    p.negate = c.scale < 0.f ? 1u << 13 : 0u;
+    const cuuint64_t D2 = static_cast<cuuint64_t>(c.D) * 2, planes = c.D / 64;
+    const cuuint64_t rows = c.k_start ? std::max(c.total_k, 1) : static_cast<cuuint64_t>(c.NB) * c.bs;
+    alignas(64) CUtensorMap tq, tk, tv;
+    CUresult r = encode4(&tq, c.dtype, c.q, c.Hq, c.total_q, planes, D2, D2 * c.Hq, G, p.tokens);
+    if (r == CUDA_SUCCESS) r = encode4(&tk, c.dtype, c.k, rows, c.Hkv, planes, D2 * c.Hkv, D2, p.rpb, 1);
+    if (r == CUDA_SUCCESS) r = encode4(&tv, c.dtype, c.v, rows, c.Hkv, planes, D2 * c.Hkv, D2, p.rpb, 1);
+    if (r != CUDA_SUCCESS) {
+        char msg[96];
+        std::snprintf(msg, sizeof msg, "cuTensorMapEncodeTiled failed (CUresult %d)", static_cast<int>(r));
+        return bad(c, PA_ERR_CUDA, msg);
+    }
+    const long long items = (static_cast<long long>(c.total_q) / (2 * p.tokens) + c.B) * c.Hkv * p.splits;
+    const int grid = static_cast<int>(std::min<long long>(items, dev.sms));
+    cudaError_t e;
+    if (c.dtype == PA_F16)
+        e = c.D == 128 ? launch<F16T, 128>(p, tq, tk, tv, grid, c.stream) : launch<F16T, 64>(p, tq, tk, tv, grid, c.stream);
+    else
+        e = c.D == 128 ? launch<BF16T, 128>(p, tq, tk, tv, grid, c.stream) : launch<BF16T, 64>(p, tq, tk, tv, grid, c.stream);
+    if (p_out) *p_out = p;
+    if (e != cudaSuccess) {
+        char msg[96];
+        std::snprintf(msg, sizeof msg, "%s: kernel launch", c.who);
+        return fail_cuda(msg, e);
+    }
+    return PA_OK;
+}
+
+// The checks of both calls, the plan and the launches.
+static pa_status prefill(const PromptCall& c, pa_dtype kv_dtype, void* workspace, size_t workspace_bytes) {
+    if (c.B < 0 || c.Hq <= 0 || c.Hkv <= 0 || c.D <= 0 || c.total_q < 0 || c.total_k < 0 || c.bs <= 0 || c.NB <= 0 || c.MB <= 0)
+        return bad(c, PA_ERR_INVALID_ARG, "sizes must be positive (num_seqs and row counts >= 0)");
+    if (c.B == 0 || c.total_q == 0) return PA_OK;
+    if (!c.out || !c.q || !c.k || !c.v || !c.q_start || !(c.k_start || (c.block_tables && c.seq_lens)))
+        return bad(c, PA_ERR_INVALID_ARG, "null pointer");
+    if (!valid_dtype(c.dtype) || !valid_cache_dtype(kv_dtype)) return bad(c, PA_ERR_INVALID_ARG, "unknown dtype");
+    if (c.Hq % c.Hkv != 0) return bad(c, PA_ERR_INVALID_ARG, "num_q_heads must be a multiple of num_kv_heads");
+    if (c.dtype != kv_dtype || (c.dtype != PA_F16 && c.dtype != PA_BF16))
+        return bad(c, PA_ERR_UNSUPPORTED, "q, K and V must be f16 or bf16, all of one type");
+    if (c.D != 64 && c.D != 128) return bad(c, PA_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
+    if (c.Hq / c.Hkv > PT_M) return bad(c, PA_ERR_UNSUPPORTED, "at most 128 query heads per KV head");
+    if (c.Hkv > 256) return bad(c, PA_ERR_UNSUPPORTED, "num_kv_heads must be <= 256");
+    if (c.block_tables && c.bs != 8 && c.bs != 16 && c.bs != 32 && c.bs != 64 && c.bs != 128)
+        return bad(c, PA_ERR_UNSUPPORTED, "block_size must be 8, 16, 32, 64 or 128");
+    if (static_cast<long long>(c.NB) * c.bs >= (1LL << 31) - PT_M || static_cast<long long>(c.MB) * c.bs >= (1LL << 30) ||
+        c.total_q >= (1 << 30) || c.total_k >= (1 << 30) || (static_cast<long long>(c.total_q) + c.B) * c.Hq >= (1LL << 31))
+        return bad(c, PA_ERR_UNSUPPORTED, "pool, table or batch too large for 32-bit row coordinates");
+    if (!aligned16(c.q) || !aligned16(c.out) || !aligned16(c.k) || !aligned16(c.v))
+        return bad(c, PA_ERR_INVALID_ARG, "q, out, K and V must be 16-byte aligned");
+    DeviceInfo dev;
+    if (!device_info(dev)) return bad(c, PA_ERR_CUDA, "cannot query the current device");
+    const int max_keys = c.k_start ? c.total_k : c.MB * c.bs;
+    const PromptPlan plan = prompt_plan(c.B, c.total_q, c.Hq, c.Hkv, c.D, max_keys, false, dev.sms);
+    if (plan.slots) {
+        if (!workspace) return bad(c, PA_ERR_WORKSPACE, "workspace pointer is null");
+        if (workspace_bytes < plan.ml_bytes + plan.acc_bytes)
+            return bad(c, PA_ERR_WORKSPACE, "workspace smaller than pa_prefill_workspace_size()");
+        if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+            return bad(c, PA_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+    }
+    return launch_prompt(c, plan, workspace, nullptr);
+}
+
+}  // namespace pa
+
+using namespace pa;
+
+extern "C" size_t pa_prefill_workspace_size(int num_seqs, int total_q, int num_q_heads, int num_kv_heads, int head_dim) {
+    if (num_seqs < 0 || total_q < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
+        num_q_heads % num_kv_heads != 0 || num_q_heads / num_kv_heads > PT_M)
+        return 0;
+    DeviceInfo dev;
+    if (!device_info(dev)) return 0;
+    // for keys of any number
+    const PromptPlan plan = prompt_plan(num_seqs, total_q, num_q_heads, num_kv_heads, head_dim, 1 << 30, false, dev.sms);
+    return std::max<size_t>(256, plan.ml_bytes + plan.acc_bytes);
+}
+
+extern "C" pa_status pa_prefill(void* out, const void* q, const void* key, const void* value, pa_dtype dtype,
+                                const int32_t* q_start, const int32_t* k_start, int num_seqs, int total_q, int total_k,
+                                int num_q_heads, int num_kv_heads, int head_dim, float scale, void* workspace,
+                                size_t workspace_bytes, int32_t* err_flag, cudaStream_t stream) {
+    clear_error();
+    PromptCall c{"prefill", out, q, dtype, key, value, q_start, k_start ? k_start : q_start, nullptr, nullptr, num_seqs,
+                 num_q_heads, num_kv_heads, head_dim, total_q, total_k, PT_M, 1, 1, scale, false, 0, err_flag, stream};
+    return prefill(c, dtype, workspace, workspace_bytes);
+}
+
+extern "C" pa_status pa_prefill_cached(void* out, const void* q, pa_dtype q_dtype, const void* k_cache, const void* v_cache,
+                                       pa_dtype kv_dtype, const int32_t* block_tables, int max_blocks_per_seq,
+                                       const int32_t* seq_lens, const int32_t* q_start, int num_seqs, int total_q,
+                                       int num_q_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                                       float scale, void* workspace, size_t workspace_bytes, int32_t* err_flag,
+                                       cudaStream_t stream) {
+    clear_error();
+    PromptCall c{"prefill_cached", out, q, q_dtype, k_cache, v_cache, q_start, nullptr, seq_lens, block_tables, num_seqs,
+                 num_q_heads, num_kv_heads, head_dim, total_q, 0, block_size, num_blocks, max_blocks_per_seq, scale, false, 0,
+                 err_flag, stream};
+    return prefill(c, kv_dtype, workspace, workspace_bytes);
+}

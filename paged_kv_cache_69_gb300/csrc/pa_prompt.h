@@ -1,0 +1,38 @@
+// pa_prompt.h -- host side of the prompt kernel: what pa_prefill.cu offers to
+// the calls that launch it.
+#pragma once
+
+#include <cstddef>
+
+#include "pa_common.h"
+
+namespace pa {
+
+struct PromptCall {
+    const char* who;                   // call named in error details
+    void* out;
+    const void* q;
+    pa_dtype dtype;                    // of q, out, K and V
+    const void *k, *v;                 // contiguous rows (k_start) or pools (block_tables)
+    const int32_t *q_start, *k_start, *seq_lens, *block_tables;
+    int B, Hq, Hkv, D, total_q, total_k, bs, NB, MB;
+    float scale;
+    bool shared;                       // q_start: members of groups, seq_lens: prefixes; partials only
+    int min_rows;
+    int32_t* err_flag;
+    cudaStream_t stream;
+};
+
+// How a call is cut: ranges of keys per item and the places of partials.
+struct PromptPlan {
+    int splits = 1;
+    size_t slots = 0, ml_bytes = 0, acc_bytes = 0;         // of the partials (0 without)
+};
+PromptPlan prompt_plan(int B, int total_q, int Hq, int Hkv, int D, int max_keys, bool shared, int sms);
+
+// The kernel; partials at `parts` (256-byte aligned, plan's bytes). p_out: the
+// kernel's parameters for a merge.
+struct PromptParams;
+pa_status launch_prompt(const PromptCall& c, const PromptPlan& plan, void* parts, PromptParams* p_out);
+
+}  // namespace pa
