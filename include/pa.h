@@ -3,6 +3,7 @@
  *
  * The library implements the data-parallel hot path of paged KV caching:
  *   pa_reshape_and_cache  write new tokens' K/V into pool slots,
+ *   pa_rope_and_cache     the same with queries and keys rotated by position,
  *   pa_gather_cache       read cached rows back as values,
  *   pa_copy_blocks        copy-on-write of shared blocks (one layer, or
  *                         all layers: pa_copy_blocks_layers),
@@ -98,6 +99,7 @@ typedef enum {
 #define PA_ERRBIT_BAD_QUERY    32u   /* pa_attention: q_start entries not increasing within
                                         [0, total_q], or a sequence with more than max_q_len
                                         query tokens; its rows are left unwritten */
+#define PA_ERRBIT_BAD_POSITION 64u   /* pa_rope_and_cache: a position outside the table */
 
 /* Human-readable name of a status. */
 const char* pa_status_string(pa_status s);
@@ -275,6 +277,46 @@ pa_status pa_reshape_and_cache(void* k_cache, void* v_cache, pa_dtype kv_dtype,
                                int num_kv_heads, int head_dim, int block_size,
                                int num_blocks, float k_scale, float v_scale,
                                int32_t* err_flag, cudaStream_t stream);
+
+/*
+ * pa_rope_and_cache -- rotate the queries and keys of new tokens by their
+ * positions and write K and V into the pool, in one launch.
+ *   q, q_out           [num_tokens, num_q_heads, head_dim]; q_out gets the rotated
+ *                      queries and may be q.  num_q_heads 0 (q and q_out null): keys
+ *                      and values alone.
+ *   key, value         [num_tokens, num_kv_heads, head_dim]; the pool gets, at slot
+ *                      slot_mapping[t], what pa_reshape_and_cache would write of the
+ *                      rotated key and the value.
+ *   key_out            the rotated keys, for a prompt's own attention (pa_prefill);
+ *                      null or key itself are both fine.
+ *   cos_sin            f32 [max_positions, rot_dim]: row p holds the rot_dim / 2
+ *                      cosines, then sines, of position p's angles.
+ *   positions          int64 [num_axes, num_tokens].  With one axis (sections
+ *                      ignored) every pair of a token turns by its position.  With
+ *                      2 to 4 (time, height, width, ...) the first sections[0] pairs
+ *                      turn by the position on axis 0, the next sections[1] by that on
+ *                      axis 1, and so on; sections is a HOST array of num_axes numbers
+ *                      that add up to rot_dim / 2.
+ * With a = x[i], b = x[i + rot_dim / 2] (interleaved != 0: a = x[2 i],
+ * b = x[2 i + 1]), pair i < rot_dim / 2 becomes a cos - b sin and b cos + a sin, in
+ * f32, rounded once to the type of q and key; elements from rot_dim on stay as they
+ * are.  rot_dim is a multiple of 16, at most head_dim; head_dim 64 or 128.
+ * Sources f32, f16 or bf16, q, key and value of one type: that of the pool, or any
+ * for fp8 and 4-bit pools, which quantise the rounded key.
+ *   slot < 0                          padding: nothing of the token is written.
+ *   slot >= num_blocks*block_size     the same, and PA_ERRBIT_BAD_SLOT.
+ *   a position outside the table      the same, and PA_ERRBIT_BAD_POSITION.
+ * Other arguments, limits and duplicate slots as for pa_reshape_and_cache; fewer
+ * than 2^31 rows (tokens x (query + 2 KV heads)) and pool slots.
+ */
+pa_status pa_rope_and_cache(void* k_cache, void* v_cache, pa_dtype kv_dtype, void* q_out,
+                            void* key_out, const void* q, const void* key, const void* value,
+                            pa_dtype src_dtype, const int64_t* positions, int num_axes,
+                            const int* sections, const float* cos_sin, int max_positions,
+                            int rot_dim, int interleaved, const int64_t* slot_mapping,
+                            int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                            int block_size, int num_blocks, float k_scale, float v_scale,
+                            int32_t* err_flag, cudaStream_t stream);
 
 /*
  * pa_gather_cache -- the inverse of pa_reshape_and_cache: row t of key and

@@ -21,7 +21,7 @@ LIB_PATH = os.path.join(HERE, "libpa.so")
 PA_F32, PA_F16, PA_BF16, PA_FP8_E4M3, PA_FP8_E5M2, PA_INT4 = 0, 1, 2, 3, 4, 5
 PA_OK = 0
 ERRBIT_BAD_BLOCK, ERRBIT_BAD_SLOT, ERRBIT_BAD_PAIR, ERRBIT_SEQ_TOO_LONG, ERRBIT_WAIT_TIMEOUT = 1, 2, 4, 8, 16
-ERRBIT_BAD_QUERY = 32
+ERRBIT_BAD_QUERY, ERRBIT_BAD_POSITION = 32, 64
 
 # entry points declared in include/pa.h
 EXPORTED = ("pa_status_string", "pa_last_error_detail", "pa_decode_workspace_size", "pa_decode",
@@ -29,7 +29,7 @@ EXPORTED = ("pa_status_string", "pa_last_error_detail", "pa_decode_workspace_siz
             "pa_copy_blocks_layers", "pa_swap_blocks", "pa_attention", "pa_attention_workspace_size",
             "pa_gather_cache", "pa_block_bytes", "pa_evict", "pa_evict_workspace_size",
             "pa_decode_weights", "pa_decode_weights_workspace_size", "pa_prefill", "pa_prefill_cached",
-            "pa_prefill_workspace_size")
+            "pa_prefill_workspace_size", "pa_rope_and_cache")
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
 _DTYPE_CODE = {torch.float32: PA_F32, torch.float16: PA_F16, torch.bfloat16: PA_BF16,
@@ -91,6 +91,9 @@ def _configure(L):
     L.pa_decode_weights.restype = c_int
     L.pa_decode_weights.argtypes = [vp, vp, vp, c_int, vp, vp, c_int, vp, c_int, vp, vp, c_int, c_int, c_int, c_int,
                                     c_int, c_int, c_float, c_float, c_float, vp, sz, vp, vp]
+    L.pa_rope_and_cache.restype = c_int
+    L.pa_rope_and_cache.argtypes = [vp, vp, c_int, vp, vp, vp, vp, vp, c_int, vp, c_int, vp, vp, c_int, c_int, c_int, vp,
+                                    c_int, c_int, c_int, c_int, c_int, c_int, c_float, c_float, vp, vp]
     L.pa_prefill_workspace_size.restype = sz
     L.pa_prefill_workspace_size.argtypes = [c_int] * 5
     L.pa_prefill.restype = c_int
@@ -308,6 +311,55 @@ def pa_reshape_and_cache(k_cache: torch.Tensor, v_cache: torch.Tensor, key: torc
     _check(lib().pa_reshape_and_cache(_ptr(k_cache), _ptr(v_cache), _code(k_cache, kv_dtype), _ptr(key),
                                       _ptr(value), _code(key), _ptr(slot_mapping), T, Hkv, D, bs, NB,
                                       float(k_scale), float(v_scale), _ptr(err_flag), _stream(stream)))
+
+
+def rope_table(num_positions: int, rot_dim: int, base: float = 10000.0, device=None) -> torch.Tensor:
+    """cos_sin of pa_rope_and_cache, float32 [num_positions, rot_dim]: cosines,
+    then sines, of position * base^(-2i / rot_dim), the angles in 64 bits."""
+    pair = torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device or "cuda")
+    angle = torch.arange(num_positions, dtype=torch.float64, device=pair.device)[:, None] * base ** (-pair / rot_dim)
+    return torch.cat([angle.cos(), angle.sin()], 1).float()
+
+
+def pa_rope_and_cache(k_cache: torch.Tensor, v_cache: torch.Tensor, q_out: Optional[torch.Tensor],
+                      q: Optional[torch.Tensor], key: torch.Tensor, value: torch.Tensor, positions: torch.Tensor,
+                      cos_sin: torch.Tensor, slot_mapping: torch.Tensor, kv_dtype=None, *,
+                      key_out: Optional[torch.Tensor] = None, sections=None, interleaved: bool = False,
+                      k_scale: float = 1.0, v_scale: float = 1.0, err_flag: Optional[torch.Tensor] = None,
+                      stream=None) -> None:
+    """Rotate q [T, Hq, D] into q_out (it may be q) and key [T, Hkv, D] by
+    positions (int64 [T], or [axes, T] with ``sections``, the rotated pairs of each
+    axis), and write K/V into pool slots slot_mapping (int64 [T]).  cos_sin is
+    float32 [positions, rot_dim] (rope_table); key_out receives the rotated keys.
+    q and q_out may be None: keys and values alone."""
+    _dev(k_cache, v_cache, q_out, q, key, value, positions, cos_sin, slot_mapping, key_out, err_flag)
+    NB, bs, Hkv, D = _pools(k_cache, v_cache, kv_dtype)
+    T = key.shape[0]
+    if tuple(key.shape) != (T, Hkv, D) or tuple(value.shape) != (T, Hkv, D) or value.dtype != key.dtype:
+        raise ValueError("key/value must be [num_tokens, num_kv_heads, head_dim] of one dtype")
+    if key_out is not None and (tuple(key_out.shape) != (T, Hkv, D) or key_out.dtype != key.dtype):
+        raise ValueError("key_out must have the shape and dtype of key")
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    Hq = 0
+    if q is not None:
+        Hq = q.shape[1] if q.dim() == 3 else 0
+        for t in (q, q_out):
+            if tuple(t.shape) != (T, Hq, D) or Hq == 0 or t.dtype != key.dtype:
+                raise ValueError("q and q_out must be [num_tokens, num_q_heads, head_dim] of key's dtype")
+    axes = 1 if sections is None else len(sections)
+    if positions.dtype != torch.int64 or positions.numel() != axes * T or (axes > 1 and tuple(positions.shape) != (axes, T)):
+        raise ValueError("positions must be int64 [num_tokens], or [len(sections), num_tokens]")
+    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
+        raise ValueError("cos_sin must be float32 [positions, rot_dim]")
+    if slot_mapping.dtype != torch.int64 or slot_mapping.numel() != T:
+        raise ValueError("slot_mapping must be int64 [num_tokens]")
+    _flag(err_flag)
+    sec = None if sections is None else (ctypes.c_int * max(1, axes))(*[int(x) for x in sections])
+    _check(lib().pa_rope_and_cache(_ptr(k_cache), _ptr(v_cache), _code(k_cache, kv_dtype), _ptr(q_out), _ptr(key_out),
+                                   _ptr(q), _ptr(key), _ptr(value), _code(key), _ptr(positions), axes, sec, _ptr(cos_sin),
+                                   cos_sin.shape[0], cos_sin.shape[1], int(bool(interleaved)), _ptr(slot_mapping), T, Hq,
+                                   Hkv, D, bs, NB, float(k_scale), float(v_scale), _ptr(err_flag), _stream(stream)))
 
 
 def pa_gather_cache(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,

@@ -19,6 +19,7 @@
 #include "pa_cache4.h"
 #include "pa_common.h"
 #include "pa_int4.cuh"
+#include "pa_rows.cuh"
 
 namespace pa {
 
@@ -26,43 +27,6 @@ constexpr int ROW_THREADS = 256;
 // Elements per lane.  (32 in the write: 108 us as with 16, and 2 us more for
 // the 64 tokens of a step.)
 constexpr int EPL = 16;
-
-// 8 consecutive elements as floats.
-template <class S>
-__device__ __forceinline__ void load8(const uint8_t* src, float (&x)[8]) {
-    if constexpr (S::code == PA_F32) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(src));
-        const float4 b = __ldg(reinterpret_cast<const float4*>(src) + 1);
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-    } else {
-        const uint4 r = __ldg(reinterpret_cast<const uint4*>(src));
-        const typename S::T* e = reinterpret_cast<const typename S::T*>(&r);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = to_float(e[k]);
-    }
-}
-template <class S>
-__device__ __forceinline__ void store8(uint8_t* dst, const float (&x)[8]) {
-    if constexpr (S::code == PA_F32) {
-        reinterpret_cast<float4*>(dst)[0] = make_float4(x[0], x[1], x[2], x[3]);
-        reinterpret_cast<float4*>(dst)[1] = make_float4(x[4], x[5], x[6], x[7]);
-    } else {
-        constexpr bool bf = S::code == PA_BF16;
-        *reinterpret_cast<uint4*>(dst) = make_uint4(pack2(x[0], x[1], bf), pack2(x[2], x[3], bf),
-                                                    pack2(x[4], x[5], bf), pack2(x[6], x[7], bf));
-    }
-}
-
-// x / d for a divisor that is the same for a whole launch: m = ceil(2^32 / d)
-// gives a quotient that is right or one too large.
-struct Div {
-    uint32_t d, m;
-};
-__device__ __forceinline__ uint32_t div_by(uint32_t x, Div v) {
-    if (v.d == 1) return x;
-    const uint32_t q = __umulhi(x, v.m);
-    return q - (q * v.d > x ? 1u : 0u);
-}
 
 struct RowArgs {
     const int64_t* slots;
@@ -128,36 +92,9 @@ write4_kernel(uint8_t* __restrict__ kc, uint8_t* __restrict__ vc, const uint8_t*
     }
     on = on && row_place<LPR>(a, slot, r);
     if (!on) return;
-    const bool nan = mn != mn;
-    if (mx > 65504.f || mn < -65504.f) {
-#pragma unroll
-        for (int k = 0; k < EPL; ++k) x[k / 8][k % 8] = fminf(fmaxf(x[k / 8][k % 8], -65504.f), 65504.f);
-        mn = fminf(fmaxf(mn, -65504.f), 65504.f);
-        mx = fminf(fmaxf(mx, -65504.f), 65504.f);
-    }
     __half step, low;
-    int4_params(mn, mx, step, low);
-    uint32_t w[NW] = {};
-    if (nan) {
-        step = low = __ushort_as_half(0x7e00);
-    } else {
-        const float fl = __half2float(low), fs = __half2float(step);
-        if (fs > 0.f) {
-            const float r15 = rcp_approx(15.f * fs);      // 15 * step is exact
-            float near = 0.f;
-#pragma unroll
-            for (int y = 0; y < NW; ++y) w[y] = int4_codes8(x[y], fl, r15, near);
-            if (near > INT4_NEAR) {
-                const float rs = 1.f / fs;
-#pragma unroll
-                for (int y = 0; y < NW; ++y) {
-                    w[y] = 0;
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) w[y] |= int4_code(x[y][k], fl, fs, rs) << (4 * k);
-                }
-            }
-        }
-    }
+    uint32_t w[NW];
+    int4_quantise(x, mn, mx, step, low, w);
     uint8_t* blk = (v ? vc : kc) + static_cast<size_t>(r.blk) * a.bs.d * a.heads.d * (D / 2 + INT4_PARAM_BYTES);
     *reinterpret_cast<uint2*>(blk + int4_code_off(r.h, r.off, a.bs.d, D) + 8 * j) = make_uint2(w[0], w[1]);
     if (j == 0)
@@ -228,9 +165,6 @@ gather_kernel(uint8_t* __restrict__ key, uint8_t* __restrict__ value, const uint
     }
 }
 
-static Div make_div(int d) {
-    return Div{static_cast<uint32_t>(d), static_cast<uint32_t>(((1ull << 32) + d - 1) / d)};
-}
 static RowArgs row_args(const int64_t* slots, int T, int Hkv, int bs, int NB, int32_t* err) {
     return RowArgs{slots, static_cast<uint32_t>(T) * static_cast<uint32_t>(Hkv), static_cast<uint32_t>(NB) * static_cast<uint32_t>(bs),
                    make_div(Hkv), make_div(bs), err};

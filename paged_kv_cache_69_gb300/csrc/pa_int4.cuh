@@ -123,4 +123,41 @@ __device__ __forceinline__ float int4_value(uint32_t c, float low, float step) {
     return __fmaf_rn(step, static_cast<float>(c), low);
 }
 
+// (step, low) and codes of a row whose extremes are mn and mx (NaN if the row
+// holds one), for the lane that has 8 NW of its elements, 8 to a word.
+template <int NW>
+__device__ __forceinline__ void int4_quantise(float (&x)[NW][8], float mn, float mx, __half& step, __half& low,
+                                              uint32_t (&w)[NW]) {
+    const bool nan = mn != mn;
+    if (mx > 65504.f || mn < -65504.f) {
+#pragma unroll
+        for (int k = 0; k < 8 * NW; ++k) x[k / 8][k % 8] = fminf(fmaxf(x[k / 8][k % 8], -65504.f), 65504.f);
+        mn = fminf(fmaxf(mn, -65504.f), 65504.f);
+        mx = fminf(fmaxf(mx, -65504.f), 65504.f);
+    }
+    int4_params(mn, mx, step, low);
+#pragma unroll
+    for (int y = 0; y < NW; ++y) w[y] = 0;
+    if (nan) {
+        step = low = __ushort_as_half(0x7e00);
+    } else {
+        const float fl = __half2float(low), fs = __half2float(step);
+        if (fs > 0.f) {
+            const float r15 = rcp_approx(15.f * fs);      // 15 * step is exact
+            float near = 0.f;
+#pragma unroll
+            for (int y = 0; y < NW; ++y) w[y] = int4_codes8(x[y], fl, r15, near);
+            if (near > INT4_NEAR) {
+                const float rs = 1.f / fs;
+#pragma unroll
+                for (int y = 0; y < NW; ++y) {
+                    w[y] = 0;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) w[y] |= int4_code(x[y][k], fl, fs, rs) << (4 * k);
+                }
+            }
+        }
+    }
+}
+
 }  // namespace pa
