@@ -10,6 +10,8 @@
  *   pa_swap_blocks        block copies between a device and a host pool,
  *   pa_decode             one decode step of attention over a paged pool,
  *   pa_decode_weights     the same, and the keys' weights added up,
+ *   pa_decode_shared      the same for sequences that share prefixes, each attended
+ *                         once,
  *   pa_attention          several causal query tokens per sequence,
  *   pa_prefill            causal attention of whole prompts, packed,
  *   pa_prefill_cached     the same over the paged pool (prompt chunks, prompts
@@ -226,6 +228,38 @@ pa_status pa_decode_weights(void* out, float* weights, const void* q, pa_dtype q
                             int32_t* err_flag, cudaStream_t stream);
 
 /*
+ * pa_decode_shared -- pa_decode for sequences that share prefixes (forks of one
+ * request, conversations about one document, a common system prompt): the keys of a
+ * prefix are read once for all sequences of its group.
+ * Group j holds the sequences group_start[j] .. group_start[j+1]-1, whose first
+ * prefix_lens[j] tokens lie in the same blocks: the block table of the group's first
+ * sequence is read for them, for the rest each sequence's own.  A prefix that ends
+ * inside a block counts up to that block.  Lengths, tables and results are those of
+ * pa_decode; groups of one, prefixes of 0 and sequences in no group are fine.
+ *   group_start       int32 [num_groups + 1] on the device, non-decreasing within
+ *                     [0, num_seqs].  A group whose entries do not fit is passed over
+ *                     with PA_ERRBIT_BAD_QUERY: its sequences attend by themselves.
+ *   prefix_lens       int32 [num_groups] on the device
+ *   workspace         at least pa_decode_shared_workspace_size(...) bytes, 256-byte
+ *                     aligned, no initialisation; calls sharing one must not overlap
+ *                     on the GPU.
+ * A sequence shorter than its group's prefix, or longer than its table, is left
+ * unwritten with PA_ERRBIT_SEQ_TOO_LONG.  f16 and bf16 pools with q of the same type;
+ * at most 128 query heads per KV head.  Precision: over the prefix as pa_prefill,
+ * else as pa_decode.
+ */
+size_t pa_decode_shared_workspace_size(int num_seqs, int num_groups, int num_q_heads,
+                                       int num_kv_heads, int max_seq_len, int head_dim);
+pa_status pa_decode_shared(void* out, const void* q, pa_dtype q_dtype,
+                           const void* k_cache, const void* v_cache, pa_dtype kv_dtype,
+                           const int32_t* block_tables, int max_blocks_per_seq,
+                           const int32_t* seq_lens, const int32_t* group_start,
+                           const int32_t* prefix_lens, int num_seqs, int num_groups,
+                           int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                           int num_blocks, float scale, void* workspace, size_t workspace_bytes,
+                           int32_t* err_flag, cudaStream_t stream);
+
+/*
  * pa_decode_noalloc -- pa_decode for callers that cannot supply a workspace.
  * The pages have no counterpart: this exists for callers that must not
  * allocate device memory on the call path, such as a serving loop whose
@@ -411,7 +445,8 @@ pa_status pa_attention(void* out, const void* q, pa_dtype q_dtype,
  *   workspace         at least pa_prefill_workspace_size(...) bytes, 256-byte
  *                     aligned, no initialisation; calls sharing one must not
  *                     overlap on the GPU.  It holds the partial results of batches
- *                     too small to fill the GPU; others do not touch it.
+ *                     too small to fill the GPU; others do not touch it.  The size
+ *                     for some numbers of sequences and rows serves all smaller ones.
  */
 size_t pa_prefill_workspace_size(int num_seqs, int total_q, int num_q_heads, int num_kv_heads,
                                  int head_dim);

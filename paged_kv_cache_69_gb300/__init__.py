@@ -29,7 +29,7 @@ EXPORTED = ("pa_status_string", "pa_last_error_detail", "pa_decode_workspace_siz
             "pa_copy_blocks_layers", "pa_swap_blocks", "pa_attention", "pa_attention_workspace_size",
             "pa_gather_cache", "pa_block_bytes", "pa_evict", "pa_evict_workspace_size",
             "pa_decode_weights", "pa_decode_weights_workspace_size", "pa_prefill", "pa_prefill_cached",
-            "pa_prefill_workspace_size", "pa_rope_and_cache")
+            "pa_prefill_workspace_size", "pa_rope_and_cache", "pa_decode_shared", "pa_decode_shared_workspace_size")
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
 _DTYPE_CODE = {torch.float32: PA_F32, torch.float16: PA_F16, torch.bfloat16: PA_BF16,
@@ -94,6 +94,11 @@ def _configure(L):
     L.pa_rope_and_cache.restype = c_int
     L.pa_rope_and_cache.argtypes = [vp, vp, c_int, vp, vp, vp, vp, vp, c_int, vp, c_int, vp, vp, c_int, c_int, c_int, vp,
                                     c_int, c_int, c_int, c_int, c_int, c_int, c_float, c_float, vp, vp]
+    L.pa_decode_shared_workspace_size.restype = sz
+    L.pa_decode_shared_workspace_size.argtypes = [c_int] * 6
+    L.pa_decode_shared.restype = c_int
+    L.pa_decode_shared.argtypes = [vp, vp, c_int, vp, vp, c_int, vp, c_int, vp, vp, vp, c_int, c_int, c_int, c_int, c_int,
+                                   c_int, c_int, c_float, vp, sz, vp, vp]
     L.pa_prefill_workspace_size.restype = sz
     L.pa_prefill_workspace_size.argtypes = [c_int] * 5
     L.pa_prefill.restype = c_int
@@ -292,6 +297,39 @@ def pa_decode_noalloc(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
                                    _code(k_cache, kv_dtype), _ptr(block_tables), block_tables.shape[1],
                                    _ptr(seq_lens), B, Hq, Hkv, D, bs, NB, float(scale), float(k_scale),
                                    float(v_scale), int(partition_tokens), _ptr(err_flag), _stream(stream)))
+    return out
+
+
+def pa_decode_shared_workspace_size(num_seqs: int, num_groups: int, num_q_heads: int, num_kv_heads: int,
+                                    max_seq_len: int, head_dim: int) -> int:
+    return int(lib().pa_decode_shared_workspace_size(num_seqs, num_groups, num_q_heads, num_kv_heads, max_seq_len, head_dim))
+
+
+def pa_decode_shared(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                     block_tables: torch.Tensor, seq_lens: torch.Tensor, group_start: torch.Tensor,
+                     prefix_lens: torch.Tensor, scale: float, kv_dtype=None, *, workspace: Optional[torch.Tensor] = None,
+                     err_flag: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """pa_decode whose sequences group_start[j] .. group_start[j+1]-1 (int32
+    [groups + 1]) share the blocks of their first prefix_lens[j] tokens (int32
+    [groups]): a prefix's keys are read once for its group."""
+    _dev(out, q, k_cache, v_cache, block_tables, seq_lens, group_start, prefix_lens, workspace, err_flag)
+    B, Hq, D = q.shape
+    NB, bs, Hkv, D2 = _pools(k_cache, v_cache, kv_dtype)
+    if D2 != D or tuple(out.shape) != (B, Hq, D) or out.dtype != q.dtype:
+        raise ValueError("q and out must be [num_seqs, num_q_heads, head_dim] of one dtype, head_dim "
+                         "that of the pools")
+    _tables(block_tables, seq_lens, B)
+    NG = prefix_lens.numel()
+    if prefix_lens.dtype != torch.int32 or group_start.dtype != torch.int32 or group_start.numel() != NG + 1:
+        raise ValueError("group_start must be int32 [num_groups + 1] and prefix_lens int32 [num_groups]")
+    _flag(err_flag)
+    MB = block_tables.shape[1]
+    if workspace is None and B > 0:
+        workspace = _scratch(pa_decode_shared_workspace_size(B, NG, Hq, Hkv, MB * bs, D), q.device, stream)
+    _check(lib().pa_decode_shared(_ptr(out), _ptr(q), _code(q), _ptr(k_cache), _ptr(v_cache), _code(k_cache, kv_dtype),
+                                  _ptr(block_tables), MB, _ptr(seq_lens), _ptr(group_start), _ptr(prefix_lens), B, NG, Hq,
+                                  Hkv, D, bs, NB, float(scale), _ptr(workspace), _nbytes(workspace), _ptr(err_flag),
+                                  _stream(stream)))
     return out
 
 

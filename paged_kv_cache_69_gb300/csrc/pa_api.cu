@@ -196,7 +196,8 @@ static pa_status decode_impl(bool tc, void* out, const void* q, pa_dtype q_dtype
                              const int32_t* seq_lens, int B, int Hq, int Hkv, int D, int bs, int NB,
                              float scale, float k_scale, float v_scale, int partition_tokens,
                              void* workspace, size_t workspace_bytes, int32_t* err_flag, cudaStream_t stream,
-                             const int32_t* q_start = nullptr, int QL = 1, int total_q = 0, const WeightsOut* weights = nullptr) {
+                             const int32_t* q_start = nullptr, int QL = 1, int total_q = 0, const WeightsOut* weights = nullptr,
+                             const Tails* tails = nullptr) {
     const bool mq = q_start != nullptr;
     clear_error();
     if (B < 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || bs <= 0 || NB <= 0 || MB <= 0)
@@ -268,7 +269,8 @@ static pa_status decode_impl(bool tc, void* out, const void* q, pa_dtype q_dtype
     const bool um = mq && !is_fp8(kv_dtype) && QL * (Hq / Hkv) >= 48 && um_rows <= 128 && UH > 0 &&
                     partition_tokens % um_ct == 0;
     const int CT = um ? um_ct : native8 ? 32 : 16;
-    const void* kern = weights ? decode_kernel_weights(kv_dtype, q_dtype, D)
+    const void* kern = tails ? decode_kernel_tail(kv_dtype, D)
+                       : weights ? decode_kernel_weights(kv_dtype, q_dtype, D)
                        : um    ? decode_kernel_mq_um(kv_dtype, q_dtype, D, CT)
                        : mq    ? decode_kernel_mq(kv_dtype, q_dtype, D)
                        : fp8t  ? decode_kernel_fp8t(kv_dtype, q_dtype, D)
@@ -386,6 +388,7 @@ static pa_status decode_impl(bool tc, void* out, const void* q, pa_dtype q_dtype
     if (wst != PA_OK) return wst;
     p.split_list = w.split_list; p.totals = w.totals; p.max_slots = w.max_slots;
     p.part_ml = w.part_ml; p.part_acc = w.part_acc;
+    if (tails) { p.seq_lens = tails->lens; p.tail_blk = tails->blk; p.chunk0 = tails->chunk0; p.unit0 = tails->unit0; }
     if (weights) { p.scores = weights->scores; p.lse = weights->lse; p.chunk0 = weights->chunk0; }
 
     // tensor maps
@@ -471,6 +474,7 @@ static pa_status decode_impl(bool tc, void* out, const void* q, pa_dtype q_dtype
     ce = cudaLaunchKernelExC(&cfg, kern, args);
     if (ce != cudaSuccess) return fail_cuda("decode: main kernel launch", ce);
 
+    if (tails) return launch_shared_merge(p, *tails, q_dtype, stream);
     const pa_status mst = launch_merge(p, q_dtype, split_heads, dev.sms, stream);
     return mst == PA_OK && weights ? launch_weights(p, *weights, stream) : mst;
 }
@@ -483,6 +487,14 @@ pa_status decode_with_weights(const WeightsOut& w, void* out, const void* q, pa_
     return decode_impl(true, out, q, q_dtype, k_cache, v_cache, kv_dtype, block_tables, MB, seq_lens, B, Hq, Hkv, D,
                        bs, NB, scale, k_scale, v_scale, 0, workspace, workspace_bytes, err_flag, stream, nullptr, 1, 0,
                        &w);
+}
+
+pa_status decode_tails(const Tails& t, void* out, const void* q, pa_dtype q_dtype, const void* k_cache,
+                       const void* v_cache, pa_dtype kv_dtype, const int32_t* block_tables, int MB,
+                       const int32_t* seq_lens, int B, int Hq, int Hkv, int D, int bs, int NB, float scale,
+                       void* workspace, size_t workspace_bytes, int32_t* err_flag, cudaStream_t stream) {
+    return decode_impl(true, out, q, q_dtype, k_cache, v_cache, kv_dtype, block_tables, MB, seq_lens, B, Hq, Hkv, D,
+                       bs, NB, scale, 1.f, 1.f, 0, workspace, workspace_bytes, err_flag, stream, nullptr, 1, 0, nullptr, &t);
 }
 
 }  // namespace pa

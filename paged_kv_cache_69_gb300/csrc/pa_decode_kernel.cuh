@@ -113,6 +113,11 @@ struct DecodeParams {
     float* scores;
     float2* lse;              // [B][Hq]
     int* chunk0;              // [B]
+    // the tails of pa_decode_shared (else null): seq_lens are those behind the shared
+    // prefix, the tables' entries start at tail_blk[i]; every segment writes a
+    // partial, and chunk0 and unit0 say where a sequence's are
+    const int32_t* tail_blk;  // [B]
+    int* unit0;               // [B]
 };
 
 // Where the scores of chunk k and head h start.
@@ -302,7 +307,9 @@ __device__ inline void make_plan(const DecodeParams& p, int range, int2* scratch
             const int L = clamp_len(p.seq_lens[i], maxL);
             const int nch = cdiv_i(L, p.ct), nu = n_units(L, p.PC, p.ct);
             if (p.chunk0) p.chunk0[i] = S;
-            if (L == 0) {
+            if (p.unit0) {
+                p.unit0[i] = U;            // the merge of the tails reads every sequence
+            } else if (L == 0) {
                 // no keys: zero outputs for every query row of the sequence
                 int qa, qn;
                 query_rows(p, i, qa, qn);
@@ -383,8 +390,9 @@ struct UmBars {
 };
 
 // WT: also keep the scores and the softmax statistics (pa_decode_weights).
+// TAIL: the tables start behind a prefix and every segment is a partial (pa_decode_shared).
 template <class KV, class QT, int D, bool TC, int CT, bool MQ = false, bool T8 = false, bool UM = false,
-          bool WT = false>
+          bool WT = false, bool TAIL = false>
 struct DecodeKernel {
     using KT = typename KV::T;
     using QE = typename QT::T;
@@ -433,6 +441,11 @@ struct DecodeKernel {
         };
         auto load_win = [&](int seq, int wb, int nblk) -> int {
             const int idx = wb + lane;
+            if constexpr (TAIL) {
+                if (seq >= p.B || idx >= nblk) return -1;
+                const int at = __ldg(p.tail_blk + seq) + idx;
+                return at < p.MB ? __ldg(p.block_tables + static_cast<size_t>(seq) * p.MB + at) : -1;
+            }
             return (seq < p.B && idx < nblk) ? __ldg(p.block_tables + static_cast<size_t>(seq) * p.MB + idx) : -1;
         };
         load_lens(pl.seq);
@@ -540,7 +553,7 @@ struct DecodeKernel {
                 if (k == pl.ce - 1 || j == nch - 1 || part_end) flags |= SEG_END;
                 if (k == pl.ce - 1 && part_end && j + 1 < nch) flags |= GAP;
                 const int nu = n_units(L, p.PC, p.ct);
-                if (nu == 1 && Si >= pl.cs && Si + nch <= pl.ce) flags |= DIRECT;
+                if (!TAIL && nu == 1 && Si >= pl.cs && Si + nch <= pl.ce) flags |= DIRECT;
                 StageDesc d;
                 d.seq = i; d.tok0 = tok0; d.vmask = vmask;
                 d.flags = flags | (static_cast<uint32_t>(qn_i) << QCOUNT_SHIFT);
@@ -2028,11 +2041,11 @@ struct DecodeKernel {
 };
 
 template <class KV, class QT, int D, bool TC, int CT, bool MQ = false, bool T8 = false, bool UM = false,
-          bool WT = false>
+          bool WT = false, bool TAIL = false>
 __global__ void __launch_bounds__(MAX_WARPS * 32, 1)
 pa_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap tk,
                  const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tq) {
-    using K = DecodeKernel<KV, QT, D, TC, CT, MQ, T8, UM, WT>;
+    using K = DecodeKernel<KV, QT, D, TC, CT, MQ, T8, UM, WT, TAIL>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(base + p.bar_off);

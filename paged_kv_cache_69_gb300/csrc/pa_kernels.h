@@ -27,6 +27,15 @@ struct WeightsOut {
     int* chunk0;
 };
 pa_status launch_weights(const DecodeParams& p, const WeightsOut& w, cudaStream_t stream);
+// The tails of pa_decode_shared: a decode call over what lies behind the shared
+// prefixes, whose partials another merge takes.
+struct PromptParams;
+struct Tails {
+    const int32_t *lens, *blk;             // tokens behind the prefix, first table entry
+    int *chunk0, *unit0;
+    const PromptParams* prefix;            // where the prefixes' partials are
+};
+pa_status launch_shared_merge(const DecodeParams& p, const Tails& t, pa_dtype out, cudaStream_t stream);
 // Kernel entry for the given cache dtype, query dtype and head_dim, or null.
 const void* decode_kernel_tc(pa_dtype kv, pa_dtype q, int D);
 const void* decode_kernel_simt(pa_dtype kv, pa_dtype q, int D);
@@ -49,6 +58,11 @@ pa_status decode_with_weights(const WeightsOut& w, void* out, const void* q, pa_
                               const int32_t* seq_lens, int B, int Hq, int Hkv, int D, int bs, int NB, float scale,
                               float k_scale, float v_scale, void* workspace, size_t workspace_bytes,
                               int32_t* err_flag, cudaStream_t stream);
+pa_status decode_tails(const Tails& t, void* out, const void* q, pa_dtype q_dtype, const void* k_cache,
+                       const void* v_cache, pa_dtype kv_dtype, const int32_t* block_tables, int MB,
+                       const int32_t* seq_lens, int B, int Hq, int Hkv, int D, int bs, int NB, float scale,
+                       void* workspace, size_t workspace_bytes, int32_t* err_flag, cudaStream_t stream);
+const void* decode_kernel_tail(pa_dtype kv, int D);
 // The 16-token kernels that keep the scores (f32 caches: CUDA cores), and the
 // merge that keeps (m, l).
 const void* decode_kernel_weights(pa_dtype kv, pa_dtype q, int D);

@@ -16,10 +16,13 @@ namespace pa {
 
 static size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
+// At most so many items per KV head: a sequence of n tokens has 1 + floor((n - 1) / TT).
+static long long prompt_items(int B, int total_q, int TT) { return B + std::max(0, total_q - B) / TT; }
+
 PromptPlan prompt_plan(int B, int total_q, int Hq, int Hkv, int D, int max_keys, bool shared, int sms) {
     PromptPlan pl;
     const long long TT = 2LL * (PT_M / (Hq / Hkv));
-    const long long items = (total_q / TT + B) * Hkv;      // at most
+    const long long items = prompt_items(B, total_q, static_cast<int>(TT)) * Hkv;
     const long long chunks = std::max(1, (max_keys + PT_M - 1) / PT_M);
     pl.splits = static_cast<int>(std::max(1LL, std::min({sms / std::max(1LL, items), chunks, 64LL})));
     if (pl.splits == 1 && !shared) return pl;
@@ -27,6 +30,17 @@ PromptPlan prompt_plan(int B, int total_q, int Hq, int Hkv, int D, int max_keys,
     pl.ml_bytes = up256(pl.slots * 2 * PT_M * sizeof(float2));
     pl.acc_bytes = up256(pl.slots * 2 * PT_M * D * sizeof(float));
     return pl;
+}
+
+// A call cut into `splits` ranges has items * splits <= sms, and no more than
+// items (1 + 1 / TT) + 2 places per KV head (prompt_slot).
+size_t prompt_part_bytes(int B, int total_q, int Hq, int Hkv, int D, int max_keys, bool shared, int sms) {
+    const long long TT = 2LL * (PT_M / (Hq / Hkv)), per_head = total_q / TT + B + 1;
+    const long long chunks = std::max(1, (max_keys + PT_M - 1) / PT_M);
+    const long long most = std::min({static_cast<long long>(std::max(1, sms / Hkv)), chunks, 64LL});
+    long long slots = most > 1 ? std::min(per_head * Hkv * most, sms + sms / TT + 1 + 2 * most * Hkv) : 0;
+    if (shared) slots = std::max(slots, per_head * Hkv);
+    return up256(slots * 2 * PT_M * sizeof(float2)) + up256(slots * 2 * PT_M * D * sizeof(float));
 }
 
 static CUresult encode4(CUtensorMap* m, pa_dtype dt, const void* base, cuuint64_t d1, cuuint64_t d2, cuuint64_t planes,
@@ -86,7 +100,7 @@ pa_status launch_prompt(const PromptCall& c, const PromptPlan& plan, void* parts
     p.splits = plan.splits;
     p.causal = !c.shared;
     p.shared = c.shared;
-    p.min_rows = c.min_rows;
+    p.lens = c.lens; p.tail_lens = c.tail_lens; p.tail_blk = c.tail_blk;
     p.rpb = c.k_start ? PT_M : std::min(c.bs, PT_M);
     if (plan.slots) {
         p.part_ml = static_cast<float2*>(parts);
@@ -106,8 +120,8 @@ pa_status launch_prompt(const PromptCall& c, const PromptPlan& plan, void* parts
         std::snprintf(msg, sizeof msg, "cuTensorMapEncodeTiled failed (CUresult %d)", static_cast<int>(r));
         return bad(c, PA_ERR_CUDA, msg);
     }
-    const long long items = (static_cast<long long>(c.total_q) / (2 * p.tokens) + c.B) * c.Hkv * p.splits;
-    const int grid = static_cast<int>(std::min<long long>(items, dev.sms));
+    const long long items = prompt_items(c.B, c.total_q, 2 * p.tokens) * c.Hkv * p.splits;
+    const int grid = static_cast<int>(std::max(1LL, std::min<long long>(items, dev.sms)));
     cudaError_t e;
     if (c.dtype == PA_F16)
         e = c.D == 128 ? launch<F16T, 128>(p, tq, tk, tv, grid, c.stream) : launch<F16T, 64>(p, tq, tk, tv, grid, c.stream);
@@ -168,8 +182,7 @@ extern "C" size_t pa_prefill_workspace_size(int num_seqs, int total_q, int num_q
     DeviceInfo dev;
     if (!device_info(dev)) return 0;
     // for keys of any number
-    const PromptPlan plan = prompt_plan(num_seqs, total_q, num_q_heads, num_kv_heads, head_dim, 1 << 30, false, dev.sms);
-    return std::max<size_t>(256, plan.ml_bytes + plan.acc_bytes);
+    return std::max<size_t>(256, prompt_part_bytes(num_seqs, total_q, num_q_heads, num_kv_heads, head_dim, 1 << 30, false, dev.sms));
 }
 
 extern "C" pa_status pa_prefill(void* out, const void* q, const void* key, const void* value, pa_dtype dtype,
@@ -178,7 +191,7 @@ extern "C" pa_status pa_prefill(void* out, const void* q, const void* key, const
                                 size_t workspace_bytes, int32_t* err_flag, cudaStream_t stream) {
     clear_error();
     PromptCall c{"prefill", out, q, dtype, key, value, q_start, k_start ? k_start : q_start, nullptr, nullptr, num_seqs,
-                 num_q_heads, num_kv_heads, head_dim, total_q, total_k, PT_M, 1, 1, scale, false, 0, err_flag, stream};
+                 num_q_heads, num_kv_heads, head_dim, total_q, total_k, PT_M, 1, 1, scale, false, nullptr, nullptr, nullptr, err_flag, stream};
     return prefill(c, dtype, workspace, workspace_bytes);
 }
 
@@ -190,7 +203,7 @@ extern "C" pa_status pa_prefill_cached(void* out, const void* q, pa_dtype q_dtyp
                                        cudaStream_t stream) {
     clear_error();
     PromptCall c{"prefill_cached", out, q, q_dtype, k_cache, v_cache, q_start, nullptr, seq_lens, block_tables, num_seqs,
-                 num_q_heads, num_kv_heads, head_dim, total_q, 0, block_size, num_blocks, max_blocks_per_seq, scale, false, 0,
-                 err_flag, stream};
+                 num_q_heads, num_kv_heads, head_dim, total_q, 0, block_size, num_blocks, max_blocks_per_seq, scale, false, nullptr,
+                 nullptr, nullptr, err_flag, stream};
     return prefill(c, kv_dtype, workspace, workspace_bytes);
 }

@@ -18,7 +18,8 @@ struct PromptCall {
     int B, Hq, Hkv, D, total_q, total_k, bs, NB, MB;
     float scale;
     bool shared;                       // q_start: members of groups, seq_lens: prefixes; partials only
-    int min_rows;
+    const int32_t* lens;               // shared: lengths of the sequences
+    int32_t *tail_lens, *tail_blk;     // shared: out
     int32_t* err_flag;
     cudaStream_t stream;
 };
@@ -28,6 +29,8 @@ struct PromptPlan {
     int splits = 1;
     size_t slots = 0, ml_bytes = 0, acc_bytes = 0;         // of the partials (0 without)
 };
+// Partials of any call of at most these numbers (a workspace made once serves smaller calls).
+size_t prompt_part_bytes(int B, int total_q, int Hq, int Hkv, int D, int max_keys, bool shared, int sms);
 PromptPlan prompt_plan(int B, int total_q, int Hq, int Hkv, int D, int max_keys, bool shared, int sms);
 
 // The kernel; partials at `parts` (256-byte aligned, plan's bytes). p_out: the

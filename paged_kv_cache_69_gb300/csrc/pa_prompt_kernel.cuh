@@ -58,7 +58,9 @@ struct PromptParams {
     int total_q, total_k;
     int tokens;                        // query tokens per tile, 128 / G
     int splits, causal, shared;
-    int min_rows;                      // shared mode: a group's prefix of fewer rows is left to the decode kernel
+    // shared mode: lengths of the sequences, and what the decode kernel behind takes
+    const int32_t* lens;               // [total_q]
+    int32_t *tail_lens, *tail_blk;
     int rpb;                           // rows per TMA box of K and V
     float c;                           // |scale| log2(e)
     uint32_t negate;                   // instruction descriptor bit of -Q, for scale < 0
@@ -112,9 +114,14 @@ struct PromptSeq {
     int a, c;                          // level of the first item, items
 };
 
+// Shared mode: a group of fewer (sequence, head) rows than this, or with fewer
+// shared tokens, is left to the decode kernel, prefix and all.
+constexpr int PT_SHARED_ROWS = 8, PT_SHARED_KEYS = 64;
+
+// The tokens of group i's prefix that are attended once: whole blocks.
 __device__ __forceinline__ int shared_prefix(const PromptParams& p, int i, int n) {
     const int P = __ldg(p.seq_lens + i);
-    if (P <= 0 || n * p.G < p.min_rows) return 0;
+    if (P < PT_SHARED_KEYS || n * p.G < PT_SHARED_ROWS) return 0;
     return min(P, p.MB * p.bs) / p.bs * p.bs;
 }
 
@@ -713,6 +720,29 @@ struct PromptKernel {
     }
 };
 
+// The sequence whose query rows hold `row`, or -1.
+__device__ __forceinline__ int prompt_seq_of(const PromptParams& p, int row) {
+    int lo = 0, hi = p.B;                                  // the last i with q_start[i] <= row
+    while (hi - lo > 1) {
+        const int m = (lo + hi) >> 1;
+        if (__ldg(p.q_start + m) <= row) lo = m; else hi = m;
+    }
+    return lo < p.B && __ldg(p.q_start + lo) <= row && row < __ldg(p.q_start + lo + 1) ? lo : -1;
+}
+
+// Shared mode: what each sequence has behind its group's prefix, for the decode
+// kernel; -1 tokens for a sequence whose length does not fit.
+__device__ __forceinline__ void write_tails(const PromptParams& p) {
+    for (int i = blockIdx.x * PT_THREADS + threadIdx.x; i < p.total_q; i += gridDim.x * PT_THREADS) {
+        const int g = prompt_seq_of(p, i);
+        const int P = g >= 0 ? prompt_seq(p, g, false).L : 0;
+        const int L = __ldg(p.lens + i);
+        const bool ok = L >= P && L <= p.MB * p.bs;
+        p.tail_lens[i] = ok ? L - P : -1;
+        p.tail_blk[i] = P / p.bs;
+    }
+}
+
 template <class KV, int D>
 __global__ void __launch_bounds__(PT_THREADS, 1)
 prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ CUtensorMap tq,
@@ -763,6 +793,7 @@ prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ CU
     // it wrote is read before this
     grid_dependency_wait();
     grid_dependents_launch();
+    if (p.shared) write_tails(p);
     if (warp == 9) {
         K::producer(p, base, full, empty, b, items, fix, bad, &tq, &tk, &tv);
     } else if (warp == 8) {
@@ -781,16 +812,6 @@ prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ CU
 // merge of the ranges of keys: out = sum_k 2^(r_k - M) O_k / sum_k 2^(r_k - M) l_k
 // One warp per (query row, head).
 // ---------------------------------------------------------------------------
-// The sequence whose query rows hold `row`, or -1.
-__device__ __forceinline__ int prompt_seq_of(const PromptParams& p, int row) {
-    int lo = 0, hi = p.B;                                  // the last i with q_start[i] <= row
-    while (hi - lo > 1) {
-        const int m = (lo + hi) >> 1;
-        if (__ldg(p.q_start + m) <= row) lo = m; else hi = m;
-    }
-    return lo < p.B && __ldg(p.q_start + lo) <= row && row < __ldg(p.q_start + lo + 1) ? lo : -1;
-}
-
 template <class KV, int D>
 __global__ void __launch_bounds__(256)
 prompt_merge_kernel(const __grid_constant__ PromptParams p) {
