@@ -35,14 +35,20 @@
 
 #include <climits>
 #include <cstdint>
+#include <type_traits>
 
 #include "pa_device.cuh"
 
 namespace pa {
 
 constexpr int PT_M = 128;              // rows of a tile, keys of a chunk
-constexpr int PT_THREADS = 320;        // 2 x 4 softmax warps, the MMA warp, the producer
-constexpr int PT_ITEMS = 2;            // items that the producer may be ahead
+constexpr int PT_THREADS = 384;        // 2 x 4 softmax warps, the MMA warp, the producer, the scheduler, one idle
+constexpr int PT_ITEMS = 4;            // items that the scheduler may be ahead
+constexpr int PT_PARTS = 2;            // parts of P that the second product starts on
+constexpr int PT_KNOWN = 1024;         // sequences whose items' numbers are kept
+// Registers of a softmax thread and of the others (two thirds and one third of the
+// block's 168 each at launch): the softmax holds a row of S.
+constexpr int PT_REGS = 208, PT_REGS_FEW = 88;
 constexpr float PT_SLACK = 8.f;        // log2 that a score may pass the reference by
 
 struct PromptParams {
@@ -72,8 +78,8 @@ struct PromptItem {
     int row0, ntok;                    // first query row, query tokens of both tiles
     int pos0, L;                       // position of the first token, keys of the sequence
     int t0, e[2];                      // chunks [t0, e[q]) of tile q
-    int it0;                           // chunks that the CTA has gone through before
     int h, slot;                       // KV head; partial slot
+    int idx;                           // sequence (or group)
 };
 
 // Non-finite values of V among keys that some row of the tile must not see: the
@@ -84,7 +90,7 @@ struct PromptFix {
 };
 
 struct PromptBars {
-    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2];
+    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][PT_PARTS], o_full[2];
     uint64_t i_full[PT_ITEMS], i_empty[PT_ITEMS];
     uint64_t fin;
     uint32_t tmem;
@@ -101,7 +107,10 @@ struct PromptLayout {
     static constexpr uint32_t ITEM = (BARS + sizeof(PromptBars) + 15) & ~15u;
     static constexpr uint32_t FIX = ITEM + PT_ITEMS * ((sizeof(PromptItem) + 15) & ~15u);
     static constexpr uint32_t BAD = (FIX + PT_ITEMS * sizeof(PromptFix) + 15) & ~15u;   // uint4 per stage
-    static constexpr uint32_t BYTES = BAD + 16 * STAGES + 1024;  // + alignment of the base
+    static constexpr uint32_t STAGE = (BAD + 16 * STAGES + 127) & ~127u;     // 2 KB per softmax warp
+    static constexpr uint32_t KNOWN = STAGE + 8 * 2048;          // (level, items) of the first sequences
+    static constexpr uint32_t BYTES = KNOWN + 8 * PT_KNOWN + 1024;   // + alignment of the base
+    static_assert(BYTES <= 227 * 1024, "shared memory of a CTA");
     static constexpr uint32_t TCOLS = 512;                       // S0, S1, O0, O1
     static constexpr uint32_t OCOL = 256;
 };
@@ -164,47 +173,46 @@ __device__ __forceinline__ int items_from(const PromptParams& p, const PromptSeq
     return p.shared ? (s.a >= u ? s.c : 0) : min(max(s.a + s.c - u, 0), s.c);
 }
 
-__device__ __forceinline__ int warp_sum(int x) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    return x;
-}
-
-// The items of the launch in order of length, for one warp.  The lanes hold the
-// first 32 sequences; more are read again (they are in L1).
+// The items of the launch in order of length, for one warp.
 struct PromptOrder {
-    PromptSeq mine;
+    int2* known;                       // (a, c) of the first PT_KNOWN sequences
     int hi;                            // no item that is still to come lies above this level
     int total;                         // items per KV head
 
     __device__ __forceinline__ PromptSeq seq(const PromptParams& p, int i) const {
-        if (i < 32) return mine;       // lane i asks for sequence i
-        return i < p.B ? prompt_seq(p, i, false) : PromptSeq{0, 0, 0, 0, 0};
+        if (i >= PT_KNOWN) return prompt_seq(p, i, false);
+        const int2 x = known[i];
+        return PromptSeq{0, 0, 0, x.x, x.y};
     }
     __device__ __forceinline__ int count_from(const PromptParams& p, int u) const {
         int x = 0;
         for (int i = threadIdx.x & 31; i < p.B; i += 32) x += items_from(p, seq(p, i), u);
-        return warp_sum(x);
+        return __reduce_add_sync(0xffffffffu, x);
     }
-    __device__ __forceinline__ void init(const PromptParams& p) {
-        const int lane = threadIdx.x & 31;
+    __device__ __forceinline__ void init(const PromptParams& p, int2* smem) {
         const bool report = blockIdx.x == 0;
-        mine = PromptSeq{0, 0, 0, 0, 0};
+        known = smem;
         int top = 0, n = 0;
-        for (int i = lane; i < p.B; i += 32) {
+        for (int i = threadIdx.x & 31; i < p.B; i += 32) {
             const PromptSeq s = prompt_seq(p, i, report);
-            if (i < 32) mine = s;
+            if (i < PT_KNOWN) known[i] = make_int2(s.a, s.c);
             if (s.c > 0) top = max(top, p.shared ? s.a : s.a + s.c - 1);
             n += s.c;
         }
-        total = warp_sum(n);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        hi = top;
+        __syncwarp();
+        total = __reduce_add_sync(0xffffffffu, n);
+        hi = __reduce_max_sync(0xffffffffu, top);
     }
     // Item k (below total): its sequence's index and numbers, its number in the sequence.
     __device__ __forceinline__ void find(const PromptParams& p, int k, int& idx, PromptSeq& s, int& t) {
-        int lo = 0;                    // the largest level that more than k items lie at or above
+        // the largest level that more than k items lie at or above: down from the last
+        // one in growing steps, then between the last two
+        int lo = hi, step = 1;
+        while (lo > 0 && count_from(p, lo) <= k) {
+            hi = lo - 1;
+            lo = max(0, lo - step);
+            step *= 2;
+        }
         while (lo < hi) {
             const int u = (lo + hi + 1) >> 1;
             if (count_from(p, u) > k) lo = u; else hi = u - 1;
@@ -212,30 +220,30 @@ struct PromptOrder {
         int r = k - count_from(p, hi + 1);
         const int lane = threadIdx.x & 31;
         for (int i0 = 0; i0 < p.B; i0 += 32) {
-            const PromptSeq x = i0 + lane < p.B ? seq(p, i0 + lane) : PromptSeq{0, 0, 0, 0, 0};
+            PromptSeq x{0, 0, 0, 0, 0};
+            if (i0 + lane < p.B) x = seq(p, i0 + lane);
             const int own = items_from(p, x, hi) - items_from(p, x, hi + 1);
+            const int all = __reduce_add_sync(0xffffffffu, own);
+            if (r >= all) {
+                r -= all;
+                continue;
+            }
             int inc = own;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int y = __shfl_up_sync(0xffffffffu, inc, o);
                 if (lane >= o) inc += y;
             }
-            const int all = __shfl_sync(0xffffffffu, inc, 31);
-            if (r < all) {
-                const int src = __ffs(__ballot_sync(0xffffffffu, inc > r)) - 1;
-                const int before = __shfl_sync(0xffffffffu, inc - own, src);
-                s.row0 = __shfl_sync(0xffffffffu, x.row0, src);
-                s.n = __shfl_sync(0xffffffffu, x.n, src);
-                s.L = __shfl_sync(0xffffffffu, x.L, src);
-                s.a = __shfl_sync(0xffffffffu, x.a, src);
-                s.c = __shfl_sync(0xffffffffu, x.c, src);
-                idx = i0 + src;
-                t = p.shared ? r - before : hi - s.a;
-                return;
-            }
-            r -= all;
+            const int src = __ffs(__ballot_sync(0xffffffffu, inc > r)) - 1;
+            const int before = __shfl_sync(0xffffffffu, inc - own, src);
+            idx = i0 + src;
+            s = prompt_seq(p, idx, false);
+            t = p.shared ? r - before : hi - s.a;
+            return;
         }
-        idx = -1;                      // not reached: k < total
+        idx = 0;                       // not reached: k < total
+        s = PromptSeq{0, 0, 0, 0, 0};
+        t = 0;
     }
 };
 
@@ -286,6 +294,13 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
         : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
     return d;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+template <int N> __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N)); }
+template <int N> __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N)); }
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     float2 d;
     asm("add.rn.f32x2 %0, %1, %2;"
@@ -315,36 +330,28 @@ struct PromptKernel {
         return false;
     }
 
-    // ---------------- producer ----------------
-    static __device__ void producer(const PromptParams& p, uint8_t* base, uint64_t* full, uint64_t* empty, PromptBars* b,
-                                    PromptItem* items, PromptFix* fix, uint4* bad, const CUtensorMap* tq,
-                                    const CUtensorMap* tk, const CUtensorMap* tv) {
+    // ---------------- scheduler: one warp finds the CTA's items ----------------
+    static __device__ void schedule(const PromptParams& p, PromptBars* b, PromptItem* items, PromptFix* fix, int2* known) {
         const int lane = threadIdx.x & 31;
         PromptOrder order;
-        order.init(p);
+        order.init(p, known);
         const int total = order.total * p.Hkv * p.splits;
         const int TT = 2 * p.tokens;
-        const uint32_t q_bytes = static_cast<uint32_t>(p.tokens * p.G) * 128u * PLANES;
-        const int nb = PT_M / p.rpb;                       // boxes of a chunk and plane
-        int issued = 0, it0 = 0, qload[2] = {0, 0};
-        bool ok = true;
-        int k = blockIdx.x;
-        for (int turn = 0; ok; ++turn) {
+        for (int turn = 0;; ++turn) {
             const int slot = turn % PT_ITEMS;
+            bool ok = true;
             if (turn >= PT_ITEMS) ok = wait(p, &b->i_empty[slot], (turn / PT_ITEMS - 1) & 1u);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
+            if (!__all_sync(0xffffffffu, ok)) return;
             // turns of alternating direction: CTA b takes b, 2 grid - 1 - b, 2 grid + b, ...
-            k = turn * gridDim.x + (turn & 1 ? static_cast<int>(gridDim.x) - 1 - static_cast<int>(blockIdx.x)
-                                             : static_cast<int>(blockIdx.x));
             // (k is below the next turn's first number: behind the last item there are no more turns)
+            const int k = turn * gridDim.x + (turn & 1 ? static_cast<int>(gridDim.x) - 1 - static_cast<int>(blockIdx.x)
+                                                       : static_cast<int>(blockIdx.x));
             PromptItem it{};
-            int idx = 0;
             if (k < total) {
                 const int part = k % p.splits, kh = k / p.splits;
                 PromptSeq s;
                 int t;
-                order.find(p, kh / p.Hkv, idx, s, t);
+                order.find(p, kh / p.Hkv, it.idx, s, t);
                 it.live = 1;
                 it.h = kh % p.Hkv;
                 it.row0 = s.row0 + t * TT;
@@ -363,8 +370,7 @@ struct PromptKernel {
                 const int t1 = static_cast<int>(static_cast<long long>(most) * (part + 1) / p.splits);
                 it.e[0] = max(it.t0, min(e[0], t1));
                 it.e[1] = max(it.t0, min(e[1], t1));
-                it.it0 = it0;
-                it.slot = (prompt_slot(s.row0, idx, t, p.tokens) * p.Hkv + it.h) * p.splits + part;
+                it.slot = (prompt_slot(s.row0, it.idx, t, p.tokens) * p.Hkv + it.h) * p.splits + part;
             }
             if (lane == 0) {
                 items[slot] = it;
@@ -375,14 +381,33 @@ struct PromptKernel {
                 for (int d = lane; d < D; d += 32) fix[slot].first[x][d] = INT_MAX;
             __syncwarp();
             if (lane == 0) mbar_arrive(&b->i_full[slot]);
+            if (!it.live) return;
+        }
+    }
+
+    // ---------------- producer ----------------
+    static __device__ void producer(const PromptParams& p, uint8_t* base, uint64_t* full, uint64_t* empty, PromptBars* b,
+                                    const PromptItem* items, uint4* bad, const CUtensorMap* tq, const CUtensorMap* tk,
+                                    const CUtensorMap* tv) {
+        const int lane = threadIdx.x & 31;
+        const uint32_t q_bytes = static_cast<uint32_t>(p.tokens * p.G) * 128u * PLANES;
+        const int nb = PT_M / p.rpb;                       // boxes of a chunk and plane
+        int issued = 0, qload[2] = {0, 0};
+        bool ok = true;
+        for (int turn = 0; ok; ++turn) {
+            const int is = turn % PT_ITEMS;
+            ok = __all_sync(0xffffffffu, wait(p, &b->i_full[is], (turn / PT_ITEMS) & 1u));
+            if (!ok) break;
+            const PromptItem it = items[is];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&b->i_empty[is]);
             if (!it.live) break;
             // the query rows of each tile that has keys
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                if (it.e[q] <= it.t0) continue;
+            auto queries = [&](int q) {
+                if (it.e[q] <= it.t0) return;
                 if (qload[q] > 0) ok = ok && wait(p, &b->q_empty[q], (qload[q] - 1) & 1u);
                 ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
+                if (!ok) return;
                 ++qload[q];
                 if (lane == 0) {
                     mbar_arrive_expect_tx(&b->q_full[q], q_bytes);
@@ -391,14 +416,13 @@ struct PromptKernel {
                         tma_load_4d(base + Lay::Q + q * Lay::TILE + pl * Lay::PLANE, tq, &b->q_full[q], 0, it.h * p.G,
                                     it.row0 + q * p.tokens, pl);
                 }
-            }
-            if (!ok) break;
+            };
             const int n = max(it.e[0], it.e[1]) - it.t0;
-            it0 += n;
+            if (n == 0) continue;
             const int32_t* table = nullptr;
             int k0 = 0;
-            if (p.k_start) k0 = __ldg(p.k_start + idx);
-            else table = p.block_tables + static_cast<size_t>(p.shared ? __ldg(p.q_start + idx) : idx) * p.MB;
+            if (p.k_start) k0 = __ldg(p.k_start + it.idx);
+            else table = p.block_tables + static_cast<size_t>(p.shared ? __ldg(p.q_start + it.idx) : it.idx) * p.MB;
             const int nblk = (it.L + p.bs - 1) / p.bs;     // paged: blocks that the sequence uses
             // lane x < nb copies box x of each chunk; the next chunk's table entry is read ahead
             auto entry = [&](int t) -> int {               // first pool row of the lane's box in chunk t, or -1
@@ -410,6 +434,9 @@ struct PromptKernel {
             };
             int next = table ? entry(it.t0) : 0;
             for (int j = 0; j < n && ok; ++j) {
+                if (j == 0) queries(0);
+                if (j == 0 && ok) queries(1);
+                if (!ok) break;
                 const int t = it.t0 + j;
                 int row = next;
                 if (table) {
@@ -471,23 +498,35 @@ struct PromptKernel {
         const uint32_t id_o = umma_idesc_f16(BF16, PT_M, D, false, true);
         const uint32_t qb = smem_u32(base + Lay::Q), kvb = smem_u32(base + Lay::KV);
         int used = 0;                                      // stages gone through
-        int qn[2] = {0, 0}, pn[2] = {0, 0};
+        int qn[2] = {0, 0};
+        uint32_t pn[2] = {0, 0};
         bool ok = true;
-        auto score = [&](int q, int st) {                  // S_q = Q_q K^T
+        auto score = [&](int q, int st, bool last) {       // S_q = Q_q K^T
             const uint32_t kb = kvb + st * Lay::TILE, qa = qb + q * Lay::TILE;
+            tc05_fence_after();
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
                 const uint32_t off = static_cast<uint32_t>(kk >> 2) * Lay::PLANE + static_cast<uint32_t>(kk & 3) * 32u;
                 umma_f16(tm + q * PT_M, umma_desc(qa + off, 16u, 1024u, 2u), umma_desc(kb + off, 16u, 1024u, 2u), id_s, kk > 0);
             }
             umma_commit(&b->s_full[q]);
+            if (last) umma_commit(&b->q_empty[q]);
         };
-        auto value = [&](int q, int st, bool first) {      // O_q (+)= P_q V
+        auto value = [&](int q, int st, bool first) {      // O_q (+)= P_q V, as the parts of P come
             const uint32_t vb = kvb + st * Lay::TILE;
+            const uint32_t phase = pn[q]++ & 1u;
 #pragma unroll
-            for (int kk = 0; kk < PT_M / 16; ++kk)
-                umma_f16_ta(tm + Lay::OCOL + q * D, tm + q * PT_M + kk * 8,
-                            umma_desc(vb + kk * 2048u, Lay::PLANE, 1024u, 2u), id_o, !first || kk > 0);
+            for (int part = 0; part < PT_PARTS; ++part) {
+                if (!wait(p, &b->p_full[q][part], phase)) return false;
+                tc05_fence_after();
+#pragma unroll
+                for (int x = 0; x < PT_M / 16 / PT_PARTS; ++x) {
+                    const int kk = part * (PT_M / 16 / PT_PARTS) + x;
+                    umma_f16_ta(tm + Lay::OCOL + q * D, tm + q * PT_M + kk * 8,
+                                umma_desc(vb + kk * 2048u, Lay::PLANE, 1024u, 2u), id_o, !first || kk > 0);
+                }
+            }
+            return true;
         };
         for (int turn = 0; ok; ++turn) {
             const int is = turn % PT_ITEMS;
@@ -497,15 +536,13 @@ struct PromptKernel {
             if (!it.live) break;
             const int n0 = it.e[0] - it.t0, n1 = it.e[1] - it.t0, n = max(n0, n1);
             if (n == 0) continue;
-            // chunk j: K in stage 2 (it0 + j), V in the one behind it
+            // chunk j: K in stage 2 j of the item's, V in the one behind it
             if (!(ok = wait(p, &full[used % S], (used / S) & 1u))) break;
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 if ((q ? n1 : n0) == 0) continue;
                 if (!(ok = wait(p, &b->q_full[q], qn[q]++ & 1u))) break;
-                tc05_fence_after();
-                score(q, used % S);
-                if ((q ? n1 : n0) == 1) umma_commit(&b->q_empty[q]);
+                score(q, used % S, (q ? n1 : n0) == 1);
             }
             if (!ok) break;
             umma_commit(&empty[used % S]);
@@ -517,18 +554,12 @@ struct PromptKernel {
                 for (int q = 0; q < 2; ++q) {
                     const int nq = q ? n1 : n0;
                     if (j < nq) {
-                        if (!(ok = wait(p, &b->p_full[q], pn[q]++ & 1u))) break;
-                        tc05_fence_after();
-                        value(q, vs, j == 0);
+                        if (!(ok = value(q, vs, j == 0))) break;
                         if (j == nq - 1) umma_commit(&b->o_full[q]);
                     }
                     if (q == 1) umma_commit(&empty[vs]);
                     if (q == 0 && j + 1 < n && !(ok = wait(p, &full[ks], ((used + 1) / S) & 1u))) break;
-                    if (j + 1 < nq) {
-                        tc05_fence_after();
-                        score(q, ks);
-                        if (j + 1 == nq - 1) umma_commit(&b->q_empty[q]);
-                    }
+                    if (j + 1 < nq) score(q, ks, j + 1 == nq - 1);
                 }
                 if (!ok) break;
                 if (j + 1 < n) umma_commit(&empty[ks]);
@@ -550,10 +581,7 @@ struct PromptKernel {
         for (int x = r; x < (PT_M - lo) * CH; x += PT_M) {
             const int row = lo + x / CH, ch = x % CH;
             uint4* at = reinterpret_cast<uint4*>(v + (ch >> 3) * Lay::PLANE + swz128(row, ch & 7));
-            if (row >= tail) {
-                *at = make_uint4(0, 0, 0, 0);
-                continue;
-            }
+            if (row >= tail) continue;
             const uint4 raw = *at;
             uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
             constexpr uint32_t EXP = BF16 ? 0x7f80u : 0x7c00u;
@@ -574,6 +602,48 @@ struct PromptKernel {
             }
         }
     }
+    // The zeros, and whether there is anything to mend: 0 * x is NaN for an x that is
+    // not finite.
+    static __device__ __forceinline__ bool unfit_values(uint8_t* v, int r, int lo, int tail) {
+        constexpr int CH = D / 8;
+        using E2 = std::conditional_t<BF16, __nv_bfloat162, __half2>;
+        E2 acc[2];
+        uint32_t zero = 0;
+        acc[0] = acc[1] = *reinterpret_cast<E2*>(&zero);
+        const E2 none = acc[0];
+        for (int x = r; x < (PT_M - lo) * CH; x += PT_M) {
+            const int row = lo + x / CH, ch = x % CH;
+            uint4* at = reinterpret_cast<uint4*>(v + (ch >> 3) * Lay::PLANE + swz128(row, ch & 7));
+            if (row >= tail) {
+                *at = make_uint4(0, 0, 0, 0);
+                continue;
+            }
+            const uint4 raw = *at;
+            const E2* e = reinterpret_cast<const E2*>(&raw);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) acc[y & 1] = __hfma2(e[y], none, acc[y & 1]);
+        }
+        acc[0] = __hadd2(acc[0], acc[1]);
+        return __hisnan(acc[0].x) || __hisnan(acc[0].y);
+    }
+
+    // 64 bytes of each of the warp's 32 rows to 32 places in memory, by way of shared
+    // memory so that four lanes write one row's 64 bytes together.  dst(k): where lane's
+    // row k * 8 + lane / 4 goes, or null.
+    static __device__ __forceinline__ void put_rows(uint8_t* buf, int lane, const uint4 (&x)[4], uint8_t* const (&dst)[4],
+                                                    int off) {
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            *reinterpret_cast<uint4*>(buf + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) = x[c];
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int row = k * 8 + (lane >> 2);
+            const uint4 y = *reinterpret_cast<const uint4*>(buf + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4));
+            if (dst[k]) *reinterpret_cast<uint4*>(dst[k] + off + ((lane & 3) << 4)) = y;
+        }
+    }
 
     static __device__ void softmax(const PromptParams& p, int q, uint8_t* base, uint64_t* full, PromptBars* b,
                                    const PromptItem* items, PromptFix* fix, const uint4* bad) {
@@ -581,9 +651,19 @@ struct PromptKernel {
         const int lane = threadIdx.x & 31;
         const uint32_t lanes = static_cast<uint32_t>(r & ~31) << 16;
         const uint32_t ts = b->tmem + lanes + q * PT_M, to = b->tmem + lanes + Lay::OCOL + q * D;
-        const int tok = r / p.G, head = r - tok * p.G;
+        uint8_t* buf = base + Lay::STAGE + (threadIdx.x >> 5) * 2048;
+        const int tok = r / p.G;
+        // (token, head) of the rows that this lane writes
+        int wtok[4], whead[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int row = (r & ~31) + k * 8 + (lane >> 2);
+            wtok[k] = row / p.G;
+            whead[k] = row - wtok[k] * p.G;
+        }
         const float c = p.c;
         uint32_t sn = 0, on = 0;
+        int vstage = 1;                                    // stage of the item's first V
         for (int turn = 0;; ++turn) {
             const int is = turn % PT_ITEMS;
             if (!__all_sync(0xffffffffu, wait(p, &b->i_full[is], (turn / PT_ITEMS) & 1u))) return;
@@ -591,129 +671,165 @@ struct PromptKernel {
             if (!it.live) return;
             const int t1 = it.e[q];
             const int first = it.pos0 + q * p.tokens;      // position of the tile's first token
-            const bool mine = tok < p.tokens && q * p.tokens + tok < it.ntok;
             const int last = p.causal ? first + tok : it.L - 1;                 // the row's last key
             const int seen = p.causal ? min(first, it.L - 1) : it.L - 1;        // the last key that every row sees
-            float ref = -INFINITY, sum = 0.f;
+            float ref = -INFINITY;
+            float2 sum = make_float2(0.f, 0.f);
             for (int t = it.t0; t < t1; ++t) {
                 if (!__all_sync(0xffffffffu, wait(p, &b->s_full[q], sn++ & 1u))) return;
                 tc05_fence_after();
                 float s[PT_M];
 #pragma unroll
                 for (int x = 0; x < 4; ++x) tmem_ld32(ts + 32 * x, s + 32 * x);
-                const int any_bad = *reinterpret_cast<volatile int*>(&b->any_bad);
+                const int any_bad = p.block_tables ? *reinterpret_cast<volatile int*>(&b->any_bad) : 0;
                 tmem_wait_ld();
-                const int rel = last - t * PT_M;
-                const int vstage = 2 * (it.it0 + t - it.t0) + 1;
+                const int vs = vstage + 2 * (t - it.t0);
                 const bool edge = t * PT_M + PT_M - 1 > seen;
                 if (edge) {
+                    const int rel = last - t * PT_M;
+                    const int least = __reduce_min_sync(0xffffffffu, rel);
 #pragma unroll
-                    for (int x = 0; x < PT_M; ++x) s[x] = x <= rel ? s[x] : -INFINITY;
+                    for (int x = 0; x < PT_M; x += 32) {
+                        if (x + 31 <= least) continue;
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) s[x + y] = x + y <= rel ? s[x + y] : -INFINITY;
+                    }
+                    if (!__all_sync(0xffffffffu, wait(p, &full[vs % S], (vs / S) & 1u))) return;
                 }
-                if (any_bad) {
-                    if (!__all_sync(0xffffffffu, wait(p, &full[vstage % S], (vstage / S) & 1u))) return;
-                    const uint4 m4 = bad[vstage % S];
+                const auto highest = [&]() {
+                    float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                    for (int x = 4; x < PT_M - 4; x += 8) {
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) mx[y] = max3(mx[y], s[x + y], s[x + 4 + y]);
+                    }
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) mx[y] = fmaxf(mx[y], s[PT_M - 4 + y]);
+                    return fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+                };
+                float top = highest();
+                if (any_bad) {                             // keys of blocks outside the pool
+                    if (!__all_sync(0xffffffffu, wait(p, &full[vs % S], (vs / S) & 1u))) return;
+                    const uint4 m4 = bad[vs % S];
                     const uint32_t w[4] = {m4.x, m4.y, m4.z, m4.w};
 #pragma unroll
                     for (int x = 0; x < PT_M; ++x)
                         if ((w[x >> 5] >> (x & 31)) & 1u) s[x] = -INFINITY;
+                    top = highest();
                 }
-                float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-                for (int x = 4; x < PT_M; x += 4) {
-                    mx[0] = fmaxf(mx[0], s[x]);
-                    mx[1] = fmaxf(mx[1], s[x + 1]);
-                    mx[2] = fmaxf(mx[2], s[x + 2]);
-                    mx[3] = fmaxf(mx[3], s[x + 3]);
-                }
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 // the reference moves at the row's first key and when it is passed by 2^8
                 const bool move = top * c > ref + (PT_SLACK + LIFT) && top > -INFINITY;
                 if (__any_sync(0xffffffffu, move)) {
                     const float to_ref = move ? top * c - LIFT : ref;
                     const float f = move ? exp2f(ref - to_ref) : 1.f;
                     ref = to_ref;
-                    sum *= f;
+                    sum.x *= f;
+                    sum.y *= f;
                     if (t > it.t0) {
 #pragma unroll
-                        for (int x = 0; x < D; x += 32) {
-                            float o[32];
-                            tmem_ld32(to + x, o);
+                        for (int x = 0; x < D; x += 16) {
+                            float o[16];
+                            tmem_ld16(to + x, o);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int y = 0; y < 32; ++y) o[y] *= f;
-                            tmem_st16(to + x, *reinterpret_cast<float(*)[16]>(o));
-                            tmem_st16(to + x + 16, *reinterpret_cast<float(*)[16]>(o + 16));
+                            for (int y = 0; y < 16; ++y) o[y] *= f;
+                            tmem_st16(to + x, o);
                         }
                     }
                 }
-                const float neg = ref > -INFINITY ? -ref : 0.f;
-                float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-                for (int x = 0; x < PT_M; x += 32) {
-                    uint32_t w[16];
-#pragma unroll
-                    for (int y = 0; y < 32; y += 2) {
-                        float2 e = fma2(make_float2(s[x + y], s[x + y + 1]), make_float2(c, c), make_float2(neg, neg));
-                        e.x = ex2_approx(e.x);
-                        e.y = ex2_approx(e.y);
-                        acc[(y >> 1) & 1] = add2(acc[(y >> 1) & 1], e);
-                        w[y >> 1] = pack2(e.x, e.y, BF16);
-                    }
-                    tmem_st16u(ts + x / 2, w);
-                }
-                acc[0] = add2(acc[0], acc[1]);
-                sum += acc[0].x + acc[0].y;
                 if (edge) {
-                    if (!__all_sync(0xffffffffu, wait(p, &full[vstage % S], (vstage / S) & 1u))) return;
-                    const int lo = max(0, seen + 1 - t * PT_M);
-                    mend_values(base + Lay::KV + (vstage % S) * Lay::TILE, fix + is, r, lo, it.L - t * PT_M, t * PT_M);
+                    uint8_t* v = base + Lay::KV + (vs % S) * Lay::TILE;
+                    const int lo = max(0, seen + 1 - t * PT_M), tail = it.L - t * PT_M;
+                    if (unfit_values(v, r, lo, tail)) mend_values(v, fix + is, r, lo, tail, t * PT_M);
                     fence_proxy_async_smem();
                 }
-                tmem_wait_st();
-                tc05_fence_before();
-                mbar_arrive(&b->p_full[q]);
+                const float neg = ref > -INFINITY ? -ref : 0.f;
+                const float2 c2 = make_float2(c, c), n2 = make_float2(neg, neg);
+                float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int part = 0; part < PT_PARTS; ++part) {
+                    constexpr int W = PT_M / PT_PARTS;
+#pragma unroll
+                    for (int x = part * W; x < (part + 1) * W; x += 32) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int y = 0; y < 32; y += 2) {
+                            float2 e = fma2(make_float2(s[x + y], s[x + y + 1]), c2, n2);
+                            e.x = ex2_approx(e.x);
+                            e.y = ex2_approx(e.y);
+                            if (y & 2) acc = add2(acc, e); else sum = add2(sum, e);
+                            w[y >> 1] = pack2(e.x, e.y, BF16);
+                        }
+                        tmem_st16u(ts + x / 2, w);
+                    }
+                    tmem_wait_st();
+                    tc05_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&b->p_full[q][part]);
+                }
+                sum = add2(sum, acc);
             }
+            vstage += 2 * (max(it.e[0], it.e[1]) - it.t0);
             // ---- the tile's rows ----
-            float o[D];
-            if (t1 > it.t0) {
+            const float total = sum.x + sum.y;
+            const bool direct = p.splits == 1 && !p.shared;
+            const float inv = !direct ? 1.f : total != 0.f ? 1.f / total : 0.f;
+            const bool any = t1 > it.t0;
+            const size_t part0 = (static_cast<size_t>(it.slot) * 2 + q) * PT_M;
+            uint8_t* dst[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const bool in = wtok[k] < p.tokens && q * p.tokens + wtok[k] < it.ntok;
+                const size_t row = static_cast<size_t>(it.row0 + q * p.tokens + wtok[k]) * p.Hq + it.h * p.G + whead[k];
+                dst[k] = !in ? nullptr
+                         : direct ? static_cast<uint8_t*>(p.out) + row * D * 2
+                         : any ? reinterpret_cast<uint8_t*>(p.part_acc + (part0 + (r & ~31) + k * 8 + (lane >> 2)) * D) : nullptr;
+            }
+            if (!direct && tok < p.tokens && q * p.tokens + tok < it.ntok) p.part_ml[part0 + r] = make_float2(ref, total);
+            bool fixed = false;
+            if (any) {
                 if (!__all_sync(0xffffffffu, wait(p, &b->o_full[q], on++ & 1u))) return;
                 tc05_fence_after();
+                fixed = *reinterpret_cast<volatile int*>(&fix[is].any);
+                __threadfence_block();
+            }
 #pragma unroll
-                for (int x = 0; x < D; x += 32) tmem_ld32(to + x, o + x);
-                tmem_wait_ld();
-                tc05_fence_before();
-                if (*reinterpret_cast<volatile int*>(&fix[is].any)) {
-                    __threadfence_block();
+            for (int x = 0; x < D; x += 32) {
+                float o[32];
+                if (any) {
+                    tmem_ld32(to + x, o);
+                    tmem_wait_ld();
+                    if (fixed) {
 #pragma unroll
-                    for (int d = 0; d < D; ++d) {
-                        if (last >= fix[is].first[0][d]) o[d] = NAN;
-                        if (last >= fix[is].first[1][d]) o[d] += INFINITY;
-                        if (last >= fix[is].first[2][d]) o[d] -= INFINITY;
+                        for (int d = 0; d < 32; ++d) {
+                            if (last >= fix[is].first[0][x + d]) o[d] = NAN;
+                            if (last >= fix[is].first[1][x + d]) o[d] += INFINITY;
+                            if (last >= fix[is].first[2][x + d]) o[d] -= INFINITY;
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int d = 0; d < 32; ++d) o[d] = 0.f;
+                }
+                uint4 w[4];
+                if (direct) {
+#pragma unroll
+                    for (int d = 0; d < 4; ++d)
+                        w[d] = make_uint4(pack2(o[8 * d] * inv, o[8 * d + 1] * inv, BF16), pack2(o[8 * d + 2] * inv, o[8 * d + 3] * inv, BF16),
+                                          pack2(o[8 * d + 4] * inv, o[8 * d + 5] * inv, BF16), pack2(o[8 * d + 6] * inv, o[8 * d + 7] * inv, BF16));
+                    put_rows(buf, lane, w, dst, x * 2);
+                } else {
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+#pragma unroll
+                        for (int d = 0; d < 4; ++d)
+                            w[d] = make_uint4(__float_as_uint(o[16 * y + 4 * d]), __float_as_uint(o[16 * y + 4 * d + 1]),
+                                              __float_as_uint(o[16 * y + 4 * d + 2]), __float_as_uint(o[16 * y + 4 * d + 3]));
+                        put_rows(buf, lane, w, dst, (x + 16 * y) * 4);
                     }
                 }
-            } else {
-#pragma unroll
-                for (int d = 0; d < D; ++d) o[d] = 0.f;
             }
-            if (mine && p.splits == 1 && !p.shared) {
-                const float inv = sum != 0.f ? 1.f / sum : 0.f;
-                uint4* dst = reinterpret_cast<uint4*>(
-                    static_cast<E*>(p.out) +
-                    (static_cast<size_t>(it.row0 + q * p.tokens + tok) * p.Hq + it.h * p.G + head) * D);
-#pragma unroll
-                for (int d = 0; d < D; d += 8)
-                    dst[d / 8] = make_uint4(pack2(o[d] * inv, o[d + 1] * inv, BF16), pack2(o[d + 2] * inv, o[d + 3] * inv, BF16),
-                                            pack2(o[d + 4] * inv, o[d + 5] * inv, BF16), pack2(o[d + 6] * inv, o[d + 7] * inv, BF16));
-            } else if (mine) {
-                const size_t at = (static_cast<size_t>(it.slot) * 2 + q) * PT_M + r;
-                p.part_ml[at] = make_float2(ref, sum);
-                if (sum != 0.f) {
-                    float4* dst = reinterpret_cast<float4*>(p.part_acc + at * D);
-#pragma unroll
-                    for (int d = 0; d < D; d += 4) dst[d / 4] = make_float4(o[d], o[d + 1], o[d + 2], o[d + 3]);
-                }
-            }
+            tc05_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&b->i_empty[is]);
         }
@@ -767,12 +883,12 @@ prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ CU
             mbar_init(&b->q_full[q], 1);
             mbar_init(&b->q_empty[q], 1);
             mbar_init(&b->s_full[q], 1);
-            mbar_init(&b->p_full[q], PT_M);
+            for (int x = 0; x < PT_PARTS; ++x) mbar_init(&b->p_full[q][x], 4);
             mbar_init(&b->o_full[q], 1);
         }
         for (int s = 0; s < PT_ITEMS; ++s) {
             mbar_init(&b->i_full[s], 1);
-            mbar_init(&b->i_empty[s], 9);                  // 8 softmax warps, the MMA thread
+            mbar_init(&b->i_empty[s], 10);                 // 8 softmax warps, the MMA thread, the producer
         }
         mbar_init(&b->fin, 1);
         b->any_bad = 0;
@@ -794,11 +910,17 @@ prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ CU
     grid_dependency_wait();
     grid_dependents_launch();
     if (p.shared) write_tails(p);
-    if (warp == 9) {
-        K::producer(p, base, full, empty, b, items, fix, bad, &tq, &tk, &tv);
-    } else if (warp == 8) {
-        if (lane == 0) K::mma(p, base, full, empty, b, items);
+    if (warp >= 8) {
+        regs_down<PT_REGS_FEW>();
+        if (warp == 8) {
+            if (elect_one()) K::mma(p, base, full, empty, b, items);
+        } else if (warp == 9) {
+            K::producer(p, base, full, empty, b, items, bad, &tq, &tk, &tv);
+        } else if (warp == 10) {
+            K::schedule(p, b, items, fix, reinterpret_cast<int2*>(base + Lay::KNOWN));
+        }
     } else {
+        regs_up<PT_REGS>();
         K::softmax(p, warp >> 2, base, full, b, items, fix, bad);
     }
     tc05_fence_before();
