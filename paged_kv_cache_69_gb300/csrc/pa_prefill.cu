@@ -14,33 +14,48 @@
 
 namespace pa {
 
+// Prefills of more rounds of items than this are not cut: their last, lightest round
+// is at most a tenth of the whole.
+constexpr int PT_ROUNDS = 8;
+
 static size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // At most so many items per KV head: a sequence of n tokens has 1 + floor((n - 1) / TT).
 static long long prompt_items(int B, int total_q, int TT) { return B + std::max(0, total_q - B) / TT; }
 
+// Partials of a call: a prefill cuts fewer items than it has CTAs, into at most 2
+// ranges per CTA in all; in shared mode every item has one, places being counted
+// as prompt_slot does.
+static size_t prompt_slots(int B, int total_q, int TT, int Hkv, bool shared, int sms) {
+    if (!shared) return 2 * static_cast<size_t>(sms);
+    return 2 * static_cast<size_t>(sms) + static_cast<size_t>(total_q / TT + B + 1) * Hkv;
+}
+
 PromptPlan prompt_plan(int B, int total_q, int Hq, int Hkv, int D, int max_keys, bool shared, int sms) {
     PromptPlan pl;
-    const long long TT = 2LL * (PT_M / (Hq / Hkv));
-    const long long items = prompt_items(B, total_q, static_cast<int>(TT)) * Hkv;
-    const long long chunks = std::max(1, (max_keys + PT_M - 1) / PT_M);
-    pl.splits = static_cast<int>(std::max(1LL, std::min({sms / std::max(1LL, items), chunks, 64LL})));
-    if (pl.splits == 1 && !shared) return pl;
-    pl.slots = static_cast<size_t>(total_q / TT + B + 1) * Hkv * pl.splits;
-    pl.ml_bytes = up256(pl.slots * 2 * PT_M * sizeof(float2));
-    pl.acc_bytes = up256(pl.slots * 2 * PT_M * D * sizeof(float));
+    const int TT = 2 * (PT_M / (Hq / Hkv));
+    const long long items = prompt_items(B, total_q, TT) * Hkv;
+    const int chunks = std::max(1, (max_keys + PT_M - 1) / PT_M);
+    if (shared) {
+        const long long places = static_cast<long long>(total_q / TT + B + 1) * Hkv;
+        pl.splits = static_cast<int>(std::min<long long>({1 + 2 * sms / places, chunks, 32}));
+    } else if (items <= PT_ROUNDS * static_cast<long long>(sms)) {
+        pl.splits = std::min(chunks, 32);
+    }
+    pl.grid = static_cast<int>(std::max(1LL, std::min<long long>(items * pl.splits, sms)));
+    if (pl.splits > 1 || shared) {
+        const size_t slots = prompt_slots(B, total_q, TT, Hkv, shared, sms);
+        pl.cut_bytes = up256((1 + static_cast<size_t>(sms)) * sizeof(int4));
+        pl.ml_bytes = up256(slots * 2 * PT_M * sizeof(float2));
+        pl.acc_bytes = up256(slots * 2 * PT_M * D * sizeof(float));
+    }
     return pl;
 }
 
-// A call cut into `splits` ranges has items * splits <= sms, and no more than
-// items (1 + 1 / TT) + 2 places per KV head (prompt_slot).
-size_t prompt_part_bytes(int B, int total_q, int Hq, int Hkv, int D, int max_keys, bool shared, int sms) {
-    const long long TT = 2LL * (PT_M / (Hq / Hkv)), per_head = total_q / TT + B + 1;
-    const long long chunks = std::max(1, (max_keys + PT_M - 1) / PT_M);
-    const long long most = std::min({static_cast<long long>(std::max(1, sms / Hkv)), chunks, 64LL});
-    long long slots = most > 1 ? std::min(per_head * Hkv * most, sms + sms / TT + 1 + 2 * most * Hkv) : 0;
-    if (shared) slots = std::max(slots, per_head * Hkv);
-    return up256(slots * 2 * PT_M * sizeof(float2)) + up256(slots * 2 * PT_M * D * sizeof(float));
+size_t prompt_part_bytes(int B, int total_q, int Hq, int Hkv, int D, bool shared, int sms) {
+    const size_t slots = prompt_slots(B, total_q, 2 * (PT_M / (Hq / Hkv)), Hkv, shared, sms);
+    return up256((1 + static_cast<size_t>(sms)) * sizeof(int4)) + up256(slots * 2 * PT_M * sizeof(float2)) +
+           up256(slots * 2 * PT_M * D * sizeof(float));
 }
 
 static CUresult encode4(CUtensorMap* m, pa_dtype dt, const void* base, cuuint64_t d1, cuuint64_t d2, cuuint64_t planes,
@@ -54,17 +69,29 @@ static CUresult encode4(CUtensorMap* m, pa_dtype dt, const void* base, cuuint64_
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
-template <class KV, int D>
+// Pool rows by groups of eight: a box holds [group][plane][row][128 bytes].
+static CUresult encode_pool(CUtensorMap* m, pa_dtype dt, const void* base, cuuint64_t rows, cuuint64_t Hkv, int D, int rpb) {
+    const EncodeTiledFn enc = encode_fn();
+    if (!enc) return CUDA_ERROR_NOT_FOUND;
+    const cuuint64_t planes = D / 64, row = Hkv * D * 2;
+    const cuuint64_t dims[5] = {64, 8, planes, rows / 8, Hkv};
+    const cuuint64_t strides[4] = {row, 128, 8 * row, static_cast<cuuint64_t>(D) * 2};
+    const cuuint32_t box[5] = {64, 8, static_cast<cuuint32_t>(planes), static_cast<cuuint32_t>(rpb / 8), 1}, es[5] = {1, 1, 1, 1, 1};
+    return enc(m, tmap_type(dt), 5, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
+template <class KV, int D, bool PAGED>
 static cudaError_t launch(const PromptParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                          int grid, cudaStream_t stream) {
-    const void* kern = reinterpret_cast<const void*>(&prompt_kernel<KV, D>);
+                          cudaStream_t stream) {
+    const void* kern = reinterpret_cast<const void*>(&prompt_kernel<KV, D, PAGED>);
     cudaError_t e = allow_shared(kern, PromptLayout<D>::BYTES);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.gridDim = dim3(static_cast<unsigned>(p.grid));
     cfg.blockDim = dim3(PT_THREADS);
     cfg.dynamicSmemBytes = PromptLayout<D>::BYTES;
     cfg.stream = stream;
@@ -73,9 +100,8 @@ static cudaError_t launch(const PromptParams& p, const CUtensorMap& tq, const CU
     void* args[] = {const_cast<PromptParams*>(&p), const_cast<CUtensorMap*>(&tq), const_cast<CUtensorMap*>(&tk),
                     const_cast<CUtensorMap*>(&tv)};
     if ((e = cudaLaunchKernelExC(&cfg, kern, args)) != cudaSuccess || p.splits == 1 || p.shared) return e;
-    const long long warps = static_cast<long long>(p.total_q) * p.Hq;
-    cfg.gridDim = dim3(static_cast<unsigned>((warps + 7) / 8));
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3(static_cast<unsigned>(p.grid * (2 * PT_M / PT_MERGE_ROWS)));
+    cfg.blockDim = dim3(32 * PT_MERGE_WARPS);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(&prompt_merge_kernel<KV, D>), args);
 }
@@ -98,35 +124,40 @@ pa_status launch_prompt(const PromptCall& c, const PromptPlan& plan, void* parts
     p.total_q = c.total_q; p.total_k = c.total_k;
     p.tokens = PT_M / G;
     p.splits = plan.splits;
+    p.grid = plan.grid;
     p.causal = !c.shared;
     p.shared = c.shared;
     p.lens = c.lens; p.tail_lens = c.tail_lens; p.tail_blk = c.tail_blk;
     p.rpb = c.k_start ? PT_M : std::min(c.bs, PT_M);
-    if (plan.slots) {
-        p.part_ml = static_cast<float2*>(parts);
-        p.part_acc = reinterpret_cast<float*>(static_cast<uint8_t*>(parts) + plan.ml_bytes);
+    while ((1 << p.bs_log2) < c.bs) ++p.bs_log2;           // block sizes are powers of two
+    while ((1 << p.rpb_log2) < p.rpb) ++p.rpb_log2;
+    if (plan.acc_bytes) {
+        uint8_t* at = static_cast<uint8_t*>(parts);
+        p.cut = reinterpret_cast<int4*>(at);
+        p.part_ml = reinterpret_cast<float2*>(at + plan.cut_bytes);
+        p.part_acc = reinterpret_cast<float*>(at + plan.cut_bytes + plan.ml_bytes);
     }
     // scale enters as a positive factor of the scores' exponent; its sign goes into the MMA
     p.c = std::max(std::fabs(c.scale) * 1.4426950408889634f, 1.17549435e-38f);
     p.negate = c.scale < 0.f ? 1u << 13 : 0u;
     const cuuint64_t D2 = static_cast<cuuint64_t>(c.D) * 2, planes = c.D / 64;
-    const cuuint64_t rows = c.k_start ? std::max(c.total_k, 1) : static_cast<cuuint64_t>(c.NB) * c.bs;
     alignas(64) CUtensorMap tq, tk, tv;
     CUresult r = encode4(&tq, c.dtype, c.q, c.Hq, c.total_q, planes, D2, D2 * c.Hq, G, p.tokens);
-    if (r == CUDA_SUCCESS) r = encode4(&tk, c.dtype, c.k, rows, c.Hkv, planes, D2 * c.Hkv, D2, p.rpb, 1);
-    if (r == CUDA_SUCCESS) r = encode4(&tv, c.dtype, c.v, rows, c.Hkv, planes, D2 * c.Hkv, D2, p.rpb, 1);
+    const void* src[2] = {c.k, c.v};
+    CUtensorMap* map[2] = {&tk, &tv};
+    for (int x = 0; x < 2 && r == CUDA_SUCCESS; ++x)
+        r = c.k_start ? encode4(map[x], c.dtype, src[x], std::max(c.total_k, 1), c.Hkv, planes, D2 * c.Hkv, D2, PT_M, 1)
+                      : encode_pool(map[x], c.dtype, src[x], static_cast<cuuint64_t>(c.NB) * c.bs, c.Hkv, c.D, p.rpb);
     if (r != CUDA_SUCCESS) {
         char msg[96];
         std::snprintf(msg, sizeof msg, "cuTensorMapEncodeTiled failed (CUresult %d)", static_cast<int>(r));
         return bad(c, PA_ERR_CUDA, msg);
     }
-    const long long items = prompt_items(c.B, c.total_q, 2 * p.tokens) * c.Hkv * p.splits;
-    const int grid = static_cast<int>(std::max(1LL, std::min<long long>(items, dev.sms)));
     cudaError_t e;
-    if (c.dtype == PA_F16)
-        e = c.D == 128 ? launch<F16T, 128>(p, tq, tk, tv, grid, c.stream) : launch<F16T, 64>(p, tq, tk, tv, grid, c.stream);
-    else
-        e = c.D == 128 ? launch<BF16T, 128>(p, tq, tk, tv, grid, c.stream) : launch<BF16T, 64>(p, tq, tk, tv, grid, c.stream);
+#define PA_PROMPT(KVT, DD) (c.k_start ? launch<KVT, DD, false>(p, tq, tk, tv, c.stream) : launch<KVT, DD, true>(p, tq, tk, tv, c.stream))
+    if (c.dtype == PA_F16) e = c.D == 128 ? PA_PROMPT(F16T, 128) : PA_PROMPT(F16T, 64);
+    else e = c.D == 128 ? PA_PROMPT(BF16T, 128) : PA_PROMPT(BF16T, 64);
+#undef PA_PROMPT
     if (p_out) *p_out = p;
     if (e != cudaSuccess) {
         char msg[96];
@@ -161,9 +192,9 @@ static pa_status prefill(const PromptCall& c, pa_dtype kv_dtype, void* workspace
     if (!device_info(dev)) return bad(c, PA_ERR_CUDA, "cannot query the current device");
     const int max_keys = c.k_start ? c.total_k : c.MB * c.bs;
     const PromptPlan plan = prompt_plan(c.B, c.total_q, c.Hq, c.Hkv, c.D, max_keys, false, dev.sms);
-    if (plan.slots) {
+    if (plan.acc_bytes) {
         if (!workspace) return bad(c, PA_ERR_WORKSPACE, "workspace pointer is null");
-        if (workspace_bytes < plan.ml_bytes + plan.acc_bytes)
+        if (workspace_bytes < plan.bytes())
             return bad(c, PA_ERR_WORKSPACE, "workspace smaller than pa_prefill_workspace_size()");
         if (reinterpret_cast<uintptr_t>(workspace) & 255u)
             return bad(c, PA_ERR_WORKSPACE, "workspace must be 256-byte aligned");
@@ -181,8 +212,7 @@ extern "C" size_t pa_prefill_workspace_size(int num_seqs, int total_q, int num_q
         return 0;
     DeviceInfo dev;
     if (!device_info(dev)) return 0;
-    // for keys of any number
-    return std::max<size_t>(256, prompt_part_bytes(num_seqs, total_q, num_q_heads, num_kv_heads, head_dim, 1 << 30, false, dev.sms));
+    return prompt_part_bytes(num_seqs, total_q, num_q_heads, num_kv_heads, head_dim, false, dev.sms);
 }
 
 extern "C" pa_status pa_prefill(void* out, const void* q, const void* key, const void* value, pa_dtype dtype,

@@ -24,14 +24,15 @@ struct PromptCall {
     cudaStream_t stream;
 };
 
-// How a call is cut: ranges of keys per item and the places of partials.
+// How a call may be cut: the most ranges of keys per item and the partials' room.
 struct PromptPlan {
-    int splits = 1;
-    size_t slots = 0, ml_bytes = 0, acc_bytes = 0;         // of the partials (0 without)
+    int grid = 1, splits = 1;
+    size_t cut_bytes = 0, ml_bytes = 0, acc_bytes = 0;     // 0 without partials
+    size_t bytes() const { return cut_bytes + ml_bytes + acc_bytes; }
 };
-// Partials of any call of at most these numbers (a workspace made once serves smaller calls).
-size_t prompt_part_bytes(int B, int total_q, int Hq, int Hkv, int D, int max_keys, bool shared, int sms);
 PromptPlan prompt_plan(int B, int total_q, int Hq, int Hkv, int D, int max_keys, bool shared, int sms);
+// Room for any call of at most these numbers (a workspace made once serves smaller calls).
+size_t prompt_part_bytes(int B, int total_q, int Hq, int Hkv, int D, bool shared, int sms);
 
 // The kernel; partials at `parts` (256-byte aligned, plan's bytes). p_out: the
 // kernel's parameters for a merge.

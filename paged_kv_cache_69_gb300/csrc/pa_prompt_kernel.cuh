@@ -42,13 +42,15 @@
 namespace pa {
 
 constexpr int PT_M = 128;              // rows of a tile, keys of a chunk
-constexpr int PT_THREADS = 384;        // 2 x 4 softmax warps, the MMA warp, the producer, the scheduler, one idle
+constexpr int PT_THREADS = 512;        // 2 x 4 softmax warps, MMA, producer, scheduler, mender, 4 that write out
 constexpr int PT_ITEMS = 4;            // items that the scheduler may be ahead
 constexpr int PT_PARTS = 2;            // parts of P that the second product starts on
+constexpr int PT_BAD = 8;              // chunks whose masks of bad blocks are kept: more than are under way
 constexpr int PT_KNOWN = 1024;         // sequences whose items' numbers are kept
-// Registers of a softmax thread and of the others (two thirds and one third of the
-// block's 168 each at launch): the softmax holds a row of S.
-constexpr int PT_REGS = 208, PT_REGS_FEW = 88;
+// Registers of a softmax thread, which holds a row of S, and of the others, out of
+// the block's 128 each at launch.
+constexpr int PT_REGS = 192, PT_REGS_FEW = 64;
+static_assert(2 * PT_REGS + 2 * PT_REGS_FEW <= 4 * 128, "registers of the block");
 constexpr float PT_SLACK = 8.f;        // log2 that a score may pass the reference by
 
 struct PromptParams {
@@ -58,16 +60,19 @@ struct PromptParams {
     const int32_t* seq_lens;           // [B] keys, paged; shared mode: prefix lengths
     const int32_t* block_tables;       // paged: [rows][MB]
     int32_t* err_flag;
-    float* part_acc;                   // [slot][2][128][D] with splits > 1
+    float* part_acc;                   // [slot][2][128][D]
     float2* part_ml;                   // [slot][2][128] (reference in log2 units, l)
     int B, Hq, Hkv, G, bs, NB, MB;
     int total_q, total_k;
     int tokens;                        // query tokens per tile, 128 / G
-    int splits, causal, shared;
+    int splits, causal, shared;        // splits: the most ranges that an item may be cut into
+    int grid;                          // CTAs
+    int4* cut;                         // for the merge: (ranges, cut items), and each one's (first row, tokens, head, place)
     // shared mode: lengths of the sequences, and what the decode kernel behind takes
     const int32_t* lens;               // [total_q]
     int32_t *tail_lens, *tail_blk;
     int rpb;                           // rows per TMA box of K and V
+    int bs_log2, rpb_log2;
     float c;                           // |scale| log2(e)
     uint32_t negate;                   // instruction descriptor bit of -Q, for scale < 0
 };
@@ -78,7 +83,8 @@ struct PromptItem {
     int row0, ntok;                    // first query row, query tokens of both tiles
     int pos0, L;                       // position of the first token, keys of the sequence
     int t0, e[2];                      // chunks [t0, e[q]) of tile q
-    int h, slot;                       // KV head; partial slot
+    int h, slot;                       // KV head; partial slot, -1: rows of out
+    int edge;                          // first chunk with keys that some row must not see
     int idx;                           // sequence (or group)
 };
 
@@ -90,11 +96,14 @@ struct PromptFix {
 };
 
 struct PromptBars {
-    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][PT_PARTS], o_full[2];
+    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][PT_PARTS], o_full[2], o_empty[2];
+    uint64_t l_full[PT_ITEMS][2];      // (reference, l) of an item's tile
+    uint64_t v_there, v_fit;           // an edge chunk's V has come, is mended; the edge chunks in turn
     uint64_t i_full[PT_ITEMS], i_empty[PT_ITEMS];
     uint64_t fin;
     uint32_t tmem;
     int any_bad;                       // a block id outside the pool was met
+    alignas(16) int box[16];           // first groups of pool rows of a chunk's boxes
 };
 
 template <int D>
@@ -106,9 +115,9 @@ struct PromptLayout {
     static constexpr uint32_t FULL = END, EMPTY = FULL + 8 * STAGES, BARS = EMPTY + 8 * STAGES;
     static constexpr uint32_t ITEM = (BARS + sizeof(PromptBars) + 15) & ~15u;
     static constexpr uint32_t FIX = ITEM + PT_ITEMS * ((sizeof(PromptItem) + 15) & ~15u);
-    static constexpr uint32_t BAD = (FIX + PT_ITEMS * sizeof(PromptFix) + 15) & ~15u;   // uint4 per stage
-    static constexpr uint32_t STAGE = (BAD + 16 * STAGES + 127) & ~127u;     // 2 KB per softmax warp
-    static constexpr uint32_t KNOWN = STAGE + 8 * 2048;          // (level, items) of the first sequences
+    static constexpr uint32_t BAD = (FIX + PT_ITEMS * sizeof(PromptFix) + 15) & ~15u;   // a uint4 each
+    static constexpr uint32_t ROWS = (BAD + 16 * PT_BAD + 15) & ~15u;        // (reference, l) of each item's rows
+    static constexpr uint32_t KNOWN = ROWS + PT_ITEMS * 2 * PT_M * 8;       // (level, items) of the first sequences
     static constexpr uint32_t BYTES = KNOWN + 8 * PT_KNOWN + 1024;   // + alignment of the base
     static_assert(BYTES <= 227 * 1024, "shared memory of a CTA");
     static constexpr uint32_t TCOLS = 512;                       // S0, S1, O0, O1
@@ -135,7 +144,7 @@ __device__ __forceinline__ int shared_prefix(const PromptParams& p, int i, int n
 }
 
 // Sequence (or group) i; n = 0 where its numbers do not fit.
-__device__ __forceinline__ PromptSeq prompt_seq(const PromptParams& p, int i, bool report) {
+static __device__ __noinline__ PromptSeq prompt_seq(const PromptParams& p, int i, bool report) {
     PromptSeq s{0, 0, 0, 0, 0};
     const int a = __ldg(p.q_start + i), b = __ldg(p.q_start + i + 1);
     bool ok = a >= 0 && b >= a && b <= p.total_q;
@@ -184,15 +193,16 @@ struct PromptOrder {
         const int2 x = known[i];
         return PromptSeq{0, 0, 0, x.x, x.y};
     }
-    __device__ __forceinline__ int count_from(const PromptParams& p, int u) const {
+    __device__ __noinline__ int count_from(const PromptParams& p, int u) const {
         int x = 0;
+#pragma unroll 1
         for (int i = threadIdx.x & 31; i < p.B; i += 32) x += items_from(p, seq(p, i), u);
         return __reduce_add_sync(0xffffffffu, x);
     }
-    __device__ __forceinline__ void init(const PromptParams& p, int2* smem) {
-        const bool report = blockIdx.x == 0;
+    __device__ __noinline__ void init(const PromptParams& p, int2* smem, bool report) {
         known = smem;
         int top = 0, n = 0;
+#pragma unroll 1
         for (int i = threadIdx.x & 31; i < p.B; i += 32) {
             const PromptSeq s = prompt_seq(p, i, report);
             if (i < PT_KNOWN) known[i] = make_int2(s.a, s.c);
@@ -204,7 +214,7 @@ struct PromptOrder {
         hi = __reduce_max_sync(0xffffffffu, top);
     }
     // Item k (below total): its sequence's index and numbers, its number in the sequence.
-    __device__ __forceinline__ void find(const PromptParams& p, int k, int& idx, PromptSeq& s, int& t) {
+    __device__ __noinline__ void find(const PromptParams& p, int k, int& idx, PromptSeq& s, int& t) {
         // the largest level that more than k items lie at or above: down from the last
         // one in growing steps, then between the last two
         int lo = hi, step = 1;
@@ -219,6 +229,7 @@ struct PromptOrder {
         }
         int r = k - count_from(p, hi + 1);
         const int lane = threadIdx.x & 31;
+#pragma unroll 1
         for (int i0 = 0; i0 < p.B; i0 += 32) {
             PromptSeq x{0, 0, 0, 0, 0};
             if (i0 + lane < p.B) x = seq(p, i0 + lane);
@@ -247,22 +258,95 @@ struct PromptOrder {
     }
 };
 
-// The place of an item among the partials: sequences take floor(n / 2 tokens) + 1
+// How the items of a launch are cut: the first `whole` not at all, the others into
+// `parts` ranges of keys each.
+struct PromptCut {
+    int whole, parts;
+};
+// CTAs take whole rounds of items; what is left of the last round, the lightest
+// items, is cut so that all CTAs have part of it (in shared mode all items).  With r
+// items of w chunks in s ranges the last rounds take ceil(r s / grid) (w / s + 6)
+// chunks' time (an item costs about 6 beside its chunks), and a merge 8.  w: that of the
+// longest item times the share of items that are as light as these or lighter.
+static __device__ __noinline__ PromptCut prompt_cut(const PromptParams& p, const PromptOrder& order) {
+    const int items = order.total * p.Hkv;
+    PromptCut c{items, 1};
+    if (p.splits > 1) {
+        c.whole = p.shared ? 0 : items / p.grid * p.grid;
+        const int r = items - c.whole;
+        const int longest = min((order.hi + (p.shared ? 1 : 2)) * 2 * p.tokens, 1 << 24) / PT_M + 1;
+        const int w = static_cast<int>(static_cast<float>(longest) * static_cast<float>(r) / static_cast<float>(max(1, items))) + 1;
+        const int k = (threadIdx.x & 31) + 1;
+        int cost = INT_MAX;
+        if (k <= min(min(p.splits, w), max(1, 2 * p.grid / max(1, r))))
+            cost = ((r * k + p.grid - 1) / p.grid * ((w + k - 1) / k + 6) + (k > 1 && !p.shared ? 8 : 0)) * 32 + k - 1;
+        if (r > 0) c.parts = (__reduce_min_sync(0xffffffffu, cost) & 31) + 1;
+    }
+    return c;
+}
+
+// The place of an item among the partials of shared mode: groups take floor(n / 2 tokens) + 1
 // places each, counted from their first query row, without a sum over the batch.
 __host__ __device__ __forceinline__ int prompt_slot(int row0, int i, int t, int tokens) {
     return row0 / (2 * tokens) + i + t;
 }
 
+// Number v in the order of a launch cut as c says.
+static __device__ __noinline__ PromptItem prompt_item(const PromptParams& p, PromptOrder& order, const PromptCut& c, int v) {
+    const int TT = 2 * p.tokens;
+    const int k = v < c.whole ? v : c.whole + (v - c.whole) / c.parts, part = v < c.whole ? 0 : (v - c.whole) % c.parts;
+    const int parts = v < c.whole ? 1 : c.parts;
+    PromptItem it{};
+    PromptSeq s;
+    int t;
+    order.find(p, k / p.Hkv, it.idx, s, t);
+    it.live = 1;
+    it.h = k % p.Hkv;
+    it.row0 = s.row0 + t * TT;
+    it.ntok = min(TT, s.n - t * TT);
+    it.pos0 = s.L - s.n + t * TT;
+    it.L = s.L;
+    int e[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int nt = min(max(it.ntok - q * p.tokens, 0), p.tokens);
+        const int end = p.causal ? it.pos0 + q * p.tokens + nt : s.L;    // keys of the tile's last row
+        e[q] = nt > 0 && end > 0 ? (end + PT_M - 1) / PT_M : 0;
+    }
+    const int most = max(e[0], e[1]);
+    it.t0 = most * part / parts;                           // (chunks < 2^23, parts <= 32)
+    const int t1 = most * (part + 1) / parts;
+    it.e[0] = max(it.t0, min(e[0], t1));
+    it.e[1] = max(it.t0, min(e[1], t1));
+    // the last key that every row of the first tile with chunks sees
+    const int seen = p.causal ? min(it.pos0 + (it.e[0] > it.t0 ? 0 : p.tokens), it.L - 1) : it.L - 1;
+    it.edge = max(0, seen + 1) / PT_M;
+    it.slot = p.shared ? (prompt_slot(s.row0, it.idx, t, p.tokens) * p.Hkv + it.h) * parts + part
+              : parts > 1 ? v - c.whole : -1;
+    return it;
+}
+
 // ---------------------------------------------------------------------------
 // tensor memory and packed arithmetic
 // ---------------------------------------------------------------------------
-// D += A B with A (16-bit pairs) in tensor memory, issued by one thread.
-__device__ __forceinline__ void umma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                            bool accumulate) {
+// The two halves of a descriptor of a 128-byte-swizzled operand (umma_desc): the
+// address, to which steps along K are added, and what does not change.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) { return (addr >> 4) | (lbo >> 4) << 16; }
+__host__ __device__ constexpr uint32_t desc_hi(uint32_t sbo) { return (sbo >> 4) | 1u << 14 | 2u << 29; }
+// D (+)= A B, issued by one thread; A from shared memory or, 16-bit pairs, tensor memory.
+template <bool ADD>
+__device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t b_hi, uint32_t idesc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-        :: "r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u) : "memory");
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %6};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}"
+        :: "r"(d_tmem), "r"(a), "r"(b), "r"(idesc), "n"(ADD ? 1 : 0), "n"(desc_hi(1024)), "r"(b_hi) : "memory");
+}
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, uint32_t b_hi, uint32_t idesc,
+                                        uint32_t add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}"
+        :: "r"(d_tmem), "r"(a_tmem), "r"(b), "r"(idesc), "r"(add), "r"(b_hi) : "memory");
 }
 // 32 consecutive columns of the warp's 32 lanes.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
@@ -312,10 +396,14 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 // ---------------------------------------------------------------------------
 // the kernel
 // ---------------------------------------------------------------------------
-template <class KV, int D>
+template <class KV, int D, bool PAGED>
 struct PromptKernel {
-    using E = typename KV::T;
     using Lay = PromptLayout<D>;
+    // K and V tiles in shared memory: 8-row groups of 128-byte rows GROUP bytes apart,
+    // planes of 64 columns PLANE.  Contiguous: whole planes, a copy each.  Paged: the
+    // planes of a group one behind the other, so that one copy brings a block's rows of
+    // both and equal steps still lead from group to group.
+    static constexpr uint32_t PLANE = PAGED ? 1024 : Lay::PLANE, GROUP = PAGED ? D / 64 * 1024 : 1024;
     static constexpr bool BF16 = KV::code == PA_BF16;
     static constexpr int PLANES = D / 64;
     static constexpr int S = Lay::STAGES;
@@ -324,8 +412,14 @@ struct PromptKernel {
     // to 2^-21); bf16 has the range of f32 and needs none of it.
     static constexpr float LIFT = BF16 ? 0.f : 7.f;
 
+    // Every wait ends after 2^31 cycles (about a second) at the latest.  The instructions
+    // are few: what the ten roles of this kernel run has to share the instruction cache.
     static __device__ __forceinline__ bool wait(const PromptParams& p, uint64_t* bar, uint32_t parity) {
-        if (mbar_wait_bounded(bar, parity)) return true;
+        if (mbar_try_wait(bar, parity)) return true;
+        const uint32_t t0 = static_cast<uint32_t>(clock());
+        do {
+            if (mbar_try_wait(bar, parity)) return true;
+        } while (static_cast<uint32_t>(clock()) - t0 < 0x80000000u);
         raise_flag(p.err_flag, PA_ERRBIT_WAIT_TIMEOUT);
         return false;
     }
@@ -334,9 +428,11 @@ struct PromptKernel {
     static __device__ void schedule(const PromptParams& p, PromptBars* b, PromptItem* items, PromptFix* fix, int2* known) {
         const int lane = threadIdx.x & 31;
         PromptOrder order;
-        order.init(p, known);
-        const int total = order.total * p.Hkv * p.splits;
-        const int TT = 2 * p.tokens;
+        order.init(p, known, blockIdx.x == 0);
+        const PromptCut c = prompt_cut(p, order);
+        const int total = c.whole + (order.total * p.Hkv - c.whole) * c.parts;
+        if (p.cut && blockIdx.x == 0 && lane == 0)
+            p.cut[0] = make_int4(c.parts, c.parts > 1 ? order.total * p.Hkv - c.whole : 0, 0, 0);
         for (int turn = 0;; ++turn) {
             const int slot = turn % PT_ITEMS;
             bool ok = true;
@@ -348,29 +444,9 @@ struct PromptKernel {
                                                        : static_cast<int>(blockIdx.x));
             PromptItem it{};
             if (k < total) {
-                const int part = k % p.splits, kh = k / p.splits;
-                PromptSeq s;
-                int t;
-                order.find(p, kh / p.Hkv, it.idx, s, t);
-                it.live = 1;
-                it.h = kh % p.Hkv;
-                it.row0 = s.row0 + t * TT;
-                it.ntok = min(TT, s.n - t * TT);
-                it.pos0 = s.L - s.n + t * TT;
-                it.L = s.L;
-                int e[2];
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const int nt = min(max(it.ntok - q * p.tokens, 0), p.tokens);
-                    const int end = p.causal ? it.pos0 + q * p.tokens + nt : s.L;    // keys of the tile's last row
-                    e[q] = nt > 0 && end > 0 ? (end + PT_M - 1) / PT_M : 0;
-                }
-                const int most = max(e[0], e[1]);
-                it.t0 = static_cast<int>(static_cast<long long>(most) * part / p.splits);
-                const int t1 = static_cast<int>(static_cast<long long>(most) * (part + 1) / p.splits);
-                it.e[0] = max(it.t0, min(e[0], t1));
-                it.e[1] = max(it.t0, min(e[1], t1));
-                it.slot = (prompt_slot(s.row0, it.idx, t, p.tokens) * p.Hkv + it.h) * p.splits + part;
+                it = prompt_item(p, order, c, k);
+                if (!p.shared && it.slot >= 0 && it.slot % c.parts == 0 && lane == 0)
+                    p.cut[1 + it.slot / c.parts] = make_int4(it.row0, it.ntok, it.h, it.slot);
             }
             if (lane == 0) {
                 items[slot] = it;
@@ -383,6 +459,16 @@ struct PromptKernel {
             if (lane == 0) mbar_arrive(&b->i_full[slot]);
             if (!it.live) return;
         }
+    }
+
+    // The NB boxes of a paged tile; coordinates (column, row of a group, plane, group, head).
+    template <int NB>
+    static __device__ __forceinline__ void boxes(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, const int* group, int h) {
+        int g[NB];
+#pragma unroll
+        for (int x = 0; x < NB; ++x) g[x] = group[x];      // all under way before the first is used
+#pragma unroll
+        for (int x = 0; x < NB; ++x) tma_load_5d(dst + x * (PT_M / NB / 8) * GROUP, map, bar, 0, 0, 0, g[x], h);
     }
 
     // ---------------- producer ----------------
@@ -409,7 +495,7 @@ struct PromptKernel {
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) return;
                 ++qload[q];
-                if (lane == 0) {
+                if (elect_one()) {
                     mbar_arrive_expect_tx(&b->q_full[q], q_bytes);
 #pragma unroll
                     for (int pl = 0; pl < PLANES; ++pl)
@@ -421,71 +507,89 @@ struct PromptKernel {
             if (n == 0) continue;
             const int32_t* table = nullptr;
             int k0 = 0;
-            if (p.k_start) k0 = __ldg(p.k_start + it.idx);
+            if constexpr (!PAGED) k0 = __ldg(p.k_start + it.idx);
             else table = p.block_tables + static_cast<size_t>(p.shared ? __ldg(p.q_start + it.idx) : it.idx) * p.MB;
-            const int nblk = (it.L + p.bs - 1) / p.bs;     // paged: blocks that the sequence uses
+            const int nblk = (it.L + p.bs - 1) >> p.bs_log2;     // paged: blocks that the sequence uses
             // lane x < nb copies box x of each chunk; the next chunk's table entry is read ahead
             auto entry = [&](int t) -> int {               // first pool row of the lane's box in chunk t, or -1
-                const int tok = t * PT_M + lane * p.rpb;
-                const int j = tok / p.bs;
+                const int tok = t * PT_M + (lane << p.rpb_log2);
+                const int j = tok >> p.bs_log2;
                 if (lane >= nb || j >= nblk) return -1;
                 const int id = __ldg(table + j);
-                return id < 0 || id >= p.NB ? -2 : id * p.bs + (tok - j * p.bs);
+                return id < 0 || id >= p.NB ? -2 : (id << p.bs_log2) + (tok & (p.bs - 1));
             };
-            int next = table ? entry(it.t0) : 0;
+            int next = PAGED ? entry(it.t0) : 0;
+#pragma unroll 1
+            for (int q = 0; q < 2 && ok; ++q) queries(q);
+#pragma unroll 1
             for (int j = 0; j < n && ok; ++j) {
-                if (j == 0) queries(0);
-                if (j == 0 && ok) queries(1);
-                if (!ok) break;
                 const int t = it.t0 + j;
                 int row = next;
-                if (table) {
+                if constexpr (PAGED) {
                     if (j + 1 < n) next = entry(t + 1);
                 } else {
                     row = k0 + t * PT_M;
                 }
-                uint4 mask = make_uint4(0, 0, 0, 0);
-                if (table) {
+                if constexpr (PAGED) {
+                    // keys of blocks outside the pool are left out; this chunk's K is not on its
+                    // way yet, so no softmax warp has come to it
                     const uint32_t miss = __ballot_sync(0xffffffffu, row == -2);
-                    if (miss) {                            // keys of blocks outside the pool are left out
-                        if (lane == 0) {
+                    const int any_bad = *reinterpret_cast<volatile int*>(&b->any_bad);
+                    if (miss | any_bad) {
+                        uint32_t w = 0;                    // lane x: the keys 32 x .. 32 x + 31
+#pragma unroll 1
+                        for (int y = 0; y < 32; ++y) w |= (miss >> ((32 * (lane & 3) + y) >> p.rpb_log2) & 1u) << y;
+                        if (lane < 4) reinterpret_cast<uint32_t*>(bad + (issued / 2) % PT_BAD)[lane] = w;
+                        if (miss && lane == 0) {
                             raise_flag(p.err_flag, PA_ERRBIT_BAD_BLOCK);
                             *reinterpret_cast<volatile int*>(&b->any_bad) = 1;
                         }
-                        uint32_t w[4] = {0, 0, 0, 0};
-                        for (int x = 0; x < nb; ++x)
-                            if ((miss >> x) & 1u)
-                                for (int y = x * p.rpb; y < (x + 1) * p.rpb; ++y) w[y >> 5] |= 1u << (y & 31);
-                        mask = make_uint4(w[0], w[1], w[2], w[3]);
+                        __syncwarp();
                     }
                 }
                 // boxes without rows start behind the pool, where TMA fills in zeros
-                const int at = table ? (row >= 0 ? row : p.NB * p.bs) : row;
-#pragma unroll
+                const int at = PAGED && row < 0 ? p.NB << p.bs_log2 : row;
+                if constexpr (PAGED) {
+                    __syncwarp();
+                    if (lane < 16) b->box[lane] = at >> 3;
+                    __syncwarp();
+                }
+#pragma unroll 1
                 for (int v = 0; v < 2; ++v) {
                     const int st = issued % S;
                     if (issued >= S) ok = ok && wait(p, &empty[st], (issued / S - 1) & 1u);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     uint8_t* dst = base + Lay::KV + st * Lay::TILE;
-                    if (lane == 0) {
-                        if (v) bad[st] = mask;
+                    // One elected thread issues the copies, their number known to the compiler and the
+                    // rows loaded ahead, so that operands stay in uniform registers: blocks of 8 and 16
+                    // tokens then take no longer than those of 128 (with a lane per box 2.1 and 1.4
+                    // times as long).
+                    if (elect_one()) {
                         mbar_arrive_expect_tx(&full[st], Lay::TILE);
+                        const CUtensorMap* map = v ? tv : tk;
+                        if constexpr (PAGED) {
+                            if (nb == 16) boxes<16>(dst, map, &full[st], b->box, it.h);
+                            else if (nb == 8) boxes<8>(dst, map, &full[st], b->box, it.h);
+                            else if (nb == 4) boxes<4>(dst, map, &full[st], b->box, it.h);
+                            else if (nb == 2) boxes<2>(dst, map, &full[st], b->box, it.h);
+                            else boxes<1>(dst, map, &full[st], b->box, it.h);
+                        } else {
+#pragma unroll
+                            for (int pl = 0; pl < PLANES; ++pl)
+                                tma_load_4d(dst + pl * PLANE, map, &full[st], 0, at, it.h, pl);
+                        }
                     }
                     __syncwarp();
-                    if (lane < nb) {
-#pragma unroll
-                        for (int pl = 0; pl < PLANES; ++pl)
-                            tma_load_4d(dst + pl * Lay::PLANE + lane * p.rpb * 128, v ? tv : tk, &full[st], 0, at, it.h, pl);
-                    }
                     ++issued;
                 }
             }
         }
         // every copy must land before the CTA exits
+#pragma unroll 1
         for (int st = max(0, issued - S); st < issued; ++st)
             if (!wait(p, &full[st % S], (st / S) & 1u)) break;
-#pragma unroll
+#pragma unroll 1
         for (int q = 0; q < 2; ++q)
             if (qload[q] > 0) wait(p, &b->q_full[q], (qload[q] - 1) & 1u);
     }
@@ -496,24 +600,30 @@ struct PromptKernel {
         const uint32_t tm = b->tmem;
         const uint32_t id_s = umma_idesc_f16(BF16, PT_M, PT_M, false, false) | p.negate;
         const uint32_t id_o = umma_idesc_f16(BF16, PT_M, D, false, true);
+        constexpr uint32_t hi = desc_hi(GROUP);
         const uint32_t qb = smem_u32(base + Lay::Q), kvb = smem_u32(base + Lay::KV);
         int used = 0;                                      // stages gone through
         int qn[2] = {0, 0};
         uint32_t pn[2] = {0, 0};
+        uint32_t on[2] = {0, 0}, edges = 0;
         bool ok = true;
         auto score = [&](int q, int st, bool last) {       // S_q = Q_q K^T
-            const uint32_t kb = kvb + st * Lay::TILE, qa = qb + q * Lay::TILE;
+            const uint32_t a = desc_lo(qb + q * Lay::TILE, 16), k = desc_lo(kvb + st * Lay::TILE, 16), d = tm + q * PT_M;
             tc05_fence_after();
+            umma_ss<false>(d, a, k, hi, id_s);
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = static_cast<uint32_t>(kk >> 2) * Lay::PLANE + static_cast<uint32_t>(kk & 3) * 32u;
-                umma_f16(tm + q * PT_M, umma_desc(qa + off, 16u, 1024u, 2u), umma_desc(kb + off, 16u, 1024u, 2u), id_s, kk > 0);
+            for (int kk = 1; kk < D / 16; ++kk) {
+                constexpr uint32_t STEP = 32u >> 4;
+                umma_ss<true>(d, a + (kk >> 2) * (Lay::PLANE >> 4) + (kk & 3) * STEP, k + (kk >> 2) * (PLANE >> 4) + (kk & 3) * STEP, hi,
+                              id_s);
             }
             umma_commit(&b->s_full[q]);
             if (last) umma_commit(&b->q_empty[q]);
         };
         auto value = [&](int q, int st, bool first) {      // O_q (+)= P_q V, as the parts of P come
-            const uint32_t vb = kvb + st * Lay::TILE;
+            // the O of the item before must have been taken out
+            if (first && on[q]++ > 0 && !wait(p, &b->o_empty[q], on[q] & 1u)) return false;
+            const uint32_t v = desc_lo(kvb + st * Lay::TILE, PLANE), d = tm + Lay::OCOL + q * D, a = tm + q * PT_M;
             const uint32_t phase = pn[q]++ & 1u;
 #pragma unroll
             for (int part = 0; part < PT_PARTS; ++part) {
@@ -522,8 +632,7 @@ struct PromptKernel {
 #pragma unroll
                 for (int x = 0; x < PT_M / 16 / PT_PARTS; ++x) {
                     const int kk = part * (PT_M / 16 / PT_PARTS) + x;
-                    umma_f16_ta(tm + Lay::OCOL + q * D, tm + q * PT_M + kk * 8,
-                                umma_desc(vb + kk * 2048u, Lay::PLANE, 1024u, 2u), id_o, !first || kk > 0);
+                    umma_ts(d, a + kk * 8, v + kk * (2 * GROUP >> 4), hi, id_o, kk > 0 || !first);
                 }
             }
             return true;
@@ -538,7 +647,7 @@ struct PromptKernel {
             if (n == 0) continue;
             // chunk j: K in stage 2 j of the item's, V in the one behind it
             if (!(ok = wait(p, &full[used % S], (used / S) & 1u))) break;
-#pragma unroll
+#pragma unroll 1
             for (int q = 0; q < 2; ++q) {
                 if ((q ? n1 : n0) == 0) continue;
                 if (!(ok = wait(p, &b->q_full[q], qn[q]++ & 1u))) break;
@@ -550,9 +659,12 @@ struct PromptKernel {
             for (int j = 0; j < n && ok; ++j) {
                 const int vs = used % S, ks = (used + 1) % S;
                 if (!(ok = wait(p, &full[vs], (used / S) & 1u))) break;
+                const bool edge = it.t0 + j >= it.edge;
+                if (edge) mbar_arrive(&b->v_there);        // mended while the softmax is at work on S
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     const int nq = q ? n1 : n0;
+                    if (q == 0 && edge && !(ok = wait(p, &b->v_fit, edges++ & 1u))) break;
                     if (j < nq) {
                         if (!(ok = value(q, vs, j == 0))) break;
                         if (j == nq - 1) umma_commit(&b->o_full[q]);
@@ -571,16 +683,20 @@ struct PromptKernel {
         wait(p, &b->fin, 0u);
     }
 
-    // ---------------- softmax: tile q, one row per thread ----------------
-    // Keys that some row of the tile must not see, in the chunk's V: rows behind the
-    // sequence become zeros; elsewhere values that are not finite, whose product with
-    // a weight of 0 would be NaN, are noted by column and first key, become zeros, and
-    // come back at the end for the rows that do see them.
-    static __device__ __noinline__ void mend_values(uint8_t* v, PromptFix* fix, int r, int lo, int tail, int key0) {
+    // ---------------- mender: one warp ----------------
+    // Keys that some row of an item must not see, in an edge chunk's V: rows behind the
+    // sequence become zeros; elsewhere values that are not finite, whose product with a
+    // weight of 0 would be NaN, are noted by column and first key, become zeros, and come
+    // back at the end for the rows that do see them.
+    static __device__ __forceinline__ uint8_t* value_at(uint8_t* v, int row, int ch) {
+        return v + (ch >> 3) * PLANE + (row >> 3) * GROUP + swz128(row & 7, ch & 7);
+    }
+    static __device__ __noinline__ void mend_values(uint8_t* v, PromptFix* fix, int lane, int lo, int tail, int key0) {
         constexpr int CH = D / 8;                          // 16-byte pieces of a row
-        for (int x = r; x < (PT_M - lo) * CH; x += PT_M) {
+#pragma unroll 1
+        for (int x = lane; x < (PT_M - lo) * CH; x += 32) {
             const int row = lo + x / CH, ch = x % CH;
-            uint4* at = reinterpret_cast<uint4*>(v + (ch >> 3) * Lay::PLANE + swz128(row, ch & 7));
+            uint4* at = reinterpret_cast<uint4*>(value_at(v, row, ch));
             if (row >= tail) continue;
             const uint4 raw = *at;
             uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
@@ -602,68 +718,74 @@ struct PromptKernel {
             }
         }
     }
-    // The zeros, and whether there is anything to mend: 0 * x is NaN for an x that is
-    // not finite.
-    static __device__ __forceinline__ bool unfit_values(uint8_t* v, int r, int lo, int tail) {
-        constexpr int CH = D / 8;
+    static __device__ void mend(const PromptParams& p, uint8_t* base, uint64_t* full, PromptBars* b, const PromptItem* items,
+                                PromptFix* fix) {
         using E2 = std::conditional_t<BF16, __nv_bfloat162, __half2>;
-        E2 acc[2];
-        uint32_t zero = 0;
-        acc[0] = acc[1] = *reinterpret_cast<E2*>(&zero);
-        const E2 none = acc[0];
-        for (int x = r; x < (PT_M - lo) * CH; x += PT_M) {
-            const int row = lo + x / CH, ch = x % CH;
-            uint4* at = reinterpret_cast<uint4*>(v + (ch >> 3) * Lay::PLANE + swz128(row, ch & 7));
-            if (row >= tail) {
-                *at = make_uint4(0, 0, 0, 0);
-                continue;
+        constexpr int CH = D / 8, RPI = 32 / CH, U = 4;    // rows per access of the warp; accesses in flight
+        const int lane = threadIdx.x & 31;
+        const int ch = lane % CH;
+        const uint32_t zero = 0;
+        const E2 none = *reinterpret_cast<const E2*>(&zero);
+        int stage = 1;                                     // of the item's first V
+        uint32_t edges = 0;
+        for (int turn = 0;; ++turn) {
+            const int is = turn % PT_ITEMS;
+            if (!__all_sync(0xffffffffu, wait(p, &b->i_full[is], (turn / PT_ITEMS) & 1u))) return;
+            const PromptItem it = items[is];
+            if (!it.live) return;
+            const int t1 = max(it.e[0], it.e[1]);
+            const int seen = p.causal ? min(it.pos0 + (it.e[0] > it.t0 ? 0 : p.tokens), it.L - 1) : it.L - 1;
+            for (int t = max(it.t0, it.edge); t < t1; ++t, ++edges) {
+                const int vs = stage + 2 * (t - it.t0);
+                // (full alone would not do: it may be rounds behind or ahead of a warp that
+                // looks at some chunks only)
+                if (!__all_sync(0xffffffffu, wait(p, &b->v_there, edges & 1u) && wait(p, &full[vs % S], (vs / S) & 1u))) return;
+                uint8_t* v = base + Lay::KV + (vs % S) * Lay::TILE;
+                const int lo = max(0, seen + 1 - t * PT_M), tail = min(PT_M, it.L - t * PT_M);
+#pragma unroll 1
+                for (int row = tail + lane / CH; row < PT_M; row += RPI)
+                    *reinterpret_cast<uint4*>(value_at(v, row, ch)) = make_uint4(0, 0, 0, 0);
+                // is there anything to mend?  0 * x is NaN for an x that is not finite
+                E2 acc[4] = {none, none, none, none};
+#pragma unroll 1
+                for (int row0 = lo + lane / CH; row0 < tail; row0 += U * RPI) {
+                    uint4 raw[U];
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const int row = row0 + u * RPI;
+                        raw[u] = row < tail ? *reinterpret_cast<const uint4*>(value_at(v, row, ch)) : make_uint4(0, 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const E2* e = reinterpret_cast<const E2*>(&raw[u]);
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) acc[y] = __hfma2(e[y], none, acc[y]);
+                    }
+                }
+                const E2 sum = __hadd2(__hadd2(acc[0], acc[1]), __hadd2(acc[2], acc[3]));
+                if (__any_sync(0xffffffffu, __hisnan(sum.x) || __hisnan(sum.y)))
+                    mend_values(v, fix + is, lane, lo, tail, t * PT_M);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&b->v_fit);
             }
-            const uint4 raw = *at;
-            const E2* e = reinterpret_cast<const E2*>(&raw);
-#pragma unroll
-            for (int y = 0; y < 4; ++y) acc[y & 1] = __hfma2(e[y], none, acc[y & 1]);
-        }
-        acc[0] = __hadd2(acc[0], acc[1]);
-        return __hisnan(acc[0].x) || __hisnan(acc[0].y);
-    }
-
-    // 64 bytes of each of the warp's 32 rows to 32 places in memory, by way of shared
-    // memory so that four lanes write one row's 64 bytes together.  dst(k): where lane's
-    // row k * 8 + lane / 4 goes, or null.
-    static __device__ __forceinline__ void put_rows(uint8_t* buf, int lane, const uint4 (&x)[4], uint8_t* const (&dst)[4],
-                                                    int off) {
-        __syncwarp();
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-            *reinterpret_cast<uint4*>(buf + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) = x[c];
-        __syncwarp();
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int row = k * 8 + (lane >> 2);
-            const uint4 y = *reinterpret_cast<const uint4*>(buf + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4));
-            if (dst[k]) *reinterpret_cast<uint4*>(dst[k] + off + ((lane & 3) << 4)) = y;
+            stage += 2 * (t1 - it.t0);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&b->i_empty[is]);
         }
     }
 
-    static __device__ void softmax(const PromptParams& p, int q, uint8_t* base, uint64_t* full, PromptBars* b,
-                                   const PromptItem* items, PromptFix* fix, const uint4* bad) {
+    // ---------------- softmax: tile q, one row per thread ----------------
+    static __device__ void softmax(const PromptParams& p, int q, PromptBars* b, const PromptItem* items, const uint4* bad,
+                                   float2* rows) {
         const int r = threadIdx.x & (PT_M - 1);            // tile row = tensor-memory lane
         const int lane = threadIdx.x & 31;
         const uint32_t lanes = static_cast<uint32_t>(r & ~31) << 16;
         const uint32_t ts = b->tmem + lanes + q * PT_M, to = b->tmem + lanes + Lay::OCOL + q * D;
-        uint8_t* buf = base + Lay::STAGE + (threadIdx.x >> 5) * 2048;
         const int tok = r / p.G;
-        // (token, head) of the rows that this lane writes
-        int wtok[4], whead[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int row = (r & ~31) + k * 8 + (lane >> 2);
-            wtok[k] = row / p.G;
-            whead[k] = row - wtok[k] * p.G;
-        }
         const float c = p.c;
-        uint32_t sn = 0, on = 0;
-        int vstage = 1;                                    // stage of the item's first V
+        uint32_t sn = 0;
+        int chunk = 0;                                     // chunks of the items before
         for (int turn = 0;; ++turn) {
             const int is = turn % PT_ITEMS;
             if (!__all_sync(0xffffffffu, wait(p, &b->i_full[is], (turn / PT_ITEMS) & 1u))) return;
@@ -681,42 +803,30 @@ struct PromptKernel {
                 float s[PT_M];
 #pragma unroll
                 for (int x = 0; x < 4; ++x) tmem_ld32(ts + 32 * x, s + 32 * x);
-                const int any_bad = p.block_tables ? *reinterpret_cast<volatile int*>(&b->any_bad) : 0;
+                const int any_bad = PAGED ? *reinterpret_cast<volatile int*>(&b->any_bad) : 0;
                 tmem_wait_ld();
-                const int vs = vstage + 2 * (t - it.t0);
                 const bool edge = t * PT_M + PT_M - 1 > seen;
-                if (edge) {
-                    const int rel = last - t * PT_M;
-                    const int least = __reduce_min_sync(0xffffffffu, rel);
+                if (edge || any_bad) {
+                    const int rel = last - t * PT_M;       // the row sees columns up to this one
+                    const uint32_t* out = reinterpret_cast<const uint32_t*>(bad + (chunk + t - it.t0) % PT_BAD);
 #pragma unroll
                     for (int x = 0; x < PT_M; x += 32) {
-                        if (x + 31 <= least) continue;
+                        uint32_t w = rel - x >= 31 ? 0xffffffffu : rel < x ? 0u : (2u << (rel - x)) - 1u;
+                        if (any_bad) w &= ~out[x / 32];
+                        if (__all_sync(0xffffffffu, w == 0xffffffffu)) continue;
 #pragma unroll
-                        for (int y = 0; y < 32; ++y) s[x + y] = x + y <= rel ? s[x + y] : -INFINITY;
+                        for (int y = 0; y < 32; ++y) s[x + y] = (w >> y) & 1u ? s[x + y] : -INFINITY;
                     }
-                    if (!__all_sync(0xffffffffu, wait(p, &full[vs % S], (vs / S) & 1u))) return;
                 }
-                const auto highest = [&]() {
-                    float mx[4] = {s[0], s[1], s[2], s[3]};
+                float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                    for (int x = 4; x < PT_M - 4; x += 8) {
+                for (int x = 4; x < PT_M - 4; x += 8) {
 #pragma unroll
-                        for (int y = 0; y < 4; ++y) mx[y] = max3(mx[y], s[x + y], s[x + 4 + y]);
-                    }
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) mx[y] = fmaxf(mx[y], s[PT_M - 4 + y]);
-                    return fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
-                };
-                float top = highest();
-                if (any_bad) {                             // keys of blocks outside the pool
-                    if (!__all_sync(0xffffffffu, wait(p, &full[vs % S], (vs / S) & 1u))) return;
-                    const uint4 m4 = bad[vs % S];
-                    const uint32_t w[4] = {m4.x, m4.y, m4.z, m4.w};
-#pragma unroll
-                    for (int x = 0; x < PT_M; ++x)
-                        if ((w[x >> 5] >> (x & 31)) & 1u) s[x] = -INFINITY;
-                    top = highest();
+                    for (int y = 0; y < 4; ++y) mx[y] = max3(mx[y], s[x + y], s[x + 4 + y]);
                 }
+#pragma unroll
+                for (int y = 0; y < 4; ++y) mx[y] = fmaxf(mx[y], s[PT_M - 4 + y]);
+                const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
                 // the reference moves at the row's first key and when it is passed by 2^8
                 const bool move = top * c > ref + (PT_SLACK + LIFT) && top > -INFINITY;
                 if (__any_sync(0xffffffffu, move)) {
@@ -726,7 +836,7 @@ struct PromptKernel {
                     sum.x *= f;
                     sum.y *= f;
                     if (t > it.t0) {
-#pragma unroll
+#pragma unroll 1
                         for (int x = 0; x < D; x += 16) {
                             float o[16];
                             tmem_ld16(to + x, o);
@@ -736,12 +846,6 @@ struct PromptKernel {
                             tmem_st16(to + x, o);
                         }
                     }
-                }
-                if (edge) {
-                    uint8_t* v = base + Lay::KV + (vs % S) * Lay::TILE;
-                    const int lo = max(0, seen + 1 - t * PT_M), tail = it.L - t * PT_M;
-                    if (unfit_values(v, r, lo, tail)) mend_values(v, fix + is, r, lo, tail, t * PT_M);
-                    fence_proxy_async_smem();
                 }
                 const float neg = ref > -INFINITY ? -ref : 0.f;
                 const float2 c2 = make_float2(c, c), n2 = make_float2(neg, neg);
@@ -769,67 +873,91 @@ struct PromptKernel {
                 }
                 sum = add2(sum, acc);
             }
-            vstage += 2 * (max(it.e[0], it.e[1]) - it.t0);
-            // ---- the tile's rows ----
-            const float total = sum.x + sum.y;
-            const bool direct = p.splits == 1 && !p.shared;
-            const float inv = !direct ? 1.f : total != 0.f ? 1.f / total : 0.f;
-            const bool any = t1 > it.t0;
-            const size_t part0 = (static_cast<size_t>(it.slot) * 2 + q) * PT_M;
-            uint8_t* dst[4];
+            chunk += max(it.e[0], it.e[1]) - it.t0;
+            // (reference, l) for the warps that write the rows out
+            rows[(is * 2 + q) * PT_M + r] = make_float2(ref, sum.x + sum.y);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&b->l_full[is][q]);
+            if (lane == 0) mbar_arrive(&b->i_empty[is]);
+        }
+    }
+
+    // ---------------- rows out: four warps, both tiles in turn ----------------
+    static __device__ __forceinline__ void put32(void* dst, const uint32_t (&w)[8]) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                     :: "l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    }
+    static __device__ void write_out(const PromptParams& p, PromptBars* b, const PromptItem* items, const PromptFix* fix,
+                                     const float2* rows) {
+        const int r = threadIdx.x & (PT_M - 1), lane = threadIdx.x & 31;
+        const uint32_t lanes = static_cast<uint32_t>(r & ~31) << 16;
+        const int tok = r / p.G, head = r - tok * p.G;
+        uint32_t n[2] = {0, 0};
+        for (int turn = 0;; ++turn) {
+            const int is = turn % PT_ITEMS;
+            if (!__all_sync(0xffffffffu, wait(p, &b->i_full[is], (turn / PT_ITEMS) & 1u))) return;
+            const PromptItem it = items[is];
+            if (!it.live) return;
+            const bool direct = it.slot < 0;
+#pragma unroll 1
+            for (int q = 0; q < 2; ++q) {
+                const uint32_t to = b->tmem + lanes + Lay::OCOL + q * D;
+                const bool mine = tok < p.tokens && q * p.tokens + tok < it.ntok;
+                const int last = p.causal ? it.pos0 + q * p.tokens + tok : it.L - 1;    // the row's last key
+                const bool any = it.e[q] > it.t0;
+                const size_t part = (static_cast<size_t>(direct ? 0 : it.slot) * 2 + q) * PT_M + r;
+                uint8_t* dst = direct ? static_cast<uint8_t*>(p.out) +
+                                            (static_cast<size_t>(it.row0 + q * p.tokens + tok) * p.Hq + it.h * p.G + head) * D * 2
+                                      : reinterpret_cast<uint8_t*>(p.part_acc + part * D);
+                if (!any) {                                // no keys: zeros, or an empty partial
+                    const uint32_t w[8] = {};
+                    if (mine && direct) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const bool in = wtok[k] < p.tokens && q * p.tokens + wtok[k] < it.ntok;
-                const size_t row = static_cast<size_t>(it.row0 + q * p.tokens + wtok[k]) * p.Hq + it.h * p.G + whead[k];
-                dst[k] = !in ? nullptr
-                         : direct ? static_cast<uint8_t*>(p.out) + row * D * 2
-                         : any ? reinterpret_cast<uint8_t*>(p.part_acc + (part0 + (r & ~31) + k * 8 + (lane >> 2)) * D) : nullptr;
-            }
-            if (!direct && tok < p.tokens && q * p.tokens + tok < it.ntok) p.part_ml[part0 + r] = make_float2(ref, total);
-            bool fixed = false;
-            if (any) {
-                if (!__all_sync(0xffffffffu, wait(p, &b->o_full[q], on++ & 1u))) return;
+                        for (int x = 0; x < D; x += 16) put32(dst + x * 2, w);
+                    }
+                    if (mine && !direct) p.part_ml[part] = make_float2(-INFINITY, 0.f);
+                    continue;
+                }
+                const uint32_t phase = n[q]++ & 1u;
+                if (!__all_sync(0xffffffffu, wait(p, &b->l_full[is][q], (turn / PT_ITEMS) & 1u) && wait(p, &b->o_full[q], phase))) return;
                 tc05_fence_after();
-                fixed = *reinterpret_cast<volatile int*>(&fix[is].any);
-                __threadfence_block();
-            }
-#pragma unroll
-            for (int x = 0; x < D; x += 32) {
-                float o[32];
-                if (any) {
-                    tmem_ld32(to + x, o);
+                const float2 ml = rows[(is * 2 + q) * PT_M + r];
+                const float inv = !direct ? 1.f : ml.y != 0.f ? 1.f / ml.y : 0.f;
+                const bool fixed = *reinterpret_cast<const volatile int*>(&fix[is].any);
+                if (mine && !direct) p.part_ml[part] = ml;
+#pragma unroll 1
+                for (int x = 0; x < D; x += 16) {
+                    float o[16];
+                    tmem_ld16(to + x, o);
                     tmem_wait_ld();
                     if (fixed) {
 #pragma unroll
-                        for (int d = 0; d < 32; ++d) {
+                        for (int d = 0; d < 16; ++d) {
                             if (last >= fix[is].first[0][x + d]) o[d] = NAN;
                             if (last >= fix[is].first[1][x + d]) o[d] += INFINITY;
                             if (last >= fix[is].first[2][x + d]) o[d] -= INFINITY;
                         }
                     }
-                } else {
+                    if (!mine) continue;
+                    uint32_t w[8];
+                    if (direct) {
 #pragma unroll
-                    for (int d = 0; d < 32; ++d) o[d] = 0.f;
-                }
-                uint4 w[4];
-                if (direct) {
+                        for (int d = 0; d < 8; ++d) w[d] = pack2(o[2 * d] * inv, o[2 * d + 1] * inv, BF16);
+                        put32(dst + x * 2, w);
+                    } else {
 #pragma unroll
-                    for (int d = 0; d < 4; ++d)
-                        w[d] = make_uint4(pack2(o[8 * d] * inv, o[8 * d + 1] * inv, BF16), pack2(o[8 * d + 2] * inv, o[8 * d + 3] * inv, BF16),
-                                          pack2(o[8 * d + 4] * inv, o[8 * d + 5] * inv, BF16), pack2(o[8 * d + 6] * inv, o[8 * d + 7] * inv, BF16));
-                    put_rows(buf, lane, w, dst, x * 2);
-                } else {
+                        for (int y = 0; y < 2; ++y) {
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-#pragma unroll
-                        for (int d = 0; d < 4; ++d)
-                            w[d] = make_uint4(__float_as_uint(o[16 * y + 4 * d]), __float_as_uint(o[16 * y + 4 * d + 1]),
-                                              __float_as_uint(o[16 * y + 4 * d + 2]), __float_as_uint(o[16 * y + 4 * d + 3]));
-                        put_rows(buf, lane, w, dst, (x + 16 * y) * 4);
+                            for (int d = 0; d < 8; ++d) w[d] = __float_as_uint(o[8 * y + d]);
+                            put32(dst + x * 4 + y * 32, w);
+                        }
                     }
                 }
+                tc05_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&b->o_empty[q]);
             }
-            tc05_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&b->i_empty[is]);
         }
@@ -859,11 +987,11 @@ __device__ __forceinline__ void write_tails(const PromptParams& p) {
     }
 }
 
-template <class KV, int D>
+template <class KV, int D, bool PAGED>
 __global__ void __launch_bounds__(PT_THREADS, 1)
 prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ CUtensorMap tq,
               const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
-    using K = PromptKernel<KV, D>;
+    using K = PromptKernel<KV, D, PAGED>;
     using Lay = PromptLayout<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -873,6 +1001,7 @@ prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ CU
     PromptItem* items = reinterpret_cast<PromptItem*>(base + Lay::ITEM);
     PromptFix* fix = reinterpret_cast<PromptFix*>(base + Lay::FIX);
     uint4* bad = reinterpret_cast<uint4*>(base + Lay::BAD);
+    float2* rows = reinterpret_cast<float2*>(base + Lay::ROWS);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < Lay::STAGES; ++s) {
@@ -885,13 +1014,18 @@ prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ CU
             mbar_init(&b->s_full[q], 1);
             for (int x = 0; x < PT_PARTS; ++x) mbar_init(&b->p_full[q][x], 4);
             mbar_init(&b->o_full[q], 1);
+            mbar_init(&b->o_empty[q], 4);
+            for (int x = 0; x < PT_ITEMS; ++x) mbar_init(&b->l_full[x][q], 4);
         }
         for (int s = 0; s < PT_ITEMS; ++s) {
             mbar_init(&b->i_full[s], 1);
-            mbar_init(&b->i_empty[s], 10);                 // 8 softmax warps, the MMA thread, the producer
+            mbar_init(&b->i_empty[s], 15);                 // all warps but the scheduler; of the MMA warp one thread
         }
+        mbar_init(&b->v_there, 1);
+        mbar_init(&b->v_fit, 1);
         mbar_init(&b->fin, 1);
         b->any_bad = 0;
+        for (int x = 0; x < PT_BAD; ++x) bad[x] = make_uint4(0, 0, 0, 0);
         fence_barrier_init();
         fence_proxy_async_smem();
     }
@@ -918,10 +1052,14 @@ prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ CU
             K::producer(p, base, full, empty, b, items, bad, &tq, &tk, &tv);
         } else if (warp == 10) {
             K::schedule(p, b, items, fix, reinterpret_cast<int2*>(base + Lay::KNOWN));
+        } else if (warp == 11) {
+            K::mend(p, base, full, b, items, fix);
+        } else {
+            K::write_out(p, b, items, fix, rows);
         }
     } else {
         regs_up<PT_REGS>();
-        K::softmax(p, warp >> 2, base, full, b, items, fix, bad);
+        K::softmax(p, warp >> 2, b, items, bad, rows);
     }
     tc05_fence_before();
     __syncthreads();
@@ -932,42 +1070,51 @@ prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ CU
 
 // ---------------------------------------------------------------------------
 // merge of the ranges of keys: out = sum_k 2^(r_k - M) O_k / sum_k 2^(r_k - M) l_k
-// One warp per (query row, head).
+// One CTA per 32 rows of a cut item, one warp per row at a time.
 // ---------------------------------------------------------------------------
+constexpr int PT_MERGE_WARPS = 8, PT_MERGE_ROWS = 32;
+
 template <class KV, int D>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(32 * PT_MERGE_WARPS)
 prompt_merge_kernel(const __grid_constant__ PromptParams p) {
-    constexpr int DPL = D / 32;
-    const int lane = threadIdx.x & 31;
-    const long long w = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    constexpr int DPL = D / 32, PER = 2 * PT_M / PT_MERGE_ROWS;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     grid_dependency_wait();
-    if (w >= static_cast<long long>(p.total_q) * p.Hq) return;
-    const int row = static_cast<int>(w / p.Hq), h = static_cast<int>(w - static_cast<long long>(row) * p.Hq);
-    const int i = prompt_seq_of(p, row);
-    if (i < 0) return;
-    const PromptSeq s = prompt_seq(p, i, false);
-    if (s.n == 0) return;
-    const int j = row - s.row0, t = j / (2 * p.tokens), u = j - t * 2 * p.tokens;
-    const int q = u >= p.tokens, r = (u - q * p.tokens) * p.G + h % p.G;
-    const size_t slot0 = (static_cast<size_t>(prompt_slot(s.row0, i, t, p.tokens)) * p.Hkv + h / p.G) * p.splits;
-    float M = -INFINITY, den = 0.f, num[DPL];
+    const int4 n = p.cut[0];
+    const int parts = n.x;
+    if (static_cast<int>(blockIdx.x) / PER >= n.y) return;
+    const int4 item = p.cut[1 + blockIdx.x / PER];         // (first row, tokens, head, place)
+    for (int y = warp; y < PT_MERGE_ROWS; y += PT_MERGE_WARPS) {
+        const int x = (blockIdx.x % PER) * PT_MERGE_ROWS + y, q = x / PT_M, r = x % PT_M;
+        const int tok = r / p.G;
+        if (tok >= p.tokens || q * p.tokens + tok >= item.y) continue;
+        const size_t at = (static_cast<size_t>(item.w) * 2 + q) * PT_M + r;
+        const float2 ml = lane < parts ? p.part_ml[at + static_cast<size_t>(lane) * 2 * PT_M] : make_float2(-INFINITY, 0.f);
+        float M = ml.x;
 #pragma unroll
-    for (int x = 0; x < DPL; ++x) num[x] = 0.f;
-    for (int k = 0; k < p.splits; ++k) {
-        const size_t at = ((slot0 + k) * 2 + q) * PT_M + r;
-        const float2 ml = p.part_ml[at];
-        if (ml.y == 0.f) continue;
-        const float Mn = fmaxf(M, ml.x), Mu = Mn > -INFINITY ? Mn : 0.f;
-        const float a = exp2f(M - Mu), e = exp2f(ml.x - Mu);
-        den = den * a + e * ml.y;
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        const float e = ml.y != 0.f ? exp2f(ml.x - (M > -INFINITY ? M : 0.f)) : 0.f;
+        float den = ml.y != 0.f ? e * ml.y : 0.f;
 #pragma unroll
-        for (int x = 0; x < DPL; ++x) num[x] = num[x] * a + e * p.part_acc[at * D + lane * DPL + x];
-        M = Mn;
+        for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+        const uint32_t some = __ballot_sync(0xffffffffu, ml.y != 0.f);
+        float num[DPL];
+#pragma unroll
+        for (int d = 0; d < DPL; ++d) num[d] = 0.f;
+#pragma unroll 4
+        for (int k = 0; k < parts; ++k) {
+            const float f = __shfl_sync(0xffffffffu, e, k);
+            if (!((some >> k) & 1u)) continue;
+#pragma unroll
+            for (int d = 0; d < DPL; ++d)
+                num[d] = fmaf(f, p.part_acc[(at + static_cast<size_t>(k) * 2 * PT_M) * D + lane * DPL + d], num[d]);
+        }
+        const float inv = den != 0.f ? 1.f / den : 0.f;
+        typename KV::T* o = static_cast<typename KV::T*>(p.out) +
+                            (static_cast<size_t>(item.x + q * p.tokens + tok) * p.Hq + item.z * p.G + r - tok * p.G) * D + lane * DPL;
+#pragma unroll
+        for (int d = 0; d < DPL; ++d) o[d] = from_float<typename KV::T>(num[d] * inv);
     }
-    const float inv = den != 0.f ? 1.f / den : 0.f;
-    typename KV::T* o = static_cast<typename KV::T*>(p.out) + (static_cast<size_t>(row) * p.Hq + h) * D + lane * DPL;
-#pragma unroll
-    for (int x = 0; x < DPL; ++x) o[x] = from_float<typename KV::T>(num[x] * inv);
 }
 
 }  // namespace pa
