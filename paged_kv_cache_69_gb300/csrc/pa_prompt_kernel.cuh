@@ -47,6 +47,7 @@ constexpr int PT_ITEMS = 4;            // items that the scheduler may be ahead
 constexpr int PT_PARTS = 2;            // parts of P that the second product starts on
 constexpr int PT_BAD = 8;              // chunks whose masks of bad blocks are kept: more than are under way
 constexpr int PT_KNOWN = 1024;         // sequences whose items' numbers are kept
+constexpr int PT_LEVELS = 1024;        // levels of length that items are counted by
 // Registers of a softmax thread, which holds a row of S, and of the others, out of
 // the block's 128 each at launch.
 constexpr int PT_REGS = 192, PT_REGS_FEW = 64;
@@ -118,7 +119,7 @@ struct PromptLayout {
     static constexpr uint32_t BAD = (FIX + PT_ITEMS * sizeof(PromptFix) + 15) & ~15u;   // a uint4 each
     static constexpr uint32_t ROWS = (BAD + 16 * PT_BAD + 15) & ~15u;        // (reference, l) of each item's rows
     static constexpr uint32_t KNOWN = ROWS + PT_ITEMS * 2 * PT_M * 8;       // (level, items) of the first sequences
-    static constexpr uint32_t BYTES = KNOWN + 8 * PT_KNOWN + 1024;   // + alignment of the base
+    static constexpr uint32_t BYTES = KNOWN + 8 * PT_KNOWN + 4 * (PT_LEVELS + 2) + 1024;   // + alignment of the base
     static_assert(BYTES <= 227 * 1024, "shared memory of a CTA");
     static constexpr uint32_t TCOLS = 512;                       // S0, S1, O0, O1
     static constexpr uint32_t OCOL = 256;
@@ -182,61 +183,114 @@ __device__ __forceinline__ int items_from(const PromptParams& p, const PromptSeq
     return p.shared ? (s.a >= u ? s.c : 0) : min(max(s.a + s.c - u, 0), s.c);
 }
 
-// The items of the launch in order of length, for one warp.
+// The items of the launch in order of length, for one warp: by levels of 2^shift
+// steps, from the highest down, within one by sequence, the longest first.
 struct PromptOrder {
     int2* known;                       // (a, c) of the first PT_KNOWN sequences
-    int hi;                            // no item that is still to come lies above this level
-    int total;                         // items per KV head
+    int* above;                        // [PT_LEVELS + 2]: items at a level and above
+    int levels, shift;
+    int top, total;                    // the highest step; items per KV head
+    int level, chunk, before;          // where the last item was found: the level's items before sequence 32 chunk
 
     __device__ __forceinline__ PromptSeq seq(const PromptParams& p, int i) const {
+        if (i >= p.B) return PromptSeq{0, 0, 0, 0, 0};
         if (i >= PT_KNOWN) return prompt_seq(p, i, false);
         const int2 x = known[i];
         return PromptSeq{0, 0, 0, x.x, x.y};
     }
-    __device__ __noinline__ int count_from(const PromptParams& p, int u) const {
-        int x = 0;
-#pragma unroll 1
-        for (int i = threadIdx.x & 31; i < p.B; i += 32) x += items_from(p, seq(p, i), u);
-        return __reduce_add_sync(0xffffffffu, x);
-    }
+    // smem: PT_KNOWN pairs, then PT_LEVELS + 2 counts
     __device__ __noinline__ void init(const PromptParams& p, int2* smem, bool report) {
+        const int lane = threadIdx.x & 31;
         known = smem;
-        int top = 0, n = 0;
+        above = reinterpret_cast<int*>(smem + PT_KNOWN);
+        int high = 0, n = 0;
 #pragma unroll 1
-        for (int i = threadIdx.x & 31; i < p.B; i += 32) {
+        for (int i = lane; i < p.B; i += 32) {
             const PromptSeq s = prompt_seq(p, i, report);
             if (i < PT_KNOWN) known[i] = make_int2(s.a, s.c);
-            if (s.c > 0) top = max(top, p.shared ? s.a : s.a + s.c - 1);
+            if (s.c > 0) high = max(high, p.shared ? s.a : s.a + s.c - 1);
             n += s.c;
         }
-        __syncwarp();
         total = __reduce_add_sync(0xffffffffu, n);
-        hi = __reduce_max_sync(0xffffffffu, top);
-    }
-    // Item k (below total): its sequence's index and numbers, its number in the sequence.
-    __device__ __noinline__ void find(const PromptParams& p, int k, int& idx, PromptSeq& s, int& t) {
-        // the largest level that more than k items lie at or above: down from the last
-        // one in growing steps, then between the last two
-        int lo = hi, step = 1;
-        while (lo > 0 && count_from(p, lo) <= k) {
-            hi = lo - 1;
-            lo = max(0, lo - step);
-            step *= 2;
-        }
-        while (lo < hi) {
-            const int u = (lo + hi + 1) >> 1;
-            if (count_from(p, u) > k) lo = u; else hi = u - 1;
-        }
-        int r = k - count_from(p, hi + 1);
-        const int lane = threadIdx.x & 31;
+        top = __reduce_max_sync(0xffffffffu, high);
+        shift = max(0, 32 - __clz(top) - 10);              // top >> shift < PT_LEVELS
+        levels = (top >> shift) + 1;
+        level = levels;
+        chunk = before = 0;
+        // differences of the levels' counts, then the counts, then their sums from above
 #pragma unroll 1
-        for (int i0 = 0; i0 < p.B; i0 += 32) {
-            PromptSeq x{0, 0, 0, 0, 0};
-            if (i0 + lane < p.B) x = seq(p, i0 + lane);
-            const int own = items_from(p, x, hi) - items_from(p, x, hi + 1);
+        for (int u = lane; u < levels + 1; u += 32) above[u] = 0;
+        __syncwarp();
+        const auto range = [&](int u0, int u1, int x) {    // x items on each of the levels u0 .. u1 - 1
+            if (u0 >= u1) return;
+            atomicAdd(above + u0, x);
+            atomicAdd(above + u1, -x);
+        };
+#pragma unroll 1
+        for (int i = lane; i < p.B; i += 32) {
+            const PromptSeq s = seq(p, i);
+            if (s.c == 0) continue;
+            const int u0 = s.a >> shift, u1 = p.shared ? u0 : (s.a + s.c - 1) >> shift;
+            if (u0 == u1) {
+                range(u0, u0 + 1, s.c);
+            } else {
+                range(u0, u0 + 1, ((u0 + 1) << shift) - s.a);
+                range(u0 + 1, u1, 1 << shift);
+                range(u1, u1 + 1, s.a + s.c - (u1 << shift));
+            }
+        }
+        __syncwarp();
+        int count = 0, sum = 0;                            // of the level before; of the levels below
+#pragma unroll 1
+        for (int u0 = 0; u0 < levels; u0 += 32) {
+            const int u = u0 + lane;
+            int x = u < levels ? above[u] : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            x += count;
+            count = __shfl_sync(0xffffffffu, x, 31);
+            int z = u < levels ? x : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, z, o);
+                if (lane >= o) z += y;
+            }
+            if (u < levels) above[u] = total - sum - (z - x);
+            sum += __shfl_sync(0xffffffffu, z, 31);
+        }
+        if (lane == 0) above[levels] = 0;
+        __syncwarp();
+    }
+    // Item k (below total, from call to call not smaller): its sequence's index and
+    // numbers, its number in the sequence.
+    __device__ __noinline__ void find(const PromptParams& p, int k, int& idx, PromptSeq& s, int& t) {
+        const int lane = threadIdx.x & 31;
+        // the highest level that more than k items lie at or above, 32 at a time
+        int u = level;
+        while (true) {
+            const int v = u - lane;
+            const uint32_t hit = __ballot_sync(0xffffffffu, v >= 0 && v < levels && above[max(v, 0)] > k);
+            if (hit) {
+                u -= __ffs(hit) - 1;
+                break;
+            }
+            u -= 32;
+            if (u < 0) { u = 0; break; }                   // not reached: above[0] = total > k
+        }
+        if (u != level) { level = u; chunk = before = 0; }
+        int r = k - above[u + 1];
+        const int lo = u << shift, hi = (u + 1) << shift;
+#pragma unroll 1
+        for (; 32 * chunk < p.B; ++chunk) {
+            const PromptSeq x = seq(p, 32 * chunk + lane);
+            const int from = items_from(p, x, hi);         // items of the sequence above the level
+            const int own = items_from(p, x, lo) - from;
             const int all = __reduce_add_sync(0xffffffffu, own);
-            if (r >= all) {
-                r -= all;
+            if (r - before >= all) {
+                before += all;
                 continue;
             }
             int inc = own;
@@ -245,11 +299,12 @@ struct PromptOrder {
                 const int y = __shfl_up_sync(0xffffffffu, inc, o);
                 if (lane >= o) inc += y;
             }
+            r -= before;
             const int src = __ffs(__ballot_sync(0xffffffffu, inc > r)) - 1;
-            const int before = __shfl_sync(0xffffffffu, inc - own, src);
-            idx = i0 + src;
+            const int in = r - __shfl_sync(0xffffffffu, inc - own, src);      // the how manieth of the sequence's
+            t = __shfl_sync(0xffffffffu, x.c - 1 - from, src) - in;
+            idx = 32 * chunk + src;
             s = prompt_seq(p, idx, false);
-            t = p.shared ? r - before : hi - s.a;
             return;
         }
         idx = 0;                       // not reached: k < total
@@ -274,7 +329,7 @@ static __device__ __noinline__ PromptCut prompt_cut(const PromptParams& p, const
     if (p.splits > 1) {
         c.whole = p.shared ? 0 : items / p.grid * p.grid;
         const int r = items - c.whole;
-        const int longest = min((order.hi + (p.shared ? 1 : 2)) * 2 * p.tokens, 1 << 24) / PT_M + 1;
+        const int longest = min((order.top + (p.shared ? 1 : 2)) * 2 * p.tokens, 1 << 24) / PT_M + 1;
         const int w = static_cast<int>(static_cast<float>(longest) * static_cast<float>(r) / static_cast<float>(max(1, items))) + 1;
         const int k = (threadIdx.x & 31) + 1;
         int cost = INT_MAX;
@@ -684,10 +739,10 @@ struct PromptKernel {
     }
 
     // ---------------- mender: one warp ----------------
-    // Keys that some row of an item must not see, in an edge chunk's V: rows behind the
-    // sequence become zeros; elsewhere values that are not finite, whose product with a
-    // weight of 0 would be NaN, are noted by column and first key, become zeros, and come
-    // back at the end for the rows that do see them.
+    // Keys that some row of an item must not see, in an edge chunk's V: values that are
+    // not finite, whose product with a weight of 0 would be NaN, become zeros.  Those of the
+    // sequence are noted by column and first key before, and come back at the end for the
+    // rows that do see them.
     static __device__ __forceinline__ uint8_t* value_at(uint8_t* v, int row, int ch) {
         return v + (ch >> 3) * PLANE + (row >> 3) * GROUP + swz128(row & 7, ch & 7);
     }
@@ -697,7 +752,10 @@ struct PromptKernel {
         for (int x = lane; x < (PT_M - lo) * CH; x += 32) {
             const int row = lo + x / CH, ch = x % CH;
             uint4* at = reinterpret_cast<uint4*>(value_at(v, row, ch));
-            if (row >= tail) continue;
+            if (row >= tail) {
+                *at = make_uint4(0, 0, 0, 0);
+                continue;
+            }
             const uint4 raw = *at;
             uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
             constexpr uint32_t EXP = BF16 ? 0x7f80u : 0x7c00u;
@@ -721,9 +779,8 @@ struct PromptKernel {
     static __device__ void mend(const PromptParams& p, uint8_t* base, uint64_t* full, PromptBars* b, const PromptItem* items,
                                 PromptFix* fix) {
         using E2 = std::conditional_t<BF16, __nv_bfloat162, __half2>;
-        constexpr int CH = D / 8, RPI = 32 / CH, U = 4;    // rows per access of the warp; accesses in flight
+        constexpr int U = 8;                               // accesses in flight
         const int lane = threadIdx.x & 31;
-        const int ch = lane % CH;
         const uint32_t zero = 0;
         const E2 none = *reinterpret_cast<const E2*>(&zero);
         int stage = 1;                                     // of the item's first V
@@ -742,19 +799,20 @@ struct PromptKernel {
                 if (!__all_sync(0xffffffffu, wait(p, &b->v_there, edges & 1u) && wait(p, &full[vs % S], (vs / S) & 1u))) return;
                 uint8_t* v = base + Lay::KV + (vs % S) * Lay::TILE;
                 const int lo = max(0, seen + 1 - t * PT_M), tail = min(PT_M, it.L - t * PT_M);
-#pragma unroll 1
-                for (int row = tail + lane / CH; row < PT_M; row += RPI)
-                    *reinterpret_cast<uint4*>(value_at(v, row, ch)) = make_uint4(0, 0, 0, 0);
-                // is there anything to mend?  0 * x is NaN for an x that is not finite
+                // is there anything to mend from the 8-row group of row lo on?  0 * x is NaN for an
+                // x that is not finite
                 E2 acc[4] = {none, none, none, none};
+                constexpr int SPANS = PAGED ? 1 : PLANES;   // stretches that lie together
+                const int first = (lo >> 3) * GROUP, end = PT_M / 8 * GROUP;
 #pragma unroll 1
-                for (int row0 = lo + lane / CH; row0 < tail; row0 += U * RPI) {
+                for (int span = 0; span < SPANS; ++span)
+#pragma unroll 1
+                for (int at = first + lane * 16; at < end; at += U * 512) {
                     uint4 raw[U];
 #pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        const int row = row0 + u * RPI;
-                        raw[u] = row < tail ? *reinterpret_cast<const uint4*>(value_at(v, row, ch)) : make_uint4(0, 0, 0, 0);
-                    }
+                    for (int u = 0; u < U; ++u)
+                        raw[u] = at + u * 512 < end ? *reinterpret_cast<const uint4*>(v + span * PLANE + at + u * 512)
+                                                    : make_uint4(0, 0, 0, 0);
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
                         const E2* e = reinterpret_cast<const E2*>(&raw[u]);
@@ -888,6 +946,21 @@ struct PromptKernel {
                      :: "l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                      : "memory");
     }
+    // What mend_values took out, for a row that sees the keys up to `last`.
+    static __device__ __noinline__ void unmend(void* row, bool direct, int last, const PromptFix* fix) {
+        using E = typename KV::T;
+#pragma unroll 1
+        for (int d = 0; d < D; ++d) {
+            const bool nan = last >= fix->first[0][d], up = last >= fix->first[1][d], down = last >= fix->first[2][d];
+            if (!(nan || up || down)) continue;
+            float x = direct ? to_float(static_cast<E*>(row)[d]) : static_cast<float*>(row)[d];
+            if (nan) x = NAN;
+            if (up) x += INFINITY;
+            if (down) x -= INFINITY;
+            if (direct) static_cast<E*>(row)[d] = from_float<E>(x);
+            else static_cast<float*>(row)[d] = x;
+        }
+    }
     static __device__ void write_out(const PromptParams& p, PromptBars* b, const PromptItem* items, const PromptFix* fix,
                                      const float2* rows) {
         const int r = threadIdx.x & (PT_M - 1), lane = threadIdx.x & 31;
@@ -927,33 +1000,29 @@ struct PromptKernel {
                 const bool fixed = *reinterpret_cast<const volatile int*>(&fix[is].any);
                 if (mine && !direct) p.part_ml[part] = ml;
 #pragma unroll 1
-                for (int x = 0; x < D; x += 16) {
-                    float o[16];
-                    tmem_ld16(to + x, o);
+                for (int x = 0; x < D; x += 32) {
+                    float o[32];
+                    tmem_ld32(to + x, o);
                     tmem_wait_ld();
-                    if (fixed) {
-#pragma unroll
-                        for (int d = 0; d < 16; ++d) {
-                            if (last >= fix[is].first[0][x + d]) o[d] = NAN;
-                            if (last >= fix[is].first[1][x + d]) o[d] += INFINITY;
-                            if (last >= fix[is].first[2][x + d]) o[d] -= INFINITY;
-                        }
-                    }
                     if (!mine) continue;
                     uint32_t w[8];
                     if (direct) {
 #pragma unroll
-                        for (int d = 0; d < 8; ++d) w[d] = pack2(o[2 * d] * inv, o[2 * d + 1] * inv, BF16);
-                        put32(dst + x * 2, w);
+                        for (int y = 0; y < 2; ++y) {
+#pragma unroll
+                            for (int d = 0; d < 8; ++d) w[d] = pack2(o[16 * y + 2 * d] * inv, o[16 * y + 2 * d + 1] * inv, BF16);
+                            put32(dst + x * 2 + y * 32, w);
+                        }
                     } else {
 #pragma unroll
-                        for (int y = 0; y < 2; ++y) {
+                        for (int y = 0; y < 4; ++y) {
 #pragma unroll
                             for (int d = 0; d < 8; ++d) w[d] = __float_as_uint(o[8 * y + d]);
                             put32(dst + x * 4 + y * 32, w);
                         }
                     }
                 }
+                if (fixed && mine) unmend(dst, direct, last, fix + is);
                 tc05_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&b->o_empty[q]);

@@ -280,3 +280,29 @@ def test_agrees_with_pa_attention():
     want, tol = ref.prompts(c.q, c.k, c.v, c.qs, c.ks, c.scale, 7.0)
     c.check(a)
     ref.check(b, a.double(), 2 * tol)
+
+
+def test_more_sequences_than_the_scheduler_keeps():
+    g = torch.Generator().manual_seed(7)
+    lens = torch.randint(0, 40, (1500,), generator=g).tolist()
+    lens[1400] = 700
+    c = Case(lens, 2, 1, 64, F16, seed=1)
+    c.check(c.flat())
+
+
+def test_lengths_of_many_levels():
+    """128 heads to a KV head: an item is two tokens, its levels are counted by steps."""
+    c = Case([1, 4097, 3000, 17], 128, 1, 64, BF16, q_lens=[1, 2300, 5, 17])
+    c.check(c.flat())
+
+
+@pytest.mark.parametrize("Hkv", [1, 3, 16])
+def test_items_about_a_round(Hkv):
+    """Just under, at and over whole rounds of items, whose rest is cut."""
+    for n in (36, 2700, 152 * 36 // Hkv, 152 * 36 // Hkv + 1, 160 * 36 // Hkv, 300 * 36 // Hkv):
+        c = Case([n + 3000], 7 * Hkv, Hkv, 64, F16, q_lens=[n], seed=n)
+        out = c.flat()
+        rows = torch.randperm(n, generator=c.order)[:40].sort().values
+        o, t = ref.attend(c.q[rows.cuda()], c.k, c.v, c.scale, (rows + 3000).cuda())
+        ref.check(out[rows.cuda()], o, t)
+        assert c.err.item() == 0
