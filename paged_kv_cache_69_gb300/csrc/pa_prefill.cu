@@ -123,6 +123,8 @@ pa_status launch_prompt(const PromptCall& c, const PromptPlan& plan, void* parts
     p.B = c.B; p.Hq = c.Hq; p.Hkv = c.Hkv; p.G = G; p.bs = c.bs; p.NB = c.NB; p.MB = c.MB;
     p.total_q = c.total_q; p.total_k = c.total_k;
     p.tokens = PT_M / G;
+    p.div_tt = make_div(2 * p.tokens);
+    p.div_hkv = make_div(c.Hkv);
     p.splits = plan.splits;
     p.grid = plan.grid;
     p.causal = !c.shared;

@@ -38,6 +38,7 @@
 #include <type_traits>
 
 #include "pa_device.cuh"
+#include "pa_rows.cuh"
 
 namespace pa {
 
@@ -47,7 +48,6 @@ constexpr int PT_ITEMS = 4;            // items that the scheduler may be ahead
 constexpr int PT_PARTS = 2;            // parts of P that the second product starts on
 constexpr int PT_BAD = 8;              // chunks whose masks of bad blocks are kept: more than are under way
 constexpr int PT_KNOWN = 1024;         // sequences whose items' numbers are kept
-constexpr int PT_LEVELS = 1024;        // levels of length that items are counted by
 // Registers of a softmax thread, which holds a row of S, and of the others, out of
 // the block's 128 each at launch.
 constexpr int PT_REGS = 192, PT_REGS_FEW = 64;
@@ -74,6 +74,7 @@ struct PromptParams {
     int32_t *tail_lens, *tail_blk;
     int rpb;                           // rows per TMA box of K and V
     int bs_log2, rpb_log2;
+    Div div_tt, div_hkv;               // by 2 * tokens, by Hkv
     float c;                           // |scale| log2(e)
     uint32_t negate;                   // instruction descriptor bit of -Q, for scale < 0
 };
@@ -118,8 +119,8 @@ struct PromptLayout {
     static constexpr uint32_t FIX = ITEM + PT_ITEMS * ((sizeof(PromptItem) + 15) & ~15u);
     static constexpr uint32_t BAD = (FIX + PT_ITEMS * sizeof(PromptFix) + 15) & ~15u;   // a uint4 each
     static constexpr uint32_t ROWS = (BAD + 16 * PT_BAD + 15) & ~15u;        // (reference, l) of each item's rows
-    static constexpr uint32_t KNOWN = ROWS + PT_ITEMS * 2 * PT_M * 8;       // (level, items) of the first sequences
-    static constexpr uint32_t BYTES = KNOWN + 8 * PT_KNOWN + 4 * (PT_LEVELS + 2) + 1024;   // + alignment of the base
+    static constexpr uint32_t KNOWN = ROWS + PT_ITEMS * 2 * PT_M * 8;       // the first sequences' numbers
+    static constexpr uint32_t BYTES = KNOWN + 16 * PT_KNOWN + 1024;   // + alignment of the base
     static_assert(BYTES <= 227 * 1024, "shared memory of a CTA");
     static constexpr uint32_t TCOLS = 512;                       // S0, S1, O0, O1
     static constexpr uint32_t OCOL = 256;
@@ -141,10 +142,14 @@ constexpr int PT_SHARED_ROWS = 8, PT_SHARED_KEYS = 64;
 __device__ __forceinline__ int shared_prefix(const PromptParams& p, int i, int n) {
     const int P = __ldg(p.seq_lens + i);
     if (P < PT_SHARED_KEYS || n * p.G < PT_SHARED_ROWS) return 0;
-    return min(P, p.MB * p.bs) / p.bs * p.bs;
+    return min(P, p.MB * p.bs) & ~(p.bs - 1);
 }
 
-// Sequence (or group) i; n = 0 where its numbers do not fit.
+__device__ __forceinline__ int prompt_items_of(const PromptParams& p, int n) {
+    return static_cast<int>(div_by(n + 2 * p.tokens - 1, p.div_tt));
+}
+
+// Sequence (or group) i; n = 0 where its numbers do not fit or it has no items.
 static __device__ __noinline__ PromptSeq prompt_seq(const PromptParams& p, int i, bool report) {
     PromptSeq s{0, 0, 0, 0, 0};
     const int a = __ldg(p.q_start + i), b = __ldg(p.q_start + i + 1);
@@ -166,150 +171,98 @@ static __device__ __noinline__ PromptSeq prompt_seq(const PromptParams& p, int i
     }
     s.row0 = a;
     s.n = b - a;
-    const int TT = 2 * p.tokens;
-    if (p.shared) {
-        s.c = s.L > 0 ? (s.n + TT - 1) / TT : 0;
-        s.a = s.L / TT;
-    } else {
-        s.c = (s.n + TT - 1) / TT;
-        s.a = max(0, s.L - s.n) / TT;
-    }
+    if (p.shared && s.L == 0) s.n = 0;
+    s.a = static_cast<int>(div_by(p.shared ? s.L : max(0, s.L - s.n), p.div_tt));
+    s.c = prompt_items_of(p, s.n);
     return s;
 }
 
-// Items of the sequence at level u and above: causal items lie one to a level from a
-// on, the items of a group all at a.
-__device__ __forceinline__ int items_from(const PromptParams& p, const PromptSeq& s, int u) {
-    return p.shared ? (s.a >= u ? s.c : 0) : min(max(s.a + s.c - u, 0), s.c);
+// Items of a sequence of c items from level a on that lie at level u or above: causal
+// items one to a level, the items of a group all at a.
+__device__ __forceinline__ int items_from(const PromptParams& p, int a, int c, int u) {
+    return p.shared ? (a >= u ? c : 0) : min(max(a + c - u, 0), c);
 }
 
-// The items of the launch in order of length, for one warp: by levels of 2^shift
-// steps, from the highest down, within one by sequence, the longest first.
+// The items of the launch in order of length, for one warp: in up to 32 bands of
+// 2^shift levels, from the highest down, within one by sequence, the longest first.
+// (Every instruction here runs once or a few times and is fetched from far away, 12
+// cycles each: short code starts sooner than clever code.)
 struct PromptOrder {
-    int2* known;                       // (a, c) of the first PT_KNOWN sequences
-    int* above;                        // [PT_LEVELS + 2]: items at a level and above
-    int levels, shift;
-    int top, total;                    // the highest step; items per KV head
-    int level, chunk, before;          // where the last item was found: the level's items before sequence 32 chunk
+    int4* known;                       // (first row, tokens, keys, level) of the first PT_KNOWN sequences
+    int top, total;                    // the highest level; items per KV head
+    int shift;                         // 31: one band, the order does not matter
+    int above;                         // lane u: items in band u and above
+    int band, chunk, before;           // where the last item was found: the band's items before sequence 32 chunk
 
-    __device__ __forceinline__ PromptSeq seq(const PromptParams& p, int i) const {
-        if (i >= p.B) return PromptSeq{0, 0, 0, 0, 0};
-        if (i >= PT_KNOWN) return prompt_seq(p, i, false);
-        const int2 x = known[i];
-        return PromptSeq{0, 0, 0, x.x, x.y};
+    __device__ __forceinline__ int4 seq(const PromptParams& p, int i) const {
+        if (i >= p.B) return make_int4(0, 0, 0, 0);
+        if (i < PT_KNOWN) return known[i];
+        const PromptSeq s = prompt_seq(p, i, false);
+        return make_int4(s.row0, s.n, s.L, s.a);
     }
-    // smem: PT_KNOWN pairs, then PT_LEVELS + 2 counts
-    __device__ __noinline__ void init(const PromptParams& p, int2* smem, bool report) {
+    __device__ __forceinline__ void init(const PromptParams& p, int4* smem, bool report) {
         const int lane = threadIdx.x & 31;
         known = smem;
-        above = reinterpret_cast<int*>(smem + PT_KNOWN);
         int high = 0, n = 0;
 #pragma unroll 1
         for (int i = lane; i < p.B; i += 32) {
             const PromptSeq s = prompt_seq(p, i, report);
-            if (i < PT_KNOWN) known[i] = make_int2(s.a, s.c);
+            if (i < PT_KNOWN) known[i] = make_int4(s.row0, s.n, s.L, s.a);
             if (s.c > 0) high = max(high, p.shared ? s.a : s.a + s.c - 1);
             n += s.c;
         }
+        __syncwarp();
         total = __reduce_add_sync(0xffffffffu, n);
         top = __reduce_max_sync(0xffffffffu, high);
-        shift = max(0, 32 - __clz(top) - 10);              // top >> shift < PT_LEVELS
-        levels = (top >> shift) + 1;
-        level = levels;
+        band = 32;
         chunk = before = 0;
-        // differences of the levels' counts, then the counts, then their sums from above
+        shift = 31;
+        above = lane == 0 ? total : 0;
+        if (total * p.Hkv <= p.grid) return;               // one round
+        shift = max(0, 27 - __clz(top));                   // top >> shift < 32
+        above = 0;
 #pragma unroll 1
-        for (int u = lane; u < levels + 1; u += 32) above[u] = 0;
-        __syncwarp();
-        const auto range = [&](int u0, int u1, int x) {    // x items on each of the levels u0 .. u1 - 1
-            if (u0 >= u1) return;
-            atomicAdd(above + u0, x);
-            atomicAdd(above + u1, -x);
-        };
+        for (int i0 = 0; i0 < p.B; i0 += 32) {
+            const int4 s = seq(p, i0 + lane);
+            const int c = prompt_items_of(p, s.y), m = min(32, p.B - i0);
 #pragma unroll 1
-        for (int i = lane; i < p.B; i += 32) {
-            const PromptSeq s = seq(p, i);
-            if (s.c == 0) continue;
-            const int u0 = s.a >> shift, u1 = p.shared ? u0 : (s.a + s.c - 1) >> shift;
-            if (u0 == u1) {
-                range(u0, u0 + 1, s.c);
-            } else {
-                range(u0, u0 + 1, ((u0 + 1) << shift) - s.a);
-                range(u0 + 1, u1, 1 << shift);
-                range(u1, u1 + 1, s.a + s.c - (u1 << shift));
-            }
+            for (int j = 0; j < m; ++j)
+                above += items_from(p, __shfl_sync(0xffffffffu, s.w, j), __shfl_sync(0xffffffffu, c, j), lane << shift);
         }
-        __syncwarp();
-        int count = 0, sum = 0;                            // of the level before; of the levels below
-#pragma unroll 1
-        for (int u0 = 0; u0 < levels; u0 += 32) {
-            const int u = u0 + lane;
-            int x = u < levels ? above[u] : 0;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, x, o);
-                if (lane >= o) x += y;
-            }
-            x += count;
-            count = __shfl_sync(0xffffffffu, x, 31);
-            int z = u < levels ? x : 0;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, z, o);
-                if (lane >= o) z += y;
-            }
-            if (u < levels) above[u] = total - sum - (z - x);
-            sum += __shfl_sync(0xffffffffu, z, 31);
-        }
-        if (lane == 0) above[levels] = 0;
-        __syncwarp();
     }
     // Item k (below total, from call to call not smaller): its sequence's index and
     // numbers, its number in the sequence.
-    __device__ __noinline__ void find(const PromptParams& p, int k, int& idx, PromptSeq& s, int& t) {
+    __device__ __forceinline__ void find(const PromptParams& p, int k, int& idx, int4& s, int& t) {
         const int lane = threadIdx.x & 31;
-        // the highest level that more than k items lie at or above, 32 at a time
-        int u = level;
-        while (true) {
-            const int v = u - lane;
-            const uint32_t hit = __ballot_sync(0xffffffffu, v >= 0 && v < levels && above[max(v, 0)] > k);
-            if (hit) {
-                u -= __ffs(hit) - 1;
-                break;
-            }
-            u -= 32;
-            if (u < 0) { u = 0; break; }                   // not reached: above[0] = total > k
-        }
-        if (u != level) { level = u; chunk = before = 0; }
-        int r = k - above[u + 1];
-        const int lo = u << shift, hi = (u + 1) << shift;
+        const int u = 31 - __clz(__ballot_sync(0xffffffffu, above > k) | 1u);
+        const int next = __shfl_sync(0xffffffffu, above, (u + 1) & 31);
+        if (u != band) { band = u; chunk = before = 0; }
+        int r = k - (u == 31 ? 0 : next);
 #pragma unroll 1
-        for (; 32 * chunk < p.B; ++chunk) {
-            const PromptSeq x = seq(p, 32 * chunk + lane);
-            const int from = items_from(p, x, hi);         // items of the sequence above the level
-            const int own = items_from(p, x, lo) - from;
-            const int all = __reduce_add_sync(0xffffffffu, own);
-            if (r - before >= all) {
-                before += all;
-                continue;
-            }
+        for (;; ++chunk) {
+            const int4 x = seq(p, 32 * chunk + lane);
+            const int c = prompt_items_of(p, x.y);
+            const int from = shift == 31 ? 0 : items_from(p, x.w, c, (u + 1) << shift);      // above the band
+            const int own = (shift == 31 ? c : items_from(p, x.w, c, u << shift)) - from;
             int inc = own;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int y = __shfl_up_sync(0xffffffffu, inc, o);
                 if (lane >= o) inc += y;
             }
+            const int all = __shfl_sync(0xffffffffu, inc, 31);
+            if (r - before >= all && 32 * (chunk + 1) < p.B) {
+                before += all;
+                continue;
+            }
             r -= before;
-            const int src = __ffs(__ballot_sync(0xffffffffu, inc > r)) - 1;
-            const int in = r - __shfl_sync(0xffffffffu, inc - own, src);      // the how manieth of the sequence's
-            t = __shfl_sync(0xffffffffu, x.c - 1 - from, src) - in;
+            const int src = 31 - __clz(__ballot_sync(0xffffffffu, inc - own <= r && own > 0) | 1u);
+            t = __shfl_sync(0xffffffffu, c - 1 - from + inc - own, src) - r;
             idx = 32 * chunk + src;
-            s = prompt_seq(p, idx, false);
+            s = make_int4(__shfl_sync(0xffffffffu, x.x, src), __shfl_sync(0xffffffffu, x.y, src),
+                          __shfl_sync(0xffffffffu, x.z, src), 0);
             return;
         }
-        idx = 0;                       // not reached: k < total
-        s = PromptSeq{0, 0, 0, 0, 0};
-        t = 0;
     }
 };
 
@@ -323,61 +276,67 @@ struct PromptCut {
 // items of w chunks in s ranges the last rounds take ceil(r s / grid) (w / s + 6)
 // chunks' time (an item costs about 6 beside its chunks), and a merge 8.  w: that of the
 // longest item times the share of items that are as light as these or lighter.
-static __device__ __noinline__ PromptCut prompt_cut(const PromptParams& p, const PromptOrder& order) {
+__device__ __forceinline__ PromptCut prompt_cut(const PromptParams& p, const PromptOrder& order) {
     const int items = order.total * p.Hkv;
     PromptCut c{items, 1};
-    if (p.splits > 1) {
-        c.whole = p.shared ? 0 : items / p.grid * p.grid;
-        const int r = items - c.whole;
-        const int longest = min((order.top + (p.shared ? 1 : 2)) * 2 * p.tokens, 1 << 24) / PT_M + 1;
-        const int w = static_cast<int>(static_cast<float>(longest) * static_cast<float>(r) / static_cast<float>(max(1, items))) + 1;
-        const int k = (threadIdx.x & 31) + 1;
-        int cost = INT_MAX;
-        if (k <= min(min(p.splits, w), max(1, 2 * p.grid / max(1, r))))
-            cost = ((r * k + p.grid - 1) / p.grid * ((w + k - 1) / k + 6) + (k > 1 && !p.shared ? 8 : 0)) * 32 + k - 1;
-        if (r > 0) c.parts = (__reduce_min_sync(0xffffffffu, cost) & 31) + 1;
-    }
+    if (p.splits == 1) return c;
+    const float grid = static_cast<float>(p.grid);
+    c.whole = p.shared ? 0 : static_cast<int>(floorf(__fdividef(items + 0.5f, grid))) * p.grid;
+    const float r = static_cast<float>(items - c.whole);
+    if (r == 0.f) return c;
+    const float longest = static_cast<float>(order.top + 2) * static_cast<float>(2 * p.tokens) * (1.f / PT_M);
+    const float w = fmaxf(1.f, ceilf(longest * __fdividef(r, static_cast<float>(items))));
+    const float k = static_cast<float>((threadIdx.x & 31) + 1);
+    float cost = ceilf(__fdividef(r * k - 0.5f, grid)) * (ceilf(__fdividef(w, k) - 0.01f) + 6.f) + (k > 1.f && !p.shared ? 8.f : 0.f);
+    if (k > 1.f && (k > static_cast<float>(p.splits) || k > w || k * r > 2.f * grid)) cost = 1e9f;
+    // the cheapest, of equal ones the first: costs are whole numbers below 2^26
+    c.parts = (__reduce_min_sync(0xffffffffu, static_cast<uint32_t>(fminf(cost, 6.7e7f)) << 5 | (threadIdx.x & 31)) & 31) + 1;
     return c;
 }
 
 // The place of an item among the partials of shared mode: groups take floor(n / 2 tokens) + 1
 // places each, counted from their first query row, without a sum over the batch.
-__host__ __device__ __forceinline__ int prompt_slot(int row0, int i, int t, int tokens) {
-    return row0 / (2 * tokens) + i + t;
+__device__ __forceinline__ int prompt_slot(const PromptParams& p, int row0, int i, int t) {
+    return static_cast<int>(div_by(row0, p.div_tt)) + i + t;
 }
 
 // Number v in the order of a launch cut as c says.
-static __device__ __noinline__ PromptItem prompt_item(const PromptParams& p, PromptOrder& order, const PromptCut& c, int v) {
+__device__ __forceinline__ PromptItem prompt_item(const PromptParams& p, PromptOrder& order, const PromptCut& c, int v) {
     const int TT = 2 * p.tokens;
-    const int k = v < c.whole ? v : c.whole + (v - c.whole) / c.parts, part = v < c.whole ? 0 : (v - c.whole) % c.parts;
-    const int parts = v < c.whole ? 1 : c.parts;
-    PromptItem it{};
-    PromptSeq s;
-    int t;
-    order.find(p, k / p.Hkv, it.idx, s, t);
-    it.live = 1;
-    it.h = k % p.Hkv;
-    it.row0 = s.row0 + t * TT;
-    it.ntok = min(TT, s.n - t * TT);
-    it.pos0 = s.L - s.n + t * TT;
-    it.L = s.L;
-    int e[2];
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        const int nt = min(max(it.ntok - q * p.tokens, 0), p.tokens);
-        const int end = p.causal ? it.pos0 + q * p.tokens + nt : s.L;    // keys of the tile's last row
-        e[q] = nt > 0 && end > 0 ? (end + PT_M - 1) / PT_M : 0;
+    int k = v, part = 0, parts = 1;
+    if (v >= c.whole) {                                    // cut items: at most two to a CTA
+        parts = c.parts;
+        k = static_cast<int>(__fdividef(v - c.whole + 0.5f, static_cast<float>(parts)));
+        part = v - c.whole - k * parts;
+        k += c.whole;
     }
-    const int most = max(e[0], e[1]);
-    it.t0 = most * part / parts;                           // (chunks < 2^23, parts <= 32)
-    const int t1 = most * (part + 1) / parts;
-    it.e[0] = max(it.t0, min(e[0], t1));
-    it.e[1] = max(it.t0, min(e[1], t1));
+    const int kk = static_cast<int>(div_by(k, p.div_hkv));
+    PromptItem it{};
+    int4 s;
+    int t;
+    order.find(p, kk, it.idx, s, t);
+    it.live = 1;
+    it.h = k - kk * p.Hkv;
+    it.row0 = s.x + t * TT;
+    it.ntok = min(TT, s.y - t * TT);
+    it.pos0 = s.z - s.y + t * TT;
+    it.L = s.z;
+    // keys of each tile's last row, in chunks
+    const int n0 = min(it.ntok, p.tokens), n1 = it.ntok - n0;
+    const int e0 = max(0, (p.causal ? it.pos0 + n0 : s.z) + PT_M - 1) / PT_M;
+    const int e1 = n1 > 0 ? max(0, (p.causal ? it.pos0 + it.ntok : s.z) + PT_M - 1) / PT_M : 0;
+    const int most = max(e0, e1);
+    int t1 = most;
+    if (parts > 1) {                                       // (chunks < 2^23, parts <= 32)
+        it.t0 = most * part / parts;
+        t1 = most * (part + 1) / parts;
+    }
+    it.e[0] = max(it.t0, min(e0, t1));
+    it.e[1] = max(it.t0, min(e1, t1));
     // the last key that every row of the first tile with chunks sees
     const int seen = p.causal ? min(it.pos0 + (it.e[0] > it.t0 ? 0 : p.tokens), it.L - 1) : it.L - 1;
     it.edge = max(0, seen + 1) / PT_M;
-    it.slot = p.shared ? (prompt_slot(s.row0, it.idx, t, p.tokens) * p.Hkv + it.h) * parts + part
-              : parts > 1 ? v - c.whole : -1;
+    it.slot = p.shared ? (prompt_slot(p, s.x, it.idx, t) * p.Hkv + it.h) * parts + part : parts > 1 ? v - c.whole : -1;
     return it;
 }
 
@@ -480,7 +439,7 @@ struct PromptKernel {
     }
 
     // ---------------- scheduler: one warp finds the CTA's items ----------------
-    static __device__ void schedule(const PromptParams& p, PromptBars* b, PromptItem* items, PromptFix* fix, int2* known) {
+    static __device__ void schedule(const PromptParams& p, PromptBars* b, PromptItem* items, PromptFix* fix, int4* known) {
         const int lane = threadIdx.x & 31;
         PromptOrder order;
         order.init(p, known, blockIdx.x == 0);
@@ -1120,7 +1079,7 @@ prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ CU
         } else if (warp == 9) {
             K::producer(p, base, full, empty, b, items, bad, &tq, &tk, &tv);
         } else if (warp == 10) {
-            K::schedule(p, b, items, fix, reinterpret_cast<int2*>(base + Lay::KNOWN));
+            K::schedule(p, b, items, fix, reinterpret_cast<int4*>(base + Lay::KNOWN));
         } else if (warp == 11) {
             K::mend(p, base, full, b, items, fix);
         } else {

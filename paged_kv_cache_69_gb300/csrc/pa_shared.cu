@@ -53,7 +53,7 @@ shared_merge_kernel(const __grid_constant__ DecodeParams p, const __grid_constan
     size_t at1 = 0;
     if (q.L > 0) {
         const int j = i - q.row0, t = j / (2 * s.tokens), u = j - t * 2 * s.tokens, tile = u >= s.tokens;
-        const size_t slot = (static_cast<size_t>(prompt_slot(q.row0, g, t, s.tokens)) * s.Hkv + h / s.G) * parts;
+        const size_t slot = (static_cast<size_t>(prompt_slot(s, q.row0, g, t)) * s.Hkv + h / s.G) * parts;
         at1 = (slot * 2 + tile) * PT_M + (u - tile * s.tokens) * s.G + h % s.G;
         n1 = parts;
     }
