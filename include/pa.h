@@ -232,10 +232,11 @@ pa_status pa_decode_weights(void* out, float* weights, const void* q, pa_dtype q
  * request, conversations about one document, a common system prompt): the keys of a
  * prefix are read once for all sequences of its group.
  * Group j holds the sequences group_start[j] .. group_start[j+1]-1, whose first
- * prefix_lens[j] tokens lie in the same blocks: the block table of the group's first
- * sequence is read for them, for the rest each sequence's own.  A prefix that ends
- * inside a block counts up to that block.  Lengths, tables and results are those of
- * pa_decode; groups of one, prefixes of 0 and sequences in no group are fine.
+ * prefix_lens[j] tokens lie in the same blocks: all their tables name those blocks,
+ * and the first one's is read for the group (each its own where there is too little to
+ * share to pay for it: fewer than 2048 tokens' reads saved).  A prefix that ends inside a
+ * block counts up to that block.  Lengths, tables and results are those of pa_decode;
+ * groups of one, prefixes of 0 and sequences in no group are fine.
  *   group_start       int32 [num_groups + 1] on the device, non-decreasing within
  *                     [0, num_seqs].  A group whose entries do not fit is passed over
  *                     with PA_ERRBIT_BAD_QUERY: its sequences attend by themselves.

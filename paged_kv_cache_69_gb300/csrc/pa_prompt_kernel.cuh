@@ -134,15 +134,19 @@ struct PromptSeq {
     int a, c;                          // level of the first item, items
 };
 
-// Shared mode: a group of fewer (sequence, head) rows than this, or with fewer
-// shared tokens, is left to the decode kernel, prefix and all.
-constexpr int PT_SHARED_ROWS = 8, PT_SHARED_KEYS = 64;
+// Shared mode: groups that would save fewer reads of a token than this are left to the
+// decode kernel, prefix and all.  (28/4 heads x 128, 32 groups: two members with 1024
+// tokens 46 us shared, 41 left to it; four, which save 3072, 52 and 54; two with 4096
+// tokens 84 and 103.)
+constexpr int PT_SHARED_SAVED = 2048;
 
-// The tokens of group i's prefix that are attended once: whole blocks.
+// The tokens that group i shares, in whole blocks, and those of them that are attended once.
+__device__ __forceinline__ int group_prefix(const PromptParams& p, int i) {
+    return max(0, min(__ldg(p.seq_lens + i), p.MB * p.bs)) & ~(p.bs - 1);
+}
 __device__ __forceinline__ int shared_prefix(const PromptParams& p, int i, int n) {
-    const int P = __ldg(p.seq_lens + i);
-    if (P < PT_SHARED_KEYS || n * p.G < PT_SHARED_ROWS) return 0;
-    return min(P, p.MB * p.bs) & ~(p.bs - 1);
+    const int P = group_prefix(p, i);
+    return static_cast<long long>(n - 1) * P >= PT_SHARED_SAVED ? P : 0;
 }
 
 __device__ __forceinline__ int prompt_items_of(const PromptParams& p, int n) {
@@ -1007,9 +1011,13 @@ __device__ __forceinline__ int prompt_seq_of(const PromptParams& p, int row) {
 __device__ __forceinline__ void write_tails(const PromptParams& p) {
     for (int i = blockIdx.x * PT_THREADS + threadIdx.x; i < p.total_q; i += gridDim.x * PT_THREADS) {
         const int g = prompt_seq_of(p, i);
-        const int P = g >= 0 ? prompt_seq(p, g, false).L : 0;
+        int P = 0, least = 0;
+        if (g >= 0) {
+            P = prompt_seq(p, g, false).L;
+            least = group_prefix(p, g);
+        }
         const int L = __ldg(p.lens + i);
-        const bool ok = L >= P && L <= p.MB * p.bs;
+        const bool ok = L >= max(P, least) && L <= p.MB * p.bs;
         p.tail_lens[i] = ok ? L - P : -1;
         p.tail_blk[i] = P / p.bs;
     }

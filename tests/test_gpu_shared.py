@@ -79,8 +79,9 @@ class Case:
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("Hq,Hkv", [(1, 1), (4, 2), (28, 4), (24, 8), (16, 1)])
 def test_groups_of_all_kinds(dtype, D, Hq, Hkv):
-    groups = [(256, [5, 300, 1, 17]), (0, [40, 3]), (64, [9]), (1000, [1, 2, 0, 30, 20, 700]), (48, [1] * 11), (128, [0, 0]),
-              (16, [5, 5])]
+    # (some share so little that they are left to the decode kernel)
+    groups = [(768, [5, 300, 1, 17]), (0, [40, 3]), (64, [9]), (1000, [1, 2, 0, 30, 20, 700]), (48, [1] * 11), (2176, [0, 0]),
+              (16, [5, 5]), (256, [3] * 9), (4000, [7])]
     c = Case(groups, Hq, Hkv, D, dtype, seed=Hq)
     c.check(c.call())
 
@@ -88,7 +89,8 @@ def test_groups_of_all_kinds(dtype, D, Hq, Hkv):
 @pytest.mark.parametrize("bs", [8, 16, 32, 64, 128])
 def test_block_sizes_and_prefixes_inside_a_block(bs):
     """What lies behind the prefix's last whole block is each sequence's own."""
-    c = Case([(bs * 7 + 3, [5, 40, 1] * 5), (bs - 1, [1, 2] * 6), (bs * 20, [0, 9] * 4)], 8, 2, 128, F16, bs=bs)
+    c = Case([(bs * 40 + 3, [5, 40, 1] * 5), (bs - 1, [1, 2] * 6), (bs * 20 + 256, [0, 9] * 4), (bs * 7, [2] * 4)], 8, 2, 128, F16,
+             bs=bs)
     c.check(c.call())
 
 
@@ -111,11 +113,12 @@ def test_long_prefix_and_long_tails():
 
 
 def test_no_group_and_sequences_in_none():
-    c = Case([(300, [5, 6, 7, 8]), (200, [9, 10])], 16, 2, 64, F16)
+    c = Case([(900, [5, 6, 7, 8]), (2100, [9, 10])], 16, 2, 64, F16)
     want = c.want()
-    for starts, prefix, bits in (([0], [], 0), ([0, 4], [300], 0), ([4, 6], [200], 0), ([0, 0, 4, 4, 6], [50, 300, 9, 200], 0),
-                                 ([0, 2, 1, 6], [300, 200, 0], pa.ERRBIT_BAD_QUERY), ([0, 4, 9], [300, 200], pa.ERRBIT_BAD_QUERY),
-                                 ([-1, 4, 6], [300, 200], pa.ERRBIT_BAD_QUERY), ([0, 4, 6], [300, -5], 0)):
+    for starts, prefix, bits in (([0], [], 0), ([0, 4], [900], 0), ([4, 6], [2100], 0),
+                                 ([0, 0, 4, 4, 6], [50, 900, 9, 2100], 0), ([0, 2, 1, 6], [900, 800, 0], pa.ERRBIT_BAD_QUERY),
+                                 ([0, 4, 9], [900, 2100], pa.ERRBIT_BAD_QUERY), ([-1, 4, 6], [900, 2100], pa.ERRBIT_BAD_QUERY),
+                                 ([0, 4, 6], [900, -5], 0), ([0, 4, 6], [-2 ** 31, 700], 0)):
         c.starts, c.prefix = c.dev(starts), c.dev(prefix)
         c.err.zero_()
         out = c.call()
@@ -124,21 +127,22 @@ def test_no_group_and_sequences_in_none():
 
 
 def test_lengths_that_do_not_fit():
-    c = Case([(320, [5, 6, 7, 8]), (200, [9, 10])], 16, 2, 64, F16)
-    want, tol = c.want()
-    c.lens[1], c.lens[5] = 300, c.tables.shape[1] * 16 + 1
-    out = c.call()
-    assert c.err.item() == pa.ERRBIT_SEQ_TOO_LONG
-    assert (out[1] == 7).all() and (out[5] == 7).all()
-    keep = torch.tensor([0, 2, 3, 4], device="cuda")
-    ref.check(out[keep], want[keep], tol[keep])
+    for shared in (320, 960):
+        c = Case([(shared, [5, 6, 7, 8]), (200, [9, 10])], 16, 2, 64, F16)
+        want, tol = c.want()
+        c.lens[1], c.lens[5] = shared - 20, c.tables.shape[1] * 16 + 1
+        out = c.call()
+        assert c.err.item() == pa.ERRBIT_SEQ_TOO_LONG
+        assert (out[1] == 7).all() and (out[5] == 7).all()
+        keep = torch.tensor([0, 2, 3, 4], device="cuda")
+        ref.check(out[keep], want[keep], tol[keep])
 
 
 def test_blocks_outside_the_pool_are_left_out():
-    c = Case([(320, [5, 60, 7, 8]), (200, [9, 10])], 16, 2, 64, F16)
+    c = Case([(960, [5, 60, 7, 8]), (200, [9, 10])], 16, 2, 64, F16)
     want, tol = c.want()
     own = c.tables.clone()
-    c.tables[1, 21] = -3                                   # tokens 336..351 of sequence 1
+    c.tables[1, 61] = -3                                   # tokens 976..991 of sequence 1
     out = c.call()
     assert c.err.item() == pa.ERRBIT_BAD_BLOCK
     keep = torch.tensor([0, 2, 3, 4, 5], device="cuda")
@@ -159,15 +163,15 @@ def test_blocks_outside_the_pool_are_left_out():
 
 @pytest.mark.parametrize("scale", [-0.4, 0.0, 2.0])
 def test_scales(scale):
-    c = Case([(200, [5, 60, 7, 8]), (100, [9, 10])], 16, 2, 128, F16, scale=scale)
+    c = Case([(900, [5, 60, 7, 8]), (100, [9, 10])], 16, 2, 128, F16, scale=scale)
     c.check(c.call())
 
 
 def test_nan_and_infinity():
     """In the prefix they reach every member, in a tail only its own sequence."""
-    c = Case([(256, [5, 20, 7, 8])], 8, 1, 64, BF16)
+    c = Case([(1024, [5, 20, 7, 8])], 8, 1, 64, BF16)
     before = c.call()
-    blk, off = int(c.tables[2, 16]), 3
+    blk, off = int(c.tables[2, 64]), 3
     c.v[blk, off, 0, 9] = math.inf
     out = c.call()
     hit = torch.zeros_like(out, dtype=torch.bool)
@@ -178,7 +182,7 @@ def test_nan_and_infinity():
 
 
 def test_same_bits_again_and_from_a_graph():
-    c = Case([(512, [5, 20, 7, 100]), (300, [50, 60])], 28, 4, 128, F16, spare=60)
+    c = Case([(1024, [5, 20, 7, 100]), (300, [50, 60])], 28, 4, 128, F16, spare=60)
     once = c.call()
     assert torch.equal(c.call(), once)
     ws = torch.empty(pa.pa_decode_shared_workspace_size(6, 2, 28, 4, c.tables.shape[1] * 16, 128), dtype=torch.uint8,
@@ -204,7 +208,7 @@ def test_same_bits_again_and_from_a_graph():
 
 
 def test_two_calls_at_once():
-    a = Case([(512, [5, 20, 7, 100])], 28, 4, 128, F16)
+    a = Case([(1024, [5, 20, 7, 100])], 28, 4, 128, F16)
     b = Case([(700, [5] * 40)], 8, 2, 64, BF16)
     wa, wb = a.call(), b.call()
     s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
@@ -230,7 +234,7 @@ def test_a_request_from_prompt_to_shared_decode():
     """The calls as a serving loop makes them: a prompt rotated and cached, attended,
     forked into branches, and two decode steps of all branches, against dense attention
     over the rotated rows."""
-    Hq, Hkv, D, bs, n, branches = 8, 2, 64, 16, 150, 6
+    Hq, Hkv, D, bs, n, branches = 8, 2, 64, 16, 603, 6
     g = torch.Generator().manual_seed(1)
     rnd = lambda *s: torch.randn(*s, generator=g).to(F16).cuda()  # noqa: E731
     table = pa.rope_table(1000, D)
@@ -273,5 +277,5 @@ def test_a_request_from_prompt_to_shared_decode():
             keys[b].append(key[b:b + 1])
             values[b].append(v[b:b + 1])
             want, tol = ref.attend(q[b:b + 1], torch.cat(keys[b]), torch.cat(values[b]), scale, dev([n + step]))
-            ref.check(out[b:b + 1], want, tol + 200 * 2.0 ** -25 * 5)
+            ref.check(out[b:b + 1], want, tol + 700 * 2.0 ** -25 * 5)
     assert err.item() == 0
