@@ -145,7 +145,7 @@ pa_status launch_prompt(const PromptCall& c, const PromptPlan& plan, void* parts
     const cuuint64_t D2 = static_cast<cuuint64_t>(c.D) * 2, planes = c.D / 64;
     alignas(64) CUtensorMap tq, tk, tv;
     CUresult r = encode4(&tq, c.dtype, c.q, c.Hq, c.total_q, planes, D2, D2 * c.Hq, G, p.tokens);
-    const void* src[2] = {c.k, c.v};
+    const void* src[2] = {c.k ? c.k : c.q, c.v ? c.v : c.q};     // (no keys: nothing is read)
     CUtensorMap* map[2] = {&tk, &tv};
     for (int x = 0; x < 2 && r == CUDA_SUCCESS; ++x)
         r = c.k_start ? encode4(map[x], c.dtype, src[x], std::max(c.total_k, 1), c.Hkv, planes, D2 * c.Hkv, D2, PT_M, 1)
@@ -174,7 +174,8 @@ static pa_status prefill(const PromptCall& c, pa_dtype kv_dtype, void* workspace
     if (c.B < 0 || c.Hq <= 0 || c.Hkv <= 0 || c.D <= 0 || c.total_q < 0 || c.total_k < 0 || c.bs <= 0 || c.NB <= 0 || c.MB <= 0)
         return bad(c, PA_ERR_INVALID_ARG, "sizes must be positive (num_seqs and row counts >= 0)");
     if (c.B == 0 || c.total_q == 0) return PA_OK;
-    if (!c.out || !c.q || !c.k || !c.v || !c.q_start || !(c.k_start || (c.block_tables && c.seq_lens)))
+    const bool keys = !c.k_start || c.total_k > 0;         // without keys there are no K and V
+    if (!c.out || !c.q || (keys && (!c.k || !c.v)) || !c.q_start || !(c.k_start || (c.block_tables && c.seq_lens)))
         return bad(c, PA_ERR_INVALID_ARG, "null pointer");
     if (!valid_dtype(c.dtype) || !valid_cache_dtype(kv_dtype)) return bad(c, PA_ERR_INVALID_ARG, "unknown dtype");
     if (c.Hq % c.Hkv != 0) return bad(c, PA_ERR_INVALID_ARG, "num_q_heads must be a multiple of num_kv_heads");

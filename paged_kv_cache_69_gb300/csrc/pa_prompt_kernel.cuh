@@ -14,21 +14,44 @@
 //
 // How.  The query heads of a KV head's group are packed: tile row u is token
 // u / G, head u % G, so that K and V are read once for the whole group.  An item
-// is 2 x 128 rows of one (sequence, KV head) and its keys, 128 at a time:
-//   - one producer warp finds the items and copies Q, K and V by TMA (128-byte
-//     swizzle; paged K and V block by block through the table);
+// is 2 x 128 rows of one (sequence, KV head) and its keys, 128 at a time, and the
+// warps of a CTA have a role each:
+//   - the scheduler finds the items, the producer copies Q, K and V by TMA (128-byte
+//     swizzle; paged K and V block by block through the table, K and V in a ring of
+//     four tiles, eight at head_dim 64);
 //   - one thread issues S_q = Q_q K^T and O_q += P_q V (q = 0, 1) as 128x128x16
 //     MMAs; S, P and O live in tensor memory (P over the columns of its S);
 //   - two groups of four warps run the softmax, one row per thread: while one of
-//     them works on its S, the tensor cores work for the other.
+//     them works on its S, the tensor cores work for the other;
+//   - one warp keeps values that some row must not see from reaching it, four
+//     write finished rows out while the next item's softmax is under way.
 // Order of the MMAs: ... P0 V(j), S0(j+1), P1 V(j), S1(j+1) ...; a commit covers
 // everything issued before it, so "S_q(j+1) is there" also says that P_q V(j) is
 // in O_q, and the softmax warps may rescale O_q without a barrier of its own.
 //
 // CTAs are persistent.  Items go out by length, longest first and in turns of
 // alternating direction, which balances causal items without a counter in memory;
-// with fewer items than CTAs each is cut into `splits` ranges of keys, merged
-// by prompt_merge_kernel.
+// what is left of the last round (with few items, everything) is cut into ranges of
+// keys, merged by prompt_merge_kernel.
+//
+// What bounds it, and what it measured.  A chunk takes a tile 4 x 128 x 128 x D
+// flop: 1024 cycles at D = 128 if the tensor cores never wait.  One prompt of 32768
+// tokens, 32/8 heads x 128, bf16: 4.8 ms, 1840 TFLOP/s (cuBLAS: 1980); D = 64 is
+// bound by the softmax instead.  On the way there:
+//   - MMAs and copies issued by an elected thread, whose operands the compiler may
+//     keep in uniform registers (7.15 -> 5.3 ms; under `lane == 0` every MMA cost some
+//     100 cycles to issue);
+//   - P handed over in two parts (5.3 -> 5.1; four parts 5.1, and more to wait for);
+//   - the roles' code kept small, since ten of them share the instruction cache: short
+//     waits, rolled loops beside the hot ones (256 short prompts 627 -> 502 us);
+//   - rows written out by warps of their own, items found by 32 bands of levels in
+//     few instructions (502 -> 447; the first item is there after 9000 cycles, which
+//     were 34000).
+// Short prompts stay bound by what an item costs beside its chunks, about 8000 cycles.
+// Not kept: the next item's scores ahead of the last products (no gain, more code);
+// one tile's rows in both tiles, the chunks in turn (no gain: such items are bound by
+// memory); skipping masked columns and key steps (the tests cost more); one lane per
+// block's copy.
 #pragma once
 
 #include <cuda.h>
@@ -79,7 +102,7 @@ struct PromptParams {
     uint32_t negate;                   // instruction descriptor bit of -Q, for scale < 0
 };
 
-// An item as the producer hands it on.
+// An item as the scheduler hands it on.
 struct PromptItem {
     int live;                          // 0: no more items (the rest is unset)
     int row0, ntok;                    // first query row, query tokens of both tiles
@@ -432,14 +455,23 @@ struct PromptKernel {
 
     // Every wait ends after 2^31 cycles (about a second) at the latest.  The instructions
     // are few: what the ten roles of this kernel run has to share the instruction cache.
+    // A wait for something that comes once per item may take as long as the item, of up to
+    // 2^23 chunks: 16 times as much.
+    template <int ROUNDS = 1>
     static __device__ __forceinline__ bool wait(const PromptParams& p, uint64_t* bar, uint32_t parity) {
         if (mbar_try_wait(bar, parity)) return true;
-        const uint32_t t0 = static_cast<uint32_t>(clock());
-        do {
-            if (mbar_try_wait(bar, parity)) return true;
-        } while (static_cast<uint32_t>(clock()) - t0 < 0x80000000u);
+#pragma unroll 1
+        for (int x = 0; x < ROUNDS; ++x) {
+            const uint32_t t0 = static_cast<uint32_t>(clock());
+            do {
+                if (mbar_try_wait(bar, parity)) return true;
+            } while (static_cast<uint32_t>(clock()) - t0 < 0x80000000u);
+        }
         raise_flag(p.err_flag, PA_ERRBIT_WAIT_TIMEOUT);
         return false;
+    }
+    static __device__ __forceinline__ bool wait_item(const PromptParams& p, uint64_t* bar, uint32_t parity) {
+        return wait<16>(p, bar, parity);
     }
 
     // ---------------- scheduler: one warp finds the CTA's items ----------------
@@ -454,7 +486,7 @@ struct PromptKernel {
         for (int turn = 0;; ++turn) {
             const int slot = turn % PT_ITEMS;
             bool ok = true;
-            if (turn >= PT_ITEMS) ok = wait(p, &b->i_empty[slot], (turn / PT_ITEMS - 1) & 1u);
+            if (turn >= PT_ITEMS) ok = wait_item(p, &b->i_empty[slot], (turn / PT_ITEMS - 1) & 1u);
             if (!__all_sync(0xffffffffu, ok)) return;
             // turns of alternating direction: CTA b takes b, 2 grid - 1 - b, 2 grid + b, ...
             // (k is below the next turn's first number: behind the last item there are no more turns)
@@ -500,7 +532,7 @@ struct PromptKernel {
         bool ok = true;
         for (int turn = 0; ok; ++turn) {
             const int is = turn % PT_ITEMS;
-            ok = __all_sync(0xffffffffu, wait(p, &b->i_full[is], (turn / PT_ITEMS) & 1u));
+            ok = __all_sync(0xffffffffu, wait_item(p, &b->i_full[is], (turn / PT_ITEMS) & 1u));
             if (!ok) break;
             const PromptItem it = items[is];
             __syncwarp();
@@ -657,7 +689,7 @@ struct PromptKernel {
         };
         for (int turn = 0; ok; ++turn) {
             const int is = turn % PT_ITEMS;
-            if (!(ok = wait(p, &b->i_full[is], (turn / PT_ITEMS) & 1u))) break;
+            if (!(ok = wait_item(p, &b->i_full[is], (turn / PT_ITEMS) & 1u))) break;
             const PromptItem it = items[is];
             mbar_arrive(&b->i_empty[is]);
             if (!it.live) break;
@@ -750,7 +782,7 @@ struct PromptKernel {
         uint32_t edges = 0;
         for (int turn = 0;; ++turn) {
             const int is = turn % PT_ITEMS;
-            if (!__all_sync(0xffffffffu, wait(p, &b->i_full[is], (turn / PT_ITEMS) & 1u))) return;
+            if (!__all_sync(0xffffffffu, wait_item(p, &b->i_full[is], (turn / PT_ITEMS) & 1u))) return;
             const PromptItem it = items[is];
             if (!it.live) return;
             const int t1 = max(it.e[0], it.e[1]);
@@ -759,7 +791,7 @@ struct PromptKernel {
                 const int vs = stage + 2 * (t - it.t0);
                 // (full alone would not do: it may be rounds behind or ahead of a warp that
                 // looks at some chunks only)
-                if (!__all_sync(0xffffffffu, wait(p, &b->v_there, edges & 1u) && wait(p, &full[vs % S], (vs / S) & 1u))) return;
+                if (!__all_sync(0xffffffffu, wait_item(p, &b->v_there, edges & 1u) && wait(p, &full[vs % S], (vs / S) & 1u))) return;
                 uint8_t* v = base + Lay::KV + (vs % S) * Lay::TILE;
                 const int lo = max(0, seen + 1 - t * PT_M), tail = min(PT_M, it.L - t * PT_M);
                 // is there anything to mend from the 8-row group of row lo on?  0 * x is NaN for an
@@ -809,7 +841,7 @@ struct PromptKernel {
         int chunk = 0;                                     // chunks of the items before
         for (int turn = 0;; ++turn) {
             const int is = turn % PT_ITEMS;
-            if (!__all_sync(0xffffffffu, wait(p, &b->i_full[is], (turn / PT_ITEMS) & 1u))) return;
+            if (!__all_sync(0xffffffffu, wait_item(p, &b->i_full[is], (turn / PT_ITEMS) & 1u))) return;
             const PromptItem it = items[is];
             if (!it.live) return;
             const int t1 = it.e[q];
@@ -932,7 +964,7 @@ struct PromptKernel {
         uint32_t n[2] = {0, 0};
         for (int turn = 0;; ++turn) {
             const int is = turn % PT_ITEMS;
-            if (!__all_sync(0xffffffffu, wait(p, &b->i_full[is], (turn / PT_ITEMS) & 1u))) return;
+            if (!__all_sync(0xffffffffu, wait_item(p, &b->i_full[is], (turn / PT_ITEMS) & 1u))) return;
             const PromptItem it = items[is];
             if (!it.live) return;
             const bool direct = it.slot < 0;
@@ -956,7 +988,7 @@ struct PromptKernel {
                     continue;
                 }
                 const uint32_t phase = n[q]++ & 1u;
-                if (!__all_sync(0xffffffffu, wait(p, &b->l_full[is][q], (turn / PT_ITEMS) & 1u) && wait(p, &b->o_full[q], phase))) return;
+                if (!__all_sync(0xffffffffu, wait_item(p, &b->l_full[is][q], (turn / PT_ITEMS) & 1u) && wait_item(p, &b->o_full[q], phase))) return;
                 tc05_fence_after();
                 const float2 ml = rows[(is * 2 + q) * PT_M + r];
                 const float inv = !direct ? 1.f : ml.y != 0.f ? 1.f / ml.y : 0.f;

@@ -306,3 +306,9 @@ def test_items_about_a_round(Hkv):
         o, t = ref.attend(c.q[rows.cuda()], c.k, c.v, c.scale, (rows + 3000).cuda())
         ref.check(out[rows.cuda()], o, t)
         assert c.err.item() == 0
+
+
+def test_no_keys_at_all():
+    c = Case([0, 0], 4, 2, 64, F16, q_lens=[3, 5])
+    out = c.flat()
+    assert c.k.shape[0] == 0 and (out == 0).all() and c.err.item() == 0
