@@ -159,8 +159,7 @@ struct PromptSeq {
 
 // Shared mode: groups that would save fewer reads of a token than this are left to the
 // decode kernel, prefix and all.  (28/4 heads x 128, 32 groups: two members with 1024
-// tokens 46 us shared, 41 left to it; four, which save 3072, 52 and 54; two with 4096
-// tokens 84 and 103.)
+// tokens 46 us shared, 41 left to it; four 52 and 54; two with 4096 tokens 84 and 103.)
 constexpr int PT_SHARED_SAVED = 2048;
 
 // The tokens that group i shares, in whole blocks, and those of them that are attended once.
@@ -342,6 +341,8 @@ __device__ __forceinline__ PromptItem prompt_item(const PromptParams& p, PromptO
     int4 s;
     int t;
     order.find(p, kk, it.idx, s, t);
+    // (q_start that falls again and again could count past 32 bits)
+    t = max(0, min(t, prompt_items_of(p, s.y) - 1));
     it.live = 1;
     it.h = k - kk * p.Hkv;
     it.row0 = s.x + t * TT;
