@@ -30,7 +30,8 @@ struct PromptPlan {
     size_t cut_bytes = 0, ml_bytes = 0, acc_bytes = 0;     // 0 without partials
     size_t bytes() const { return cut_bytes + ml_bytes + acc_bytes; }
 };
-PromptPlan prompt_plan(int B, int total_q, int Hq, int Hkv, int D, int max_keys, bool shared, int sms);
+PromptPlan prompt_plan(int B, int total_q, int Hq, int Hkv, int D, int max_keys, bool prompts, bool shared,
+                       int sms);
 // Room for any call of at most these numbers (a workspace made once serves smaller calls).
 size_t prompt_part_bytes(int B, int total_q, int Hq, int Hkv, int D, bool shared, int sms);
 

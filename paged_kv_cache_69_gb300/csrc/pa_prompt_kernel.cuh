@@ -32,7 +32,7 @@
 // CTAs are persistent.  Items go out by length, longest first and in turns of
 // alternating direction, which balances causal items without a counter in memory;
 // what is left of the last round (with few items, everything) is cut into ranges of
-// keys, merged by prompt_merge_kernel.
+// keys where that pays, merged by prompt_merge_kernel.
 //
 // What bounds it, and what it measured.  A chunk takes a tile 4 x 128 x 128 x D
 // flop: 1024 cycles at D = 128 if the tensor cores never wait.  One prompt of 32768
@@ -91,7 +91,7 @@ struct PromptParams {
     int tokens;                        // query tokens per tile, 128 / G
     int splits, causal, shared;        // splits: the most ranges that an item may be cut into
     int grid;                          // CTAs
-    int4* cut;                         // for the merge: (ranges, cut items), and each one's (first row, tokens, head, place)
+    int4* cut;                         // for the merge: (b, cut items, a), and each one's (first row, tokens, head, place)
     // shared mode: lengths of the sequences, and what the decode kernel behind takes
     const int32_t* lens;               // [total_q]
     int32_t *tail_lens, *tail_blk;
@@ -292,31 +292,69 @@ struct PromptOrder {
     }
 };
 
-// How the items of a launch are cut: the first `whole` not at all, the others into
-// `parts` ranges of keys each.
+// How the items of a launch are cut: the first `whole` not at all; the others, one behind
+// the other, into spans of a / b items each, a < b (or not at all, b = 1).  A span is at
+// most the end of an item and the start of the next; all spans end at multiples of 1 / b of
+// an item, so that items of one length read the same keys at the same time.
 struct PromptCut {
-    int whole, parts;
+    int whole, a, b;
 };
-// CTAs take whole rounds of items; what is left of the last round, the lightest
-// items, is cut so that all CTAs have part of it (in shared mode all items).  With r
-// items of w chunks in s ranges the last rounds take ceil(r s / grid) (w / s + 6)
-// chunks' time (an item costs about 6 beside its chunks), and a merge 8.  w: that of the
-// longest item times the share of items that are as light as these or lighter.
+// CTAs take whole rounds of items; what is left of the last round, the lightest items, is
+// cut so that all CTAs have part of it.  (In shared mode all items are cut into b parts each.)
+// With r items left, spans of a / b take ceil(w a / b) chunks' time of items of w chunks, and 6
+// for each item that they are of (what an item costs beside its chunks); the merge takes 8.
+// The rounds before leave CTAs unequal, so that the first, middle and last span count with
+// what their CTA had before, and so does the last CTA.
+// (2048 tokens behind 63488, 32/8 heads, 256 items: 1292 us, uncut 1354.  512 tokens each behind
+// 100-8192, 28/4 heads, 232 items of unequal length: 126 uncut, 139 cut as if all were equal.)
 __device__ __forceinline__ PromptCut prompt_cut(const PromptParams& p, const PromptOrder& order) {
     const int items = order.total * p.Hkv;
-    PromptCut c{items, 1};
+    PromptCut c{items, 1, 1};
     if (p.splits == 1) return c;
     const float grid = static_cast<float>(p.grid);
-    c.whole = p.shared ? 0 : static_cast<int>(floorf(__fdividef(items + 0.5f, grid))) * p.grid;
+    const int R = p.shared ? 0 : static_cast<int>(floorf(__fdividef(items + 0.5f, grid)));
+    c.whole = R * p.grid;
     const float r = static_cast<float>(items - c.whole);
     if (r == 0.f) return c;
-    const float longest = static_cast<float>(order.top + 2) * static_cast<float>(2 * p.tokens) * (1.f / PT_M);
-    const float w = fmaxf(1.f, ceilf(longest * __fdividef(r, static_cast<float>(items))));
-    const float k = static_cast<float>((threadIdx.x & 31) + 1);
-    float cost = ceilf(__fdividef(r * k - 0.5f, grid)) * (ceilf(__fdividef(w, k) - 0.01f) + 6.f) + (k > 1.f && !p.shared ? 8.f : 0.f);
-    if (k > 1.f && (k > static_cast<float>(p.splits) || k > w || k * r > 2.f * grid)) cost = 1e9f;
+    const float b = static_cast<float>((threadIdx.x & 31) + 1);
+    const float full = ceilf(__fdividef(r * b - 0.5f, grid));
+    const float a = p.shared ? 1.f : full, rounds = p.shared ? full : 1.f, part = __fdividef(a, b);
+    const int spans = static_cast<int>(ceilf(__fdividef(r, part) - 0.01f));
+    const int at[4] = {0, spans >> 1, spans - 1, p.grid - 1};      // places in the last round
+    const int bands = order.shift == 31 ? 1 : 32;
+    float w = 0.f, load[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+    for (int t = 0; t <= R; ++t) {
+        int rank[4], u[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            const int i = t == R ? static_cast<int>(at[y] * part) : (t ^ R) & 1 ? p.grid - 1 - at[y] : at[y];
+            rank[y] = static_cast<int>(div_by(max(0, t * p.grid + i), p.div_hkv));
+            u[y] = 0;
+        }
+#pragma unroll 1
+        for (int x = 1; x < bands; ++x) {
+            const int n = __shfl_sync(0xffffffffu, order.above, x);
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+                if (n > rank[y]) u[y] = x;
+        }
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            // chunks of the longest item of the band
+            const int level = order.shift == 31 ? order.top : min(order.top, ((u[y] + 1) << order.shift) - 1);
+            const float n = fmaxf(1.f, ceilf(static_cast<float>(level + 2) * static_cast<float>(2 * p.tokens) * (1.f / PT_M)));
+            if (y == 0) w = n;
+            if (t < R) load[y] += n + 6.f;
+            else if (y < 3) load[y] += ceilf(n * part - 0.01f) + (a > 1.f ? 12.f : 6.f);
+        }
+    }
+    float cost = rounds * fmaxf(fmaxf(load[0], load[1]), fmaxf(load[2], load[3])) + (b > 1.f && !p.shared ? 8.f : 0.f);
+    if (b > 1.f && (b > static_cast<float>(p.splits) || b > w || a >= b || r * b > 2.f * grid * a)) cost = 1e9f;
     // the cheapest, of equal ones the first: costs are whole numbers below 2^26
-    c.parts = (__reduce_min_sync(0xffffffffu, static_cast<uint32_t>(fminf(cost, 6.7e7f)) << 5 | (threadIdx.x & 31)) & 31) + 1;
+    const int best = __reduce_min_sync(0xffffffffu, static_cast<uint32_t>(fminf(cost, 6.7e7f)) << 5 | (threadIdx.x & 31)) & 31;
+    c.b = best + 1;
+    c.a = static_cast<int>(__shfl_sync(0xffffffffu, a, best));
     return c;
 }
 
@@ -326,15 +364,25 @@ __device__ __forceinline__ int prompt_slot(const PromptParams& p, int row0, int 
     return static_cast<int>(div_by(row0, p.div_tt)) + i + t;
 }
 
-// Number v in the order of a launch cut as c says.
-__device__ __forceinline__ PromptItem prompt_item(const PromptParams& p, PromptOrder& order, const PromptCut& c, int v) {
+// Number v in the order of a launch cut as c says: an item, or a span's first part or, second
+// set, its other.  more: there is another; first: for an item's first part the item's number
+// among the cut ones, else -1.
+__device__ __forceinline__ PromptItem prompt_item(const PromptParams& p, PromptOrder& order, const PromptCut& c, int v,
+                                                  bool second, int& first, bool& more) {
     const int TT = 2 * p.tokens;
-    int k = v, part = 0, parts = 1;
-    if (v >= c.whole) {                                    // cut items: at most two to a CTA
-        parts = c.parts;
-        k = static_cast<int>(__fdividef(v - c.whole + 0.5f, static_cast<float>(parts)));
-        part = v - c.whole - k * parts;
-        k += c.whole;
+    int k = v, from = 0, to = c.b, place = -1;             // parts from / b to to / b of item k
+    first = -1;
+    more = false;
+    if (v >= c.whole && c.b > 1) {                         // at most two spans to a CTA
+        const int span = v - c.whole;
+        const int i = static_cast<int>(__fdividef(span * c.a + 0.5f, static_cast<float>(c.b))) + (second ? 1 : 0);
+        k = c.whole + i;
+        from = max(0, span * c.a - i * c.b);
+        to = (span + 1) * c.a - i * c.b;
+        more = to > c.b && k + 1 < order.total * p.Hkv;
+        to = min(to, c.b);
+        place = span + i;                                  // those of an item one behind the other
+        if (from == 0) first = i;
     }
     const int kk = static_cast<int>(div_by(k, p.div_hkv));
     PromptItem it{};
@@ -355,16 +403,16 @@ __device__ __forceinline__ PromptItem prompt_item(const PromptParams& p, PromptO
     const int e1 = n1 > 0 ? max(0, (p.causal ? it.pos0 + it.ntok : s.z) + PT_M - 1) / PT_M : 0;
     const int most = max(e0, e1);
     int t1 = most;
-    if (parts > 1) {                                       // (chunks < 2^23, parts <= 32)
-        it.t0 = most * part / parts;
-        t1 = most * (part + 1) / parts;
+    if (c.b > 1) {                                         // (chunks < 2^23, b <= 32)
+        it.t0 = most * from / c.b;
+        t1 = most * to / c.b;
     }
     it.e[0] = max(it.t0, min(e0, t1));
     it.e[1] = max(it.t0, min(e1, t1));
     // the last key that every row of the first tile with chunks sees
     const int seen = p.causal ? min(it.pos0 + (it.e[0] > it.t0 ? 0 : p.tokens), it.L - 1) : it.L - 1;
     it.edge = max(0, seen + 1) / PT_M;
-    it.slot = p.shared ? (prompt_slot(p, s.x, it.idx, t) * p.Hkv + it.h) * parts + part : parts > 1 ? v - c.whole : -1;
+    it.slot = p.shared ? (prompt_slot(p, s.x, it.idx, t) * p.Hkv + it.h) * c.b + from : place;
     return it;
 }
 
@@ -480,25 +528,32 @@ struct PromptKernel {
         const int lane = threadIdx.x & 31;
         PromptOrder order;
         order.init(p, known, blockIdx.x == 0);
-        const PromptCut c = prompt_cut(p, order);
-        const int total = c.whole + (order.total * p.Hkv - c.whole) * c.parts;
-        if (p.cut && blockIdx.x == 0 && lane == 0)
-            p.cut[0] = make_int4(c.parts, c.parts > 1 ? order.total * p.Hkv - c.whole : 0, 0, 0);
-        for (int turn = 0;; ++turn) {
+        int total = order.total * p.Hkv;
+        PromptCut c{total, 1, 1};
+        bool more = false, planned = false;
+        for (int turn = 0, round = 0;; ++turn) {
             const int slot = turn % PT_ITEMS;
             bool ok = true;
             if (turn >= PT_ITEMS) ok = wait_item(p, &b->i_empty[slot], (turn / PT_ITEMS - 1) & 1u);
             if (!__all_sync(0xffffffffu, ok)) return;
-            // turns of alternating direction: CTA b takes b, 2 grid - 1 - b, 2 grid + b, ...
-            // (k is below the next turn's first number: behind the last item there are no more turns)
-            const int k = turn * gridDim.x + (turn & 1 ? static_cast<int>(gridDim.x) - 1 - static_cast<int>(blockIdx.x)
-                                                       : static_cast<int>(blockIdx.x));
+            if (!planned && (round == 1 || p.shared || total < p.grid)) {      // (behind a whole round its items go first)
+                planned = true;
+                c = prompt_cut(p, order);
+                const int left = total - c.whole;
+                total = c.whole + (c.b > 1 ? (left * c.b + c.a - 1) / c.a : left);
+                if (p.cut && blockIdx.x == 0 && lane == 0) p.cut[0] = make_int4(c.b, c.b > 1 ? left : 0, c.a, 0);
+            }
+            // rounds of alternating direction: CTA b takes b, 2 grid - 1 - b, 2 grid + b, ...
+            // (k is below the next round's first number: behind the last item there are no more rounds)
+            const int k = round * gridDim.x + (round & 1 ? static_cast<int>(gridDim.x) - 1 - static_cast<int>(blockIdx.x)
+                                                         : static_cast<int>(blockIdx.x));
             PromptItem it{};
             if (k < total) {
-                it = prompt_item(p, order, c, k);
-                if (!p.shared && it.slot >= 0 && it.slot % c.parts == 0 && lane == 0)
-                    p.cut[1 + it.slot / c.parts] = make_int4(it.row0, it.ntok, it.h, it.slot);
+                int first;
+                it = prompt_item(p, order, c, k, more, first, more);
+                if (!p.shared && first >= 0 && lane == 0) p.cut[1 + first] = make_int4(it.row0, it.ntok, it.h, it.slot);
             }
+            if (!more) ++round;
             if (lane == 0) {
                 items[slot] = it;
                 fix[slot].any = 0;
@@ -1150,9 +1205,10 @@ prompt_merge_kernel(const __grid_constant__ PromptParams p) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     grid_dependency_wait();
     const int4 n = p.cut[0];
-    const int parts = n.x;
-    if (static_cast<int>(blockIdx.x) / PER >= n.y) return;
-    const int4 item = p.cut[1 + blockIdx.x / PER];         // (first row, tokens, head, place)
+    const int i = blockIdx.x / PER;
+    if (i >= n.y) return;
+    const int parts = ((i + 1) * n.x + n.z - 1) / n.z - i * n.x / n.z;      // spans that item i has part in
+    const int4 item = p.cut[1 + i];                        // (first row, tokens, head, place)
     for (int y = warp; y < PT_MERGE_ROWS; y += PT_MERGE_WARPS) {
         const int x = (blockIdx.x % PER) * PT_MERGE_ROWS + y, q = x / PT_M, r = x % PT_M;
         const int tok = r / p.G;

@@ -211,7 +211,7 @@ extern "C" pa_status pa_decode_shared(void* out, const void* q, pa_dtype q_dtype
     const size_t base = round256(pa_decode_workspace_size(B, Hq, max_len, D, 0));
     int32_t* part[4];
     for (int x = 0; x < 4; ++x) part[x] = reinterpret_cast<int32_t*>(ws + base + x * ints(B));
-    const PromptPlan plan = prompt_plan(num_groups, B, Hq, Hkv, D, max_len, true, dev.sms);
+    const PromptPlan plan = prompt_plan(num_groups, B, Hq, Hkv, D, max_len, false, true, dev.sms);
     const PromptCall c{"decode_shared", out, q, q_dtype, k_cache, v_cache, group_start, nullptr, prefix_lens, block_tables,
                        num_groups, Hq, Hkv, D, B, 0, block_size, num_blocks, MB, scale, true, seq_lens, part[0], part[1],
                        err_flag, stream};

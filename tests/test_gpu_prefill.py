@@ -312,3 +312,22 @@ def test_no_keys_at_all():
     c = Case([0, 0], 4, 2, 64, F16, q_lens=[3, 5])
     out = c.flat()
     assert c.k.shape[0] == 0 and (out == 0).all() and c.err.item() == 0
+
+
+@pytest.mark.parametrize("k", [5, 20, 40, 51, 76, 79, 100, 130])
+def test_spans_of_cut_items(k):
+    """2 k items, every row of them: cut into spans that end inside an item and start in the one before."""
+    n = 36 * k - 5
+    c = Case([n + 2500], 14, 2, 64, BF16, q_lens=[n], seed=k)
+    want, tol = ref.attend(c.q, c.k, c.v, c.scale, torch.arange(2500, 2500 + n, device="cuda"))
+    for out in (c.flat(), c.cached(64)):
+        ref.check(out, want, tol)
+    assert c.err.item() == 0
+
+
+@pytest.mark.parametrize("lens,chunk", [([6000, 900, 3000], [1500, 700, 36]), ([4000, 4000, 200, 100], [1300, 900, 200, 100]),
+                                        ([2000] * 9, [300] * 9), ([5000, 60, 50, 40], [700, 60, 50, 40])])
+def test_spans_of_unequal_items(lens, chunk):
+    c = Case(lens, 14, 2, 128, F16, q_lens=chunk, seed=len(lens))
+    c.check(c.flat())
+    c.check(c.cached(16))
