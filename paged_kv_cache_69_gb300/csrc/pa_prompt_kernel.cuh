@@ -992,9 +992,12 @@ struct PromptKernel {
     }
 
     // ---------------- rows out: four warps, both tiles in turn ----------------
-    static __device__ __forceinline__ void put32(void* dst, const uint32_t (&w)[8]) {
-        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
-                     :: "l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+    // 32 bytes: one access where the address is a multiple of 32 (`wide`), which a caller's
+    // tensor need not be, else two of 16.  (Two of 16 always: 256 short prompts 476 us, so 456.)
+    static __device__ __forceinline__ void put32(void* dst, const uint32_t (&w)[8], bool wide) {
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %9, 0;\n\t@p st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n\t"
+                     "@!p st.global.v4.b32 [%0], {%1,%2,%3,%4};\n\t@!p st.global.v4.b32 [%0+16], {%5,%6,%7,%8};\n\t}"
+                     :: "l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "r"(static_cast<int>(wide))
                      : "memory");
     }
     // What mend_values took out, for a row that sees the keys up to `last`.
@@ -1017,6 +1020,8 @@ struct PromptKernel {
         const int r = threadIdx.x & (PT_M - 1), lane = threadIdx.x & 31;
         const uint32_t lanes = static_cast<uint32_t>(r & ~31) << 16;
         const int tok = r / p.G, head = r - tok * p.G;
+        // rows are 128 or 256 bytes: all of them lie as out itself does
+        const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
         uint32_t n[2] = {0, 0};
         for (int turn = 0;; ++turn) {
             const int is = turn % PT_ITEMS;
@@ -1038,7 +1043,7 @@ struct PromptKernel {
                     const uint32_t w[8] = {};
                     if (mine && direct) {
 #pragma unroll
-                        for (int x = 0; x < D; x += 16) put32(dst + x * 2, w);
+                        for (int x = 0; x < D; x += 16) put32(dst + x * 2, w, wide);
                     }
                     if (mine && !direct) p.part_ml[part] = make_float2(-INFINITY, 0.f);
                     continue;
@@ -1062,14 +1067,14 @@ struct PromptKernel {
                         for (int y = 0; y < 2; ++y) {
 #pragma unroll
                             for (int d = 0; d < 8; ++d) w[d] = pack2(o[16 * y + 2 * d] * inv, o[16 * y + 2 * d + 1] * inv, BF16);
-                            put32(dst + x * 2 + y * 32, w);
+                            put32(dst + x * 2 + y * 32, w, wide);
                         }
                     } else {
 #pragma unroll
                         for (int y = 0; y < 4; ++y) {
 #pragma unroll
                             for (int d = 0; d < 8; ++d) w[d] = __float_as_uint(o[8 * y + d]);
-                            put32(dst + x * 4 + y * 32, w);
+                            put32(dst + x * 4 + y * 32, w, true);     // (the workspace is 256-byte aligned)
                         }
                     }
                 }
