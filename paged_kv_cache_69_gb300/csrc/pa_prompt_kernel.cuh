@@ -1203,17 +1203,27 @@ prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ CU
 // ---------------------------------------------------------------------------
 constexpr int PT_MERGE_WARPS = 8, PT_MERGE_ROWS = 32;
 
+// Spans that cut item i < grid has part in, by the launch's entry n and the item's own; 0 where
+// there is no such item, and for entries that cannot be one: behind a wait that ran out they
+// are whatever the workspace held, and nothing outside the call's buffers may follow from them.
+__host__ __device__ inline int cut_parts(const PromptParams& p, int i, int4 n, int4 item) {
+    if (i >= n.y || n.x < 2 || n.x > 32 || n.z < 1 || n.z >= n.x) return 0;
+    const int parts = ((i + 1) * n.x + n.z - 1) / n.z - i * n.x / n.z;      // at most n.x: an item has n.x / n.z of them
+    const bool fits = item.x >= 0 && item.y >= 1 && item.y <= 2 * p.tokens && item.x <= p.total_q - item.y &&
+                      item.z >= 0 && item.z < p.Hkv && item.w >= 0 && item.w <= 2 * p.grid - parts;
+    return fits ? parts : 0;
+}
+
 template <class KV, int D>
 __global__ void __launch_bounds__(32 * PT_MERGE_WARPS)
 prompt_merge_kernel(const __grid_constant__ PromptParams p) {
     constexpr int DPL = D / 32, PER = 2 * PT_M / PT_MERGE_ROWS;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     grid_dependency_wait();
-    const int4 n = p.cut[0];
     const int i = blockIdx.x / PER;
-    if (i >= n.y) return;
-    const int parts = ((i + 1) * n.x + n.z - 1) / n.z - i * n.x / n.z;      // spans that item i has part in
-    const int4 item = p.cut[1 + i];                        // (first row, tokens, head, place)
+    const int4 n = p.cut[0], item = p.cut[1 + i];          // (first row, tokens, head, place)
+    const int parts = cut_parts(p, i, n, item);
+    if (parts == 0) return;
     for (int y = warp; y < PT_MERGE_ROWS; y += PT_MERGE_WARPS) {
         const int x = (blockIdx.x % PER) * PT_MERGE_ROWS + y, q = x / PT_M, r = x % PT_M;
         const int tok = r / p.G;

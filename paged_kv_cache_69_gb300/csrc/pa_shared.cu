@@ -51,7 +51,7 @@ shared_merge_kernel(const __grid_constant__ DecodeParams p, const __grid_constan
     PromptSeq q{0, 0, 0, 0, 0};
     if (g >= 0) q = prompt_seq(s, g, false);
     grid_dependency_wait();
-    const int parts = s.cut[0].x;
+    const int parts = min(max(s.cut[0].x, 0), s.splits);   // (behind a wait that ran out it may be anything)
     const int tail = p.seq_lens[i];
     if (tail < 0) return;
     // the prefix's partials: one per range of keys
