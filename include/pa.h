@@ -249,7 +249,7 @@ pa_status pa_decode_weights(void* out, float* weights, const void* q, pa_dtype q
  * A sequence shorter than its group's prefix, or longer than its table, is left
  * unwritten with PA_ERRBIT_SEQ_TOO_LONG.  f16 and bf16 pools with q of the same type;
  * at most 128 query heads per KV head.  Precision: over the prefix as pa_prefill,
- * else as pa_decode.
+ * else as pa_decode; f16 outputs of finite values are finite, within +-65504.
  */
 size_t pa_decode_shared_workspace_size(int num_seqs, int num_groups, int num_q_heads,
                                        int num_kv_heads, int max_seq_len, int head_dim);
@@ -444,7 +444,8 @@ pa_status pa_attention(void* out, const void* q, pa_dtype q_dtype,
  * f16 or bf16, q, K, V and out of one type; head_dim 64 or 128; at most 128 query
  * heads per KV head; tensors 16-byte aligned.  Scores, sums and outputs are held
  * in f32; the weights enter P*V rounded to the type (f16: 11 bits down to 2^-21 of
- * the row's largest, fewer below; bf16: 8 bits).
+ * the row's largest, fewer below; bf16: 8 bits).  f16 outputs of finite values are
+ * finite, within +-65504.
  *   workspace         at least pa_prefill_workspace_size(...) bytes, 256-byte
  *                     aligned, no initialisation; calls sharing one must not
  *                     overlap on the GPU.  It holds the partial results of batches

@@ -1000,6 +1000,20 @@ struct PromptKernel {
                      :: "l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "r"(static_cast<int>(wide))
                      : "memory");
     }
+    // Rows of f16 once more, where some quotient passes the largest f16 (as FiniteHalf says).
+    // (Apart from the rows' own loop, which only looks for such quotients: limited there, 256 short
+    // prompts take 465 us, so 455.)
+    static __device__ __noinline__ void put_limited(uint32_t from, uint8_t* dst, float inv, bool mine) {
+#pragma unroll 1
+        for (int x = 0; x < D; x += 16) {
+            float o[16];
+            tmem_ld16(from + x, o);
+            tmem_wait_ld();
+            if (!mine) continue;
+#pragma unroll
+            for (int y = 0; y < 16; ++y) reinterpret_cast<FiniteHalf*>(dst)[x + y] = from_float<FiniteHalf>(o[y] * inv);
+        }
+    }
     // What mend_values took out, for a row that sees the keys up to `last`.
     static __device__ __noinline__ void unmend(void* row, bool direct, int last, const PromptFix* fix) {
         using E = typename KV::T;
@@ -1055,6 +1069,7 @@ struct PromptKernel {
                 const float inv = !direct ? 1.f : ml.y != 0.f ? 1.f / ml.y : 0.f;
                 const bool fixed = *reinterpret_cast<const volatile int*>(&fix[is].any);
                 if (mine && !direct) p.part_ml[part] = ml;
+                float top = 0.f;
 #pragma unroll 1
                 for (int x = 0; x < D; x += 32) {
                     float o[32];
@@ -1063,6 +1078,10 @@ struct PromptKernel {
                     if (!mine) continue;
                     uint32_t w[8];
                     if (direct) {
+                        if constexpr (!BF16) {
+#pragma unroll
+                            for (int y = 0; y < 32; y += 2) top = max3(top, fabsf(o[y]), fabsf(o[y + 1]));
+                        }
 #pragma unroll
                         for (int y = 0; y < 2; ++y) {
 #pragma unroll
@@ -1078,6 +1097,7 @@ struct PromptKernel {
                         }
                     }
                 }
+                if (!BF16 && __any_sync(0xffffffffu, direct && top * inv > 65504.f)) put_limited(to, dst, inv, mine);
                 if (fixed && mine) unmend(dst, direct, last, fix + is);
                 tc05_fence_before();
                 __syncwarp();
@@ -1250,10 +1270,11 @@ prompt_merge_kernel(const __grid_constant__ PromptParams p) {
                 num[d] = fmaf(f, p.part_acc[(at + static_cast<size_t>(k) * 2 * PT_M) * D + lane * DPL + d], num[d]);
         }
         const float inv = den != 0.f ? 1.f / den : 0.f;
-        typename KV::T* o = static_cast<typename KV::T*>(p.out) +
-                            (static_cast<size_t>(item.x + q * p.tokens + tok) * p.Hq + item.z * p.G + r - tok * p.G) * D + lane * DPL;
+        using OutT = std::conditional_t<KV::code == PA_F16, FiniteHalf, typename KV::T>;
+        OutT* o = static_cast<OutT*>(p.out) +
+                  (static_cast<size_t>(item.x + q * p.tokens + tok) * p.Hq + item.z * p.G + r - tok * p.G) * D + lane * DPL;
 #pragma unroll
-        for (int d = 0; d < DPL; ++d) o[d] = from_float<typename KV::T>(num[d] * inv);
+        for (int d = 0; d < DPL; ++d) o[d] = from_float<OutT>(num[d] * inv);
     }
 }
 

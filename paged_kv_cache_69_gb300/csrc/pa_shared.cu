@@ -142,8 +142,8 @@ shared_merge_kernel(const __grid_constant__ DecodeParams p, const __grid_constan
 }
 
 pa_status launch_shared_merge(const DecodeParams& p, const Tails& t, pa_dtype out, cudaStream_t stream) {
-    const void* kern = out == PA_F16 ? (p.D == 128 ? reinterpret_cast<const void*>(&shared_merge_kernel<__half, 128>)
-                                                   : reinterpret_cast<const void*>(&shared_merge_kernel<__half, 64>))
+    const void* kern = out == PA_F16 ? (p.D == 128 ? reinterpret_cast<const void*>(&shared_merge_kernel<FiniteHalf, 128>)
+                                                   : reinterpret_cast<const void*>(&shared_merge_kernel<FiniteHalf, 64>))
                                      : (p.D == 128 ? reinterpret_cast<const void*>(&shared_merge_kernel<__nv_bfloat16, 128>)
                                                    : reinterpret_cast<const void*>(&shared_merge_kernel<__nv_bfloat16, 64>));
     cudaLaunchAttribute attr[1];
