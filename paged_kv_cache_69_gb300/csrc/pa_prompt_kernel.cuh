@@ -1125,7 +1125,8 @@ __device__ __forceinline__ void write_tails(const PromptParams& p) {
     for (int i = blockIdx.x * PT_THREADS + threadIdx.x; i < p.total_q; i += gridDim.x * PT_THREADS) {
         const int g = prompt_seq_of(p, i);
         int P = 0, least = 0;
-        if (g >= 0) {
+        // (a group whose entries leave the batch has no say on its sequences)
+        if (g >= 0 && __ldg(p.q_start + g) >= 0 && __ldg(p.q_start + g + 1) <= p.total_q) {
             P = prompt_seq(p, g, false).L;
             least = group_prefix(p, g);
         }
