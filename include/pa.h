@@ -246,6 +246,9 @@ pa_status pa_decode_weights(void* out, float* weights, const void* q, pa_dtype q
  *   workspace         at least pa_decode_shared_workspace_size(...) bytes, 256-byte
  *                     aligned, no initialisation; calls sharing one must not overlap
  *                     on the GPU.
+ *                     Beside pa_decode's it has one f32 row per (sequence, query head)
+ *                     and, for prefixes cut into ranges, at most 512 rows per SM (40 MB
+ *                     at head_dim 128); the number of groups adds nothing.
  * A sequence shorter than its group's prefix, or longer than its table, is left
  * unwritten with PA_ERRBIT_SEQ_TOO_LONG.  f16 and bf16 pools with q of the same type;
  * at most 128 query heads per KV head.  Precision: over the prefix as pa_prefill,

@@ -26,13 +26,13 @@ static size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 // At most so many items per KV head: a sequence of n tokens has 1 + floor((n - 1) / TT).
 static long long prompt_items(int B, int total_q, int TT) { return B + std::max(0, total_q - B) / TT; }
 
-// Partials of a call: a prefill cuts fewer items than it has CTAs, into at most 2
-// ranges per CTA in all; in shared mode every item has one, places being counted
-// as prompt_slot does.
-static size_t prompt_slots(int B, int total_q, int TT, int Hkv, bool shared, int sms) {
-    if (!shared) return 2 * static_cast<size_t>(sms);
-    return 2 * static_cast<size_t>(sms) + static_cast<size_t>(total_q / TT + B + 1) * Hkv;
-}
+// Rows of partials of a prefill: it cuts fewer items than it has CTAs, into at most 2 ranges
+// per CTA in all, each with both tiles' rows.
+static size_t prefill_rows(int sms) { return 2 * static_cast<size_t>(sms) * 2 * PT_M; }
+
+static size_t ml_size(size_t rows) { return up256(rows * sizeof(float2)); }
+static size_t acc_size(size_t rows, int D) { return up256(rows * D * sizeof(float)); }
+static size_t cut_size(int sms) { return up256((1 + static_cast<size_t>(sms)) * sizeof(int4)); }
 
 PromptPlan prompt_plan(int B, int total_q, int Hq, int Hkv, int D, int max_keys, bool prompts, bool shared,
                        int sms) {
@@ -51,18 +51,24 @@ PromptPlan prompt_plan(int B, int total_q, int Hq, int Hkv, int D, int max_keys,
     }
     pl.grid = static_cast<int>(std::max(1LL, std::min<long long>(items * pl.splits, sms)));
     if (pl.splits > 1 || shared) {
-        const size_t slots = prompt_slots(B, total_q, TT, Hkv, shared, sms);
-        pl.cut_bytes = up256((1 + static_cast<size_t>(sms)) * sizeof(int4));
-        pl.ml_bytes = up256(slots * 2 * PT_M * sizeof(float2));
-        pl.acc_bytes = up256(slots * 2 * PT_M * D * sizeof(float));
+        const size_t rows = shared ? static_cast<size_t>(total_q) * Hq * pl.splits : prefill_rows(sms);
+        pl.cut_bytes = cut_size(sms);
+        pl.ml_bytes = ml_size(rows);
+        pl.acc_bytes = acc_size(rows, D);
     }
     return pl;
 }
 
-size_t prompt_part_bytes(int B, int total_q, int Hq, int Hkv, int D, bool shared, int sms) {
-    const size_t slots = prompt_slots(B, total_q, 2 * (PT_M / (Hq / Hkv)), Hkv, shared, sms);
-    return up256((1 + static_cast<size_t>(sms)) * sizeof(int4)) + up256(slots * 2 * PT_M * sizeof(float2)) +
-           up256(slots * 2 * PT_M * D * sizeof(float));
+size_t prompt_part_bytes(int total_q, int Hq, int D, bool shared, int sms) {
+    size_t rows = prefill_rows(sms);
+    if (shared) {
+        // total_q Hq rows, each in 1 + floor(2 sms / places) ranges, of which there are 32 at most.  There
+        // are more places than total_q Hq / (2 PT_M), so that the second term has fewer rows
+        // than 2 sms x 2 PT_M, with fewer sequences too.
+        const size_t once = static_cast<size_t>(total_q) * Hq;
+        rows = std::min(once + rows, 32 * once);
+    }
+    return cut_size(sms) + ml_size(rows) + acc_size(rows, D);
 }
 
 static CUresult encode4(CUtensorMap* m, pa_dtype dt, const void* base, cuuint64_t d1, cuuint64_t d2, cuuint64_t planes,
@@ -88,10 +94,10 @@ static CUresult encode_pool(CUtensorMap* m, pa_dtype dt, const void* base, cuuin
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
-template <class KV, int D, bool PAGED>
+template <class KV, int D, bool PAGED, bool SHARED = false>
 static cudaError_t launch(const PromptParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                           cudaStream_t stream) {
-    const void* kern = reinterpret_cast<const void*>(&prompt_kernel<KV, D, PAGED>);
+    const void* kern = reinterpret_cast<const void*>(&prompt_kernel<KV, D, PAGED, SHARED>);
     cudaError_t e = allow_shared(kern, PromptLayout<D>::BYTES);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
@@ -106,7 +112,7 @@ static cudaError_t launch(const PromptParams& p, const CUtensorMap& tq, const CU
     cfg.numAttrs = 1;
     void* args[] = {const_cast<PromptParams*>(&p), const_cast<CUtensorMap*>(&tq), const_cast<CUtensorMap*>(&tk),
                     const_cast<CUtensorMap*>(&tv)};
-    if ((e = cudaLaunchKernelExC(&cfg, kern, args)) != cudaSuccess || p.splits == 1 || p.shared) return e;
+    if ((e = cudaLaunchKernelExC(&cfg, kern, args)) != cudaSuccess || p.splits == 1 || SHARED) return e;
     cfg.gridDim = dim3(static_cast<unsigned>(p.grid * (2 * PT_M / PT_MERGE_ROWS)));
     cfg.blockDim = dim3(32 * PT_MERGE_WARPS);
     cfg.dynamicSmemBytes = 0;
@@ -163,7 +169,10 @@ pa_status launch_prompt(const PromptCall& c, const PromptPlan& plan, void* parts
         return bad(c, PA_ERR_CUDA, msg);
     }
     cudaError_t e;
-#define PA_PROMPT(KVT, DD) (c.k_start ? launch<KVT, DD, false>(p, tq, tk, tv, c.stream) : launch<KVT, DD, true>(p, tq, tk, tv, c.stream))
+#define PA_PROMPT(KVT, DD)                                                  \
+    (c.shared    ? launch<KVT, DD, true, true>(p, tq, tk, tv, c.stream)     \
+     : c.k_start ? launch<KVT, DD, false>(p, tq, tk, tv, c.stream)          \
+                 : launch<KVT, DD, true>(p, tq, tk, tv, c.stream))
     if (c.dtype == PA_F16) e = c.D == 128 ? PA_PROMPT(F16T, 128) : PA_PROMPT(F16T, 64);
     else e = c.D == 128 ? PA_PROMPT(BF16T, 128) : PA_PROMPT(BF16T, 64);
 #undef PA_PROMPT
@@ -222,7 +231,7 @@ extern "C" size_t pa_prefill_workspace_size(int num_seqs, int total_q, int num_q
         return 0;
     DeviceInfo dev;
     if (!device_info(dev)) return 0;
-    return prompt_part_bytes(num_seqs, total_q, num_q_heads, num_kv_heads, head_dim, false, dev.sms);
+    return prompt_part_bytes(total_q, num_q_heads, head_dim, false, dev.sms);
 }
 
 extern "C" pa_status pa_prefill(void* out, const void* q, const void* key, const void* value, pa_dtype dtype,

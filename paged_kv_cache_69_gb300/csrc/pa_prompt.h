@@ -33,7 +33,7 @@ struct PromptPlan {
 PromptPlan prompt_plan(int B, int total_q, int Hq, int Hkv, int D, int max_keys, bool prompts, bool shared,
                        int sms);
 // Room for any call of at most these numbers (a workspace made once serves smaller calls).
-size_t prompt_part_bytes(int B, int total_q, int Hq, int Hkv, int D, bool shared, int sms);
+size_t prompt_part_bytes(int total_q, int Hq, int D, bool shared, int sms);
 
 // The kernel; partials at `parts` (256-byte aligned, plan's bytes). p_out: the
 // kernel's parameters for a merge.

@@ -84,8 +84,8 @@ struct PromptParams {
     const int32_t* seq_lens;           // [B] keys, paged; shared mode: prefix lengths
     const int32_t* block_tables;       // paged: [rows][MB]
     int32_t* err_flag;
-    float* part_acc;                   // [slot][2][128][D]
-    float2* part_ml;                   // [slot][2][128] (reference in log2 units, l)
+    float* part_acc;                   // [place][2][128][D]; shared mode: [sequence][head][range][D]
+    float2* part_ml;                   // the same without D: (reference in log2 units, l)
     int B, Hq, Hkv, G, bs, NB, MB;
     int total_q, total_k;
     int tokens;                        // query tokens per tile, 128 / G
@@ -108,7 +108,9 @@ struct PromptItem {
     int row0, ntok;                    // first query row, query tokens of both tiles
     int pos0, L;                       // position of the first token, keys of the sequence
     int t0, e[2];                      // chunks [t0, e[q]) of tile q
-    int h, slot;                       // KV head; partial slot, -1: rows of out
+    int h;                             // KV head
+    int place;                         // of the partials, -1: rows of out; shared mode: the item's range of keys
+    int ranges;                        // shared mode: how many there are
     int edge;                          // first chunk with keys that some row must not see
     int idx;                           // sequence (or group)
 };
@@ -201,6 +203,16 @@ static __device__ __noinline__ PromptSeq prompt_seq(const PromptParams& p, int i
     s.a = static_cast<int>(div_by(p.shared ? s.L : max(0, s.L - s.n), p.div_tt));
     s.c = prompt_items_of(p, s.n);
     return s;
+}
+
+// The sequence whose query rows hold `row`, or -1.
+__device__ __forceinline__ int prompt_seq_of(const PromptParams& p, int row) {
+    int lo = 0, hi = p.B;                                  // the last i with q_start[i] <= row
+    while (hi - lo > 1) {
+        const int m = (lo + hi) >> 1;
+        if (__ldg(p.q_start + m) <= row) lo = m; else hi = m;
+    }
+    return lo < p.B && __ldg(p.q_start + lo) <= row && row < __ldg(p.q_start + lo + 1) ? lo : -1;
 }
 
 // Items of a sequence of c items from level a on that lie at level u or above: causal
@@ -358,12 +370,6 @@ __device__ __forceinline__ PromptCut prompt_cut(const PromptParams& p, const Pro
     return c;
 }
 
-// The place of an item among the partials of shared mode: groups take floor(n / 2 tokens) + 1
-// places each, counted from their first query row, without a sum over the batch.
-__device__ __forceinline__ int prompt_slot(const PromptParams& p, int row0, int i, int t) {
-    return static_cast<int>(div_by(row0, p.div_tt)) + i + t;
-}
-
 // Number v in the order of a launch cut as c says: an item, or a span's first part or, second
 // set, its other.  more: there is another; first: for an item's first part the item's number
 // among the cut ones, else -1.
@@ -412,7 +418,8 @@ __device__ __forceinline__ PromptItem prompt_item(const PromptParams& p, PromptO
     // the last key that every row of the first tile with chunks sees
     const int seen = p.causal ? min(it.pos0 + (it.e[0] > it.t0 ? 0 : p.tokens), it.L - 1) : it.L - 1;
     it.edge = max(0, seen + 1) / PT_M;
-    it.slot = p.shared ? (prompt_slot(p, s.x, it.idx, t) * p.Hkv + it.h) * c.b + from : place;
+    it.place = p.shared ? from : place;
+    it.ranges = c.b;
     return it;
 }
 
@@ -486,7 +493,9 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 // ---------------------------------------------------------------------------
 // the kernel
 // ---------------------------------------------------------------------------
-template <class KV, int D, bool PAGED>
+// SHARED: the shared mode, whose rows go out as partials by (sequence, head).  (A kernel of its own:
+// the places of both kinds worked out by one take 256 short prompts from 454 to 462 us.)
+template <class KV, int D, bool PAGED, bool SHARED>
 struct PromptKernel {
     using Lay = PromptLayout<D>;
     // K and V tiles in shared memory: 8-row groups of 128-byte rows GROUP bytes apart,
@@ -551,7 +560,7 @@ struct PromptKernel {
             if (k < total) {
                 int first;
                 it = prompt_item(p, order, c, k, more, first, more);
-                if (!p.shared && first >= 0 && lane == 0) p.cut[1 + first] = make_int4(it.row0, it.ntok, it.h, it.slot);
+                if (!p.shared && first >= 0 && lane == 0) p.cut[1 + first] = make_int4(it.row0, it.ntok, it.h, it.place);
             }
             if (!more) ++round;
             if (lane == 0) {
@@ -1042,17 +1051,16 @@ struct PromptKernel {
             if (!__all_sync(0xffffffffu, wait_item(p, &b->i_full[is], (turn / PT_ITEMS) & 1u))) return;
             const PromptItem it = items[is];
             if (!it.live) return;
-            const bool direct = it.slot < 0;
+            const bool direct = !SHARED && it.place < 0;
 #pragma unroll 1
             for (int q = 0; q < 2; ++q) {
                 const uint32_t to = b->tmem + lanes + Lay::OCOL + q * D;
                 const bool mine = tok < p.tokens && q * p.tokens + tok < it.ntok;
                 const int last = p.causal ? it.pos0 + q * p.tokens + tok : it.L - 1;    // the row's last key
                 const bool any = it.e[q] > it.t0;
-                const size_t part = (static_cast<size_t>(direct ? 0 : it.slot) * 2 + q) * PT_M + r;
-                uint8_t* dst = direct ? static_cast<uint8_t*>(p.out) +
-                                            (static_cast<size_t>(it.row0 + q * p.tokens + tok) * p.Hq + it.h * p.G + head) * D * 2
-                                      : reinterpret_cast<uint8_t*>(p.part_acc + part * D);
+                const size_t row = static_cast<size_t>(it.row0 + q * p.tokens + tok) * p.Hq + it.h * p.G + head;
+                const size_t part = SHARED ? row * it.ranges + it.place : (static_cast<size_t>(direct ? 0 : it.place) * 2 + q) * PT_M + r;
+                uint8_t* dst = direct ? static_cast<uint8_t*>(p.out) + row * D * 2 : reinterpret_cast<uint8_t*>(p.part_acc + part * D);
                 if (!any) {                                // no keys: zeros, or an empty partial
                     const uint32_t w[8] = {};
                     if (mine && direct) {
@@ -1109,16 +1117,6 @@ struct PromptKernel {
     }
 };
 
-// The sequence whose query rows hold `row`, or -1.
-__device__ __forceinline__ int prompt_seq_of(const PromptParams& p, int row) {
-    int lo = 0, hi = p.B;                                  // the last i with q_start[i] <= row
-    while (hi - lo > 1) {
-        const int m = (lo + hi) >> 1;
-        if (__ldg(p.q_start + m) <= row) lo = m; else hi = m;
-    }
-    return lo < p.B && __ldg(p.q_start + lo) <= row && row < __ldg(p.q_start + lo + 1) ? lo : -1;
-}
-
 // Shared mode: what each sequence has behind its group's prefix, for the decode
 // kernel; -1 tokens for a sequence whose length does not fit.
 __device__ __forceinline__ void write_tails(const PromptParams& p) {
@@ -1137,11 +1135,11 @@ __device__ __forceinline__ void write_tails(const PromptParams& p) {
     }
 }
 
-template <class KV, int D, bool PAGED>
+template <class KV, int D, bool PAGED, bool SHARED>
 __global__ void __launch_bounds__(PT_THREADS, 1)
 prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ CUtensorMap tq,
               const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
-    using K = PromptKernel<KV, D, PAGED>;
+    using K = PromptKernel<KV, D, PAGED, SHARED>;
     using Lay = PromptLayout<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -1193,7 +1191,7 @@ prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ CU
     // it wrote is read before this
     grid_dependency_wait();
     grid_dependents_launch();
-    if (p.shared) write_tails(p);
+    if constexpr (SHARED) write_tails(p);
     if (warp >= 8) {
         regs_down<PT_REGS_FEW>();
         if (warp == 8) {

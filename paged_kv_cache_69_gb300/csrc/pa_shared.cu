@@ -55,14 +55,8 @@ shared_merge_kernel(const __grid_constant__ DecodeParams p, const __grid_constan
     const int tail = p.seq_lens[i];
     if (tail < 0) return;
     // the prefix's partials: one per range of keys
-    int n1 = 0;
-    size_t at1 = 0;
-    if (q.L > 0) {
-        const int j = i - q.row0, t = j / (2 * s.tokens), u = j - t * 2 * s.tokens, tile = u >= s.tokens;
-        const size_t slot = (static_cast<size_t>(prompt_slot(s, q.row0, g, t)) * s.Hkv + h / s.G) * parts;
-        at1 = (slot * 2 + tile) * PT_M + (u - tile * s.tokens) * s.G + h % s.G;
-        n1 = parts;
-    }
+    const int n1 = q.L > 0 ? parts : 0;
+    const size_t at1 = static_cast<size_t>(w) * parts;
     // the tail's: slot range + unit for each range that holds some of its chunks
     int n2 = 0, r0 = 0, U = 0, S = 0, nch = 0;
     long long W = 0;
@@ -84,7 +78,7 @@ shared_merge_kernel(const __grid_constant__ DecodeParams p, const __grid_constan
         const float* acc = nullptr;
         float2 ml = make_float2(-INFINITY, 0.f);
         if (k < n1) {
-            const size_t at = at1 + static_cast<size_t>(k) * 2 * PT_M;
+            const size_t at = at1 + k;
             ml = s.part_ml[at];
             acc = s.part_acc + at * D;
         } else if (k < n1 + n2) {
@@ -174,7 +168,7 @@ extern "C" size_t pa_decode_shared_workspace_size(int num_seqs, int num_groups, 
     DeviceInfo dev;
     if (base == 0 || !device_info(dev)) return 0;
     return round256(base) + 4 * ints(num_seqs) +
-           prompt_part_bytes(num_groups, num_seqs, num_q_heads, num_kv_heads, head_dim, true, dev.sms);
+           prompt_part_bytes(num_seqs, num_q_heads, head_dim, true, dev.sms);
 }
 
 extern "C" pa_status pa_decode_shared(void* out, const void* q, pa_dtype q_dtype, const void* k_cache, const void* v_cache,

@@ -23,3 +23,25 @@ def test_prefixes_of_groups_that_leave_the_batch(starts, prefix):
     out = c.call()
     assert c.err.item() == pa.ERRBIT_BAD_QUERY
     ref.check(out, *want)
+
+
+def test_many_small_groups():
+    """Groups of one and two beside large ones, more of them than CTAs."""
+    g = torch.Generator().manual_seed(8)
+    n = [1 + int(x) for x in torch.randint(0, 2, (330,), generator=g)] + [70, 33]
+    c = Case([(2100 if m == 2 and i % 40 == 0 else 40 * (m > 2) * 16, [1 + (i + j) % 5 for j in range(m)]) for i, m in enumerate(n)],
+             8, 2, 64, F16)
+    c.check(c.call())
+
+
+@pytest.mark.parametrize("groups", [0, 1, 16, 256, 1024])
+def test_workspace_grows_with_rows_and_not_with_groups(groups):
+    """Beside what pa_decode takes: a partial per (sequence, head), and those of prefixes cut into ranges
+    to fill the GPU, two per SM of 256 rows each."""
+    B, Hq, Hkv, D = 1024, 32, 8, 128
+    base = pa.pa_decode_workspace_size(B, Hq, 8192, D, 0)
+    more = pa.pa_decode_shared_workspace_size(B, groups, Hq, Hkv, 8192, D) - base
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert 0 < more <= (B * Hq + 2 * sms * 256) * (D * 4 + 8) + (1 << 16)
+    few = pa.pa_decode_shared_workspace_size(2, 1, 4, 2, 8192, 64) - pa.pa_decode_workspace_size(2, 4, 8192, 64, 0)
+    assert few <= 32 * 2 * 4 * (64 * 4 + 8) + (1 << 16)
