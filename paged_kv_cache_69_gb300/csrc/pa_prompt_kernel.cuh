@@ -215,6 +215,12 @@ __device__ __forceinline__ int prompt_seq_of(const PromptParams& p, int row) {
     return lo < p.B && __ldg(p.q_start + lo) <= row && row < __ldg(p.q_start + lo + 1) ? lo : -1;
 }
 
+// Shared mode: whether a row's group is `group` (groups whose entries fall back overlap; a row
+// then belongs to one of them).
+static __device__ __noinline__ bool prompt_member(const PromptParams& p, int row, int group) {
+    return row < p.total_q && prompt_seq_of(p, row) == group;
+}
+
 // Items of a sequence of c items from level a on that lie at level u or above: causal
 // items one to a level, the items of a group all at a.
 __device__ __forceinline__ int items_from(const PromptParams& p, int a, int c, int u) {
@@ -1055,7 +1061,8 @@ struct PromptKernel {
 #pragma unroll 1
             for (int q = 0; q < 2; ++q) {
                 const uint32_t to = b->tmem + lanes + Lay::OCOL + q * D;
-                const bool mine = tok < p.tokens && q * p.tokens + tok < it.ntok;
+                const bool mine = tok < p.tokens && q * p.tokens + tok < it.ntok &&
+                                  (!SHARED || prompt_member(p, it.row0 + q * p.tokens + tok, it.idx));
                 const int last = p.causal ? it.pos0 + q * p.tokens + tok : it.L - 1;    // the row's last key
                 const bool any = it.e[q] > it.t0;
                 const size_t row = static_cast<size_t>(it.row0 + q * p.tokens + tok) * p.Hq + it.h * p.G + head;

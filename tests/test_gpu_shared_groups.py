@@ -25,6 +25,19 @@ def test_prefixes_of_groups_that_leave_the_batch(starts, prefix):
     ref.check(out, *want)
 
 
+@pytest.mark.parametrize("starts,prefix", [([0, 200, 100, 240], [1024, 0, 512]), ([0, 200, 100, 240], [512, 0, 1024]),
+                                           ([30, 240, 0, 100, 90, 240], [1024, 0, 1008, 0, 560]),
+                                           ([0, 240, 0, 240, 0, 240, 0, 240], [1024, 0, 512, 0, 256, 0, 1024])])
+def test_groups_that_overlap(starts, prefix):
+    """Entries that fall back: what lies between belongs to two groups that fit, and is attended with one of them."""
+    c = Case([(1024, [1 + i % 40 for i in range(240)])], 16, 2, 64, F16)
+    want = c.want()
+    c.starts, c.prefix = c.dev(starts), c.dev(prefix)
+    out = c.call()
+    assert c.err.item() == pa.ERRBIT_BAD_QUERY
+    ref.check(out, *want)
+
+
 def test_many_small_groups():
     """Groups of one and two beside large ones, more of them than CTAs."""
     g = torch.Generator().manual_seed(8)
