@@ -149,7 +149,8 @@ size_t pa_decode_workspace_size(int num_seqs, int num_q_heads, int max_seq_len,
  *                     rounded up to a multiple of 32 to 128 tokens).
  * Precision: scores and sums accumulate in fp32.  The probabilities enter
  * P*V rounded to the MMA operand type: bf16 (8 significant bits) for bf16
- * caches, f16 (11 bits) for f16 caches and fp8 caches on 16-token chunks.  With
+ * caches, f16 (11 bits) for f16 caches and fp8 caches on 16-token chunks.  Outputs
+ * of f16 caches are finite, within +-65504, where the values are.  With
  * a 4-bit cache it is the product of a probability and its value row's step that
  * is rounded, to f16: 11 bits down to 2^-20 of the largest such product of the
  * query row, fewer below.  There a bf16 query is scaled by a power of two into

@@ -158,7 +158,7 @@ static pa_status carve_workspace(void* workspace, size_t bytes, int B, int prow,
 }
 
 pa_status launch_merge(const DecodeParams& p, pa_dtype out, bool split_heads, int sms, cudaStream_t stream,
-                       bool limit) {
+                       F16Out limit) {
     const void* rkern = p.scores ? reduce_kernel_weights(out, p.D, limit) : reduce_kernel(out, p.D, split_heads, limit);
     if (!rkern) return fail(PA_ERR_UNSUPPORTED, "decode: no reduce kernel for this output dtype");
     cudaLaunchAttribute attr[1];
@@ -475,7 +475,7 @@ static pa_status decode_impl(bool tc, void* out, const void* q, pa_dtype q_dtype
     if (ce != cudaSuccess) return fail_cuda("decode: main kernel launch", ce);
 
     if (tails) return launch_shared_merge(p, *tails, q_dtype, stream);
-    const pa_status mst = launch_merge(p, q_dtype, split_heads, dev.sms, stream);
+    const pa_status mst = launch_merge(p, q_dtype, split_heads, dev.sms, stream, kv_dtype == PA_F16 ? F16Out::FINITE : F16Out::ANY);
     return mst == PA_OK && weights ? launch_weights(p, *weights, stream) : mst;
 }
 

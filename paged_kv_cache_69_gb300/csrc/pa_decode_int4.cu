@@ -1091,7 +1091,7 @@ pa_status decode_int4(const Int4Call& c) {
     void* args[] = {&a};
     ce = cudaLaunchKernelExC(&cfg, kern, args);
     if (ce != cudaSuccess) return fail_cuda("decode: main kernel launch", ce);
-    const pa_status st = launch_merge(p, c.q_dtype, c.partition_tokens > 0, c.sms, c.stream, true);
+    const pa_status st = launch_merge(p, c.q_dtype, c.partition_tokens > 0, c.sms, c.stream, F16Out::LIMITED);
     return st == PA_OK && c.weights ? launch_weights(p, *c.weights, c.stream) : st;
 }
 

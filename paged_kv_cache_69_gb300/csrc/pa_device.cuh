@@ -46,9 +46,13 @@ template <> __device__ __forceinline__ LimitedHalf from_float<LimitedHalf>(float
 // A f16 output whose finite values stay within +-65504; infinities and NaN as they are.  For the
 // quotients of attention: weights enter the products rounded and the sum of weights as they
 // are, so that a quotient may pass the largest value by 2^-11 of it, and 65520 rounds to infinity.
+// (The limit lets infinities and NaN go; 2^-126 x brings them back and is nothing beside a finite x.)
+__device__ __forceinline__ float finite_f16(float x) {
+    return __fmaf_rn(x, 1.17549435e-38f, fmaxf(fminf(x, 65504.f), -65504.f));
+}
 struct FiniteHalf { __half h; };
 template <> __device__ __forceinline__ FiniteHalf from_float<FiniteHalf>(float x) {
-    return FiniteHalf{__float2half_rn(fabsf(x) > 65504.f && fabsf(x) < INFINITY ? copysignf(65504.f, x) : x)};
+    return FiniteHalf{__float2half_rn(finite_f16(x))};
 }
 template <> __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 

@@ -13,10 +13,12 @@ struct Workspace {
     float* part_acc;
     int max_slots;
 };
-// Launch of the log-sum-exp merge behind a main kernel's (limit: f16 outputs
-// stay within +-65504), and behind that, if
+// f16 outputs: as they come (fp8 pools, whose scales may lead past f16), finite ones within
+// +-65504 (f16 pools), all of them (4-bit pools).
+enum class F16Out { ANY, FINITE, LIMITED };
+// Launch of the log-sum-exp merge behind a main kernel's, and behind that, if
 // p.scores is set, of the kernel that adds the weights up.
-pa_status launch_merge(const DecodeParams& p, pa_dtype out, bool split_heads, int sms, cudaStream_t stream, bool limit = false);
+pa_status launch_merge(const DecodeParams& p, pa_dtype out, bool split_heads, int sms, cudaStream_t stream, F16Out limit);
 // What pa_decode_weights adds to a decode call: the pool that is added to, the
 // new tokens' counts (or null) and where the scores, (m, l) and first chunks go.
 struct WeightsOut {
@@ -51,7 +53,7 @@ const void* decode_kernel_mq(pa_dtype kv, pa_dtype q, int D);
 const void* decode_kernel_mq_um(pa_dtype kv, pa_dtype q, int D, int CT);
 // Log-sum-exp merge; split_heads: several warps per (sequence, head), for
 // partitioned sequences with many partials.
-const void* reduce_kernel(pa_dtype out, int D, bool split_heads, bool limit);
+const void* reduce_kernel(pa_dtype out, int D, bool split_heads, F16Out limit);
 // pa_decode with the weights added up.
 pa_status decode_with_weights(const WeightsOut& w, void* out, const void* q, pa_dtype q_dtype, const void* k_cache,
                               const void* v_cache, pa_dtype kv_dtype, const int32_t* block_tables, int MB,
@@ -66,5 +68,5 @@ const void* decode_kernel_tail(pa_dtype kv, int D);
 // The 16-token kernels that keep the scores (f32 caches: CUDA cores), and the
 // merge that keeps (m, l).
 const void* decode_kernel_weights(pa_dtype kv, pa_dtype q, int D);
-const void* reduce_kernel_weights(pa_dtype out, int D, bool limit);
+const void* reduce_kernel_weights(pa_dtype out, int D, F16Out limit);
 }  // namespace pa

@@ -132,11 +132,12 @@ const void* decode_kernel_weights(pa_dtype kv, pa_dtype q, int D) {
     return nullptr;
 }
 
-const void* reduce_kernel_weights(pa_dtype out, int D, bool limit) {
+const void* reduce_kernel_weights(pa_dtype out, int D, F16Out limit) {
 #define PA_RED(T) (D == 128 ? reinterpret_cast<const void*>(&pa_reduce_kernel<T, 128, 1, true>) \
                    : D == 64 ? reinterpret_cast<const void*>(&pa_reduce_kernel<T, 64, 1, true>) : nullptr)
     if (out == PA_F32) return PA_RED(float);
-    if (out == PA_F16) return limit ? PA_RED(LimitedHalf) : PA_RED(__half);
+    if (out == PA_F16)
+        return limit == F16Out::LIMITED ? PA_RED(LimitedHalf) : limit == F16Out::FINITE ? PA_RED(FiniteHalf) : PA_RED(__half);
     if (out == PA_BF16) return PA_RED(__nv_bfloat16);
 #undef PA_RED
     return nullptr;
