@@ -47,6 +47,11 @@ def test_many_small_groups():
     c.check(c.call())
 
 
+def test_more_groups_than_the_scheduler_keeps():
+    c = Case([(16 * (i % 3), [1 + i % 7]) for i in range(1300)] + [(1024, [1, 2, 3, 40])] + [(0, [2])] * 50 + [(2048, [5, 6])], 4, 2, 64, F16)
+    c.check(c.call())
+
+
 @pytest.mark.parametrize("groups", [0, 1, 16, 256, 1024])
 def test_workspace_grows_with_rows_and_not_with_groups(groups):
     """Beside what pa_decode takes: a partial per (sequence, head), and those of prefixes cut into ranges
