@@ -401,8 +401,8 @@ template <class KV, class QT, int D, bool TC, int CT, bool MQ = false, bool T8 =
 struct DecodeKernel {
     using KT = typename KV::T;
     using QE = typename QT::T;
-    // outputs of f16 pools on the tensor cores (fp8 values have a scale that may lead past f16; 64
-    // sequences of 100-8192 tokens 95.1 us, unlimited 94.7)
+    // outputs of f16 pools on the tensor cores (fp8 values have a scale that may lead past f16; a
+    // step of 64 sequences of 100-8192 tokens 95.1 us, unlimited 94.7)
     using OE = std::conditional_t<TC && KV::code == PA_F16 && QT::code == PA_F16, FiniteHalf, QE>;
     static constexpr bool FP8 = (KV::bytes == 1);             // e4m3 or e5m2
     // 32-token chunks are the native-e4m3 tensor-core variant (fp8 operands,

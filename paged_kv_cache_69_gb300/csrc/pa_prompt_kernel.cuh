@@ -46,12 +46,12 @@
 //     waits, rolled loops beside the hot ones (256 short prompts 627 -> 502 us);
 //   - rows written out by warps of their own, items found by 32 bands of levels in
 //     few instructions (502 -> 447; the first item is there after 9000 cycles, which
-//     were 34000).
+//     were 34000; 452-456 with f16 outputs limited and rows on any 16-byte boundary).
 // Short prompts stay bound by what an item costs beside its chunks, about 8000 cycles.
 // Not kept: the next item's scores ahead of the last products (no gain, more code);
-// one tile's rows in both tiles, the chunks in turn (no gain: such items are bound by
-// memory); skipping masked columns and key steps (the tests cost more); one lane per
-// block's copy.
+// one tile's rows in both tiles, the chunks in turn (no gain as built, though neither memory
+// nor the tensor cores bound such items: 47% and 24%); skipping masked columns and key steps
+// (the tests cost more); one lane per block's copy.
 #pragma once
 
 #include <cuda.h>

@@ -16,8 +16,10 @@
 //
 // Bound by HBM on prompts: 65536 tokens of 32/8 heads x 128, bf16, 248 us, 6640 GB/s
 // (326 without the hints that rows pass once, or with 256 threads; 2, 3, 6 and 8 rows
-// per lane: 287, 294, 305, 436).  On the 64 tokens of a decode step by the launch and
-// one chain of loads (position, then table), 5.6 us.
+// per lane: 287, 294, 305, 436).  Slots in any order: 277 us, into 8-bit pools 315, into 4-bit
+// ones 465 (a row's extremes and codes: 3.1 TB/s), with key_out 9 to 15 more.  On the 64 tokens of a
+// decode step by the launch and one chain of loads (position, then table), 4.2-6.2 us, whatever
+// the pool.
 #include <algorithm>
 #include <climits>
 #include <cstdio>
@@ -240,9 +242,12 @@ static cudaError_t launch_rope(RopeArgs a, cudaStream_t stream) {
         const uint32_t per = ROPE_THREADS / lpr;
         kern<<<(a.units + per - 1) / per, ROPE_THREADS, 0, stream>>>(a);
     };
-    // Four rows per lane on prompts; the few tokens of a decode step spread over more lanes
-    // (36 rows a token, one against four: 64 tokens 5.7 and 7.6 us, 256 5.7 and 7.3, 455 7.0 and
-    // 7.6, 1024 9.8 and 7.7, 16384 68 and 54).
+    // Four rows per lane on prompts; the few tokens of a decode step spread over more lanes.  The
+    // border lies where it does at 36 rows a token of 128 16-bit elements (one row against four: 64
+    // tokens 5.7 and 7.6 us, 256 5.7 and 7.3, 455 7.0 and 7.6, 1024 9.8 and 7.7, 16384 68 and 54).  At
+    // head_dim 64, where as many rows are half the threads, four are never the faster: 18 rows of
+    // bf16 and 2048, 5003 and 16384 tokens 6.2, 8.3 and 17.9 us with one, 6.3, 8.4 and 18.4 with four; 8
+    // rows of f32 and 2048 and 5003 tokens 6.2 and 6.7 against 6.3 and 8.4.
     if (static_cast<long long>(a.T) * rows >= 16384) go(rope_kernel<S, KV, 4>, 4);
     else go(rope_kernel<S, KV, 1>, 1);
     return cudaGetLastError();

@@ -11,10 +11,12 @@
 // 256 rows instead of once per sequence.
 //
 // Three launches, each the dependent of the one before.  128 sequences behind 32768 tokens,
-// 32/8 heads x 128, bf16, 20-2048 tokens of their own: 163 us (the bytes alone 99): the prefix 56
-// (bound by the tensor cores, 59% of their cycles), the tails 91 (HBM, 5.9 TB/s), the merge 13 (a
-// chain of dependent loads).  32 groups of four behind 2048, 28/4 heads: 67 = 38 + 22 + 11, each
-// too short to fill the GPU.  pa_decode on the first batch would read 17 GB, some 2500 us.
+// 32/8 heads x 128, bf16, 20-2048 tokens of their own: 165 us (the bytes alone 99): the prefix 59
+// (tensor cores 56% of their cycles, DRAM 30%: one span of 28 chunks per CTA, whose start and end
+// nothing covers), the tails 92 (HBM, 5.9 TB/s), the merge 13 (a chain of dependent loads).  32
+// groups of four behind 2048, 28/4 heads: 68 = 38 + 22 + 11; the prefix there has 28 of an item's 256
+// rows, so that the score, softmax and product of a chunk follow one another (tensor cores 24%,
+// DRAM 47%).  pa_decode on the first batch would read 17 GB, some 2500 us.
 #include <cuda.h>
 
 #include <algorithm>
